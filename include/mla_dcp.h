@@ -13,6 +13,15 @@
  *   mla_lse_combine_vup     the combine with the V-up fused into its epilogue
  *   mla_gather_kv           test hook: bit-exact gather of paged history
  *
+ * and what a serving loop does to the cache around it:
+ *
+ *   mla_dcp_decode_partial_fp4  the partials over a 4-bit (E2M1) latent cache
+ *   mla_kv_append           RMS norm, rotation and the write of new tokens into
+ *                           a 16-bit, E4M3 or E2M1 cache, queries rotated too
+ *   mla_kv_fork             sequences forked from others, pages shared
+ *   mla_kv_free             pages of sequences given back
+ *   mla_kv_copy_pages       pages copied within or between pools
+ *
  * Sources (web pages, cited by title and section):
  *   [PR]  vllm-ascend PR #16977 study page, "DCP decode: streams and V-up"
  *         (huashanblogllm.xyz study-dcp-decode-streams-vup)
@@ -71,8 +80,28 @@ enum {
   MLA_DEV_OK = 0,
   MLA_DEV_BAD_BLOCK_ID = 1,  /* a block_table entry outside [0, num_blocks)       */
   MLA_DEV_WAIT_TIMEOUT = 2,  /* a pipeline wait ran out of its spin budget         */
-  MLA_DEV_BAD_SEQ_LEN = 3    /* a seq_lens entry outside [0, max_blocks*block_size] */
+  MLA_DEV_BAD_SEQ_LEN = 3,   /* a seq_lens entry outside [0, max_blocks*block_size] */
+  MLA_DEV_BAD_SLOT = 4,      /* a slots entry outside [-1, num_blocks*block_size)  */
+  MLA_DEV_BAD_POSITION = 5,  /* a positions entry outside [0, max_pos)             */
+  MLA_DEV_BAD_ROW = 6,       /* a row id out of range, or a fork into a taken row  */
+  MLA_DEV_NO_FREE_PAGE = 7,  /* fewer free pages than a fork needs                 */
+  MLA_DEV_BAD_REF_COUNT = 8  /* a page given back that no row holds                */
 };
+
+/* How a cached row (512 latent + 64 RoPE values) is stored. */
+typedef enum {
+  MLA_KV_MODEL = 0,          /* 576 values of the 16-bit model dtype: 1152 bytes   */
+  MLA_KV_E4M3 = 1,           /* 576 E4M3 bytes, value = e * kv_scale               */
+  MLA_KV_E2M1 = 2            /* 4-bit codes and block scales, 324 bytes (below)    */
+} mla_kv_format;
+
+/* An E2M1 page of block_size tokens is block_size * 324 contiguous bytes: the
+ * codes of all its tokens, [block_size][288] (element 2i in the low half of
+ * byte i, element 2i + 1 in the high half), then their block scales,
+ * [block_size][36], one E4M3 byte s for every 16 elements.  A code is a sign
+ * bit, two exponent bits and one mantissa bit: the magnitudes 0, 0.5, 1, 1.5,
+ * 2, 3, 4, 6.  An element's value is code * s * kv_scale. */
+enum { MLA_E2M1_ROW_BYTES = 324 };
 
 enum {
   MLA_D_LATENT = 512, /* kv_lora_rank: width of c_KV  ([TP] "物理矛盾")          */
@@ -206,6 +235,35 @@ int mla_dcp_decode_partial_fp8(const void* q_abs, const void* q_pe, const void* 
                                float kv_scale, int in_dtype, int part_dtype, void* o_part,
                                float* lse_part, int32_t* err_flag, void* workspace,
                                uint64_t workspace_bytes, int head_slices, mla_stream_t stream);
+
+/*
+ * mla_dcp_decode_partial_fp4 -- mla_dcp_decode_partial_sliced over a 4-bit
+ * (E2M1) latent cache.  A library addition with no counterpart in the sources
+ * beyond their pointer to KV compression ([KM] sections 3.2 and 5.2).
+ *
+ * Differences from mla_dcp_decode_partial_sliced:
+ *   kv_cache   [num_blocks] E2M1 pages (MLA_KV_E2M1 above); the slots of a
+ *              last block past L_b may hold any bytes
+ *   kv_cur     [B, q_len, 576] values of in_dtype (not codes), or NULL
+ *   kv_scale   > 0 and finite (scale * kv_scale too); MLA_ERR_BAD_SHAPE otherwise
+ *   workspace  of mla_dcp_decode_partial_fp4_workspace_size bytes, or NULL
+ * Precision: every code * s is a value of either 16-bit type, so the tensor
+ * cores multiply the cache as it is stored by the query as it is given; the
+ * softmax weights are rounded to in_dtype before the PV product, as in the
+ * 16-bit call.
+ */
+int mla_dcp_decode_partial_fp4(const void* q_abs, const void* q_pe, const void* kv_cache,
+                               const int32_t* block_table, const int32_t* seq_lens,
+                               const void* kv_cur, int B, int q_len, int H, int num_blocks,
+                               int block_size, int max_blocks, int num_shards, float scale,
+                               float kv_scale, int in_dtype, int part_dtype, void* o_part,
+                               float* lse_part, int32_t* err_flag, void* workspace,
+                               uint64_t workspace_bytes, int head_slices, mla_stream_t stream);
+
+/* Bytes of workspace of mla_dcp_decode_partial_fp4, as
+ * mla_dcp_decode_partial_workspace_size (0 for invalid sizes). */
+uint64_t mla_dcp_decode_partial_fp4_workspace_size(int B, int q_len, int num_shards,
+                                                   int has_current);
 
 /*
  * mla_dcp_decode_partial_workspace_size -- bytes of workspace that
@@ -350,6 +408,118 @@ int mla_lse_combine_vup(const void* o_part, const float* lse_part, int num_parts
 int mla_gather_kv(const void* kv_cache, const int32_t* block_table, const int32_t* seq_lens,
                   int B, int num_blocks, int block_size, int max_blocks, int max_len,
                   void* dst, int32_t* err_flag, mla_stream_t stream);
+
+/*
+ * mla_kv_append -- new tokens' rows into the paged cache, in one launch.
+ * A library addition: the partial calls read rows that something has to write.
+ *
+ * For token t, with c = c_kv[t], k = k_pe[t]:
+ *   latent  y = c * w / sqrt(mean(c^2) + eps), w = norm_weight (NULL: y = c)
+ *   key     pair (a, b) of k -> (a cos - b sin, a sin + b cos), with
+ *           cos, sin = cos_sin[m][i], cos_sin[m][32 + i] for pair i, m = the
+ *           position of t on the pair's axis.  interleaved != 0: pair i is
+ *           elements (2i, 2i + 1); 0: elements (i, i + 32).
+ *   queries q_out[t, h] = q_pe[t, h] rotated the same way
+ * and the row (y, key) is stored in slot slots[t]: token slots[t] % block_size
+ * of block slots[t] / block_size.  slots[t] = -1 stores it nowhere (padding).
+ *
+ * Rounding.  16-bit and E4M3 values and E2M1 codes and scales are the nearest
+ * of the row value itself (ties to even; E4M3 saturates at 448, E2M1 at 6):
+ *   E4M3  e = rn(value / kv_scale)
+ *   E2M1  s = rn_E4M3(max|value| / (6 kv_scale)) over each 16 elements,
+ *         code = rn_E2M1(value / (s kv_scale)), 0 where s is 0; a zero keeps
+ *         its sign; a block that holds a NaN gets s = NaN
+ * (exactly so where kv_scale is a power of two; q_out is computed in fp32).
+ * Row sums and values are fp32: inputs beyond 1e18 overflow the mean.
+ *
+ *   c_kv      [T, 512] dtype, rows c_stride elements apart
+ *   k_pe      [T, 64] dtype, rows k_stride elements apart
+ *   q_pe      [T, H, 64] dtype, strides q_stride, q_head_stride; or NULL
+ *   q_out     [T, H, 64] dtype, strides qo_stride, qo_head_stride; may be q_pe
+ *             itself (same strides); NULL with q_pe
+ *             (strides >= 0, multiples of 8 elements)
+ *   positions [num_axes, T] int32 in [0, max_pos), num_axes 1 to 3
+ *   sections  HOST array [num_axes]: pairs of each axis in turn, sum 32
+ *   cos_sin   [max_pos, 64] float32: a row holds 32 cosines, then 32 sines
+ *   slots     [T] int32, distinct (of equal ones the slot's bytes are
+ *             unspecified); outside [-1, num_blocks * block_size): error,
+ *             not stored
+ *   kv_cache  [num_blocks, block_size, 576] dtype or E4M3 bytes, or E2M1 pages,
+ *             by kv_format; kv_scale (not read for MLA_KV_MODEL) in [1e-30, 1e30]
+ *   kv_out    [T, 576], or NULL: the same rows for the partial call's kv_cur:
+ *             dtype for MLA_KV_MODEL and, as the values that were stored, for
+ *             MLA_KV_E2M1; E4M3 bytes for MLA_KV_E4M3.  Every token has a row,
+ *             stored or not.
+ * Positions and slots out of range set MLA_DEV_BAD_POSITION / MLA_DEV_BAD_SLOT.
+ */
+int mla_kv_append(const void* c_kv, int64_t c_stride, const void* k_pe, int64_t k_stride,
+                  const void* norm_weight, float eps, const void* q_pe, int64_t q_stride,
+                  int64_t q_head_stride, const int32_t* positions, int num_axes,
+                  const int32_t* sections, const float* cos_sin, int max_pos, int interleaved,
+                  const int32_t* slots, int T, int H, int num_blocks, int block_size, int dtype,
+                  int kv_format, float kv_scale, void* kv_cache, void* q_out, int64_t qo_stride,
+                  int64_t qo_head_stride, void* kv_out, int32_t* err_flag, mla_stream_t stream);
+
+/*
+ * mla_kv_copy_pages -- page src_ids[i] of one pool to page dst_ids[i] of
+ * another (or the same), for i < n, in each of num_layers layers.  For moving
+ * sequences between pools, swapping them out and in, and packing a pool.
+ * A library addition.
+ *   src, dst   page p of layer l starts at l * layer_stride + p * page_bytes;
+ *              page_bytes and layer strides are multiples of 16, a page at
+ *              most 1 GiB
+ *   src_ids, dst_ids [n] int32 (device).  dst_ids are distinct, and within one
+ *              pool no page is both a source and a destination; the bytes of
+ *              pages that break this are unspecified.  An id out of range sets
+ *              MLA_DEV_BAD_BLOCK_ID and its page is skipped.
+ */
+int mla_kv_copy_pages(const void* src, uint64_t src_layer_stride, int src_blocks, void* dst,
+                      uint64_t dst_layer_stride, int dst_blocks, uint64_t page_bytes,
+                      int num_layers, const int32_t* src_ids, const int32_t* dst_ids, int n,
+                      int32_t* err_flag, mla_stream_t stream);
+
+/*
+ * mla_kv_free -- rows of a block table give their pages back.  A library
+ * addition.
+ *   For each r in rows: ref_counts of the first ceil(seq_lens[r] / block_size)
+ *   pages of row r go down by one, those entries become -1, seq_lens[r] 0.
+ *   block_table [num_rows, max_blocks] int32, seq_lens [num_rows] int32,
+ *   ref_counts [num_blocks] int32: rows that hold each page, 0 = free
+ *   rows [n] int32 (device); a row named twice is given back once
+ * MLA_DEV_BAD_ROW, MLA_DEV_BAD_SEQ_LEN (that row's pages stay counted),
+ * MLA_DEV_BAD_BLOCK_ID and MLA_DEV_BAD_REF_COUNT (a count that is 0 already;
+ * it stays 0) as they are met.
+ */
+int mla_kv_free(int32_t* block_table, int32_t* seq_lens, int32_t* ref_counts, const int32_t* rows,
+                int n, int num_rows, int num_blocks, int block_size, int max_blocks,
+                int32_t* err_flag, mla_stream_t stream);
+
+/*
+ * mla_kv_fork -- sequences forked from others (samples of one prompt, beams):
+ * the child's row shares the parent's full pages and gets a copy of its last,
+ * partly filled one, so that both can be appended to.  A library addition.
+ *
+ * For pair k, p = parents[k], c = children[k], L = seq_lens[p]:
+ *   block_table[c][j] = block_table[p][j], ref_counts of it + 1, j < L / block_size
+ *   if L % block_size: entry L / block_size is a free page, ref_counts 1, with
+ *   the bytes of p's page in every layer; the free pages taken are the lowest
+ *   ids whose ref_counts are 0, in the order of the pairs
+ *   the other entries of the row are -1;  seq_lens[c] = L
+ * A child's row holds nothing before (seq_lens[c] = 0; mla_kv_free), is forked
+ * into once and is no parent of the call, or MLA_DEV_BAD_ROW; too few free
+ * pages: MLA_DEV_NO_FREE_PAGE.  In both cases, and for a parent's length out of
+ * range (MLA_DEV_BAD_SEQ_LEN), nothing at all is changed.
+ *   kv_cache   pools of every layer, as in mla_kv_copy_pages
+ *   parents, children [n] int32 (device), 1 <= n <= num_rows <= 65536
+ *   workspace  of mla_kv_fork_workspace_size(n) bytes; calls that may overlap
+ *              in time need their own (and must not share a block table)
+ */
+uint64_t mla_kv_fork_workspace_size(int n);
+int mla_kv_fork(void* kv_cache, uint64_t layer_stride, uint64_t page_bytes, int num_layers,
+                int32_t* block_table, int32_t* seq_lens, int32_t* ref_counts,
+                const int32_t* parents, const int32_t* children, int n, int num_rows,
+                int num_blocks, int block_size, int max_blocks, void* workspace,
+                uint64_t workspace_bytes, int32_t* err_flag, mla_stream_t stream);
 
 /*
  * mla_debug_set_spin_limit -- test hook for the device error path: the

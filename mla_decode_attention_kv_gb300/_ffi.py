@@ -17,6 +17,7 @@ _LIB = None
 P = ctypes.c_void_p
 I = ctypes.c_int
 F = ctypes.c_float
+L = ctypes.c_int64
 
 # name -> (restype, argtypes), mirroring include/mla_dcp.h
 SIGNATURES = {
@@ -26,6 +27,17 @@ SIGNATURES = {
                                           P, ctypes.c_uint64, I, P]),
     "mla_dcp_decode_partial_fp8": (I, [P, P, P, P, P, P, I, I, I, I, I, I, I, F, F, I, I, P, P,
                                        P, P, ctypes.c_uint64, I, P]),
+    "mla_dcp_decode_partial_fp4": (I, [P, P, P, P, P, P, I, I, I, I, I, I, I, F, F, I, I, P, P,
+                                       P, P, ctypes.c_uint64, I, P]),
+    "mla_dcp_decode_partial_fp4_workspace_size": (ctypes.c_uint64, [I, I, I, I]),
+    "mla_kv_append": (I, [P, L, P, L, P, F, P, L, L, P, I, P, P, I, I, P, I, I, I, I, I, I, F, P,
+                          P, L, L, P, P, P]),
+    "mla_kv_copy_pages": (I, [P, ctypes.c_uint64, I, P, ctypes.c_uint64, I, ctypes.c_uint64, I, P,
+                              P, I, P, P]),
+    "mla_kv_free": (I, [P, P, P, P, I, I, I, I, I, P, P]),
+    "mla_kv_fork_workspace_size": (ctypes.c_uint64, [I]),
+    "mla_kv_fork": (I, [P, ctypes.c_uint64, ctypes.c_uint64, I, P, P, P, P, P, I, I, I, I, I, P,
+                        ctypes.c_uint64, P, P]),
     "mla_dcp_decode_partial_workspace_size": (ctypes.c_uint64, [I, I, I, I]),
     "mla_dcp_combine_exchanged": (I, [P, P, I, I, I, I, I, I, I, I, P, P, P]),
     "mla_dcp_decode_partial_noalloc": (I, [P, P, P, P, P, P, I, I, I, I, I, I, I, F, I, I, P, P, P,
@@ -43,6 +55,7 @@ SIGNATURES = {
 STATUS = {0: "MLA_OK", 1: "MLA_ERR_NULL_POINTER", 2: "MLA_ERR_BAD_SHAPE",
           3: "MLA_ERR_BAD_DTYPE", 4: "MLA_ERR_MISALIGNED", 5: "MLA_ERR_BAD_SHARDS",
           6: "MLA_ERR_BAD_BLOCK", 7: "MLA_ERR_CUDA"}
+KV_FORMAT = {"model": 0, "e4m3": 1, "e2m1": 2}
 DTYPE = {"bf16": 0, "fp16": 1, "fp32": 2}
 
 

@@ -16,6 +16,7 @@ import torch
 from . import _ffi
 
 D_LATENT, D_ROPE, D_QK, D_V = 512, 64, 576, 128
+E2M1_ROW = 324      # bytes of one token in an E2M1 page: 288 of codes, 36 of block scales
 DEFAULT_SCALE = 1.0 / math.sqrt(128 + D_ROPE)
 
 _TORCH_DT = {torch.bfloat16: "bf16", torch.float16: "fp16", torch.float32: "fp32"}
@@ -47,17 +48,19 @@ _WORKSPACES = {}
 
 
 def partial_workspace(device, B: int, q_len: int, num_shards: int, has_current: bool,
-                      stream=None):
-    """The default workspace of mla_dcp_decode_partial on `device` for calls on
-    `stream` (one per (device, stream), grown as needed), or None for sizes
+                      stream=None, fp4: bool = False):
+    """The default workspace of mla_dcp_decode_partial (fp4: of
+    mla_dcp_decode_partial_fp4) on `device` for calls on `stream` (one per (device, stream), grown as needed), or None for sizes
     the library rejects.  Calls on one stream run one after another, so they
     can share it; calls on different streams get different workspaces.  Two
     calls that may overlap in time on the same stream handle (graphs replayed
     concurrently, say) must pass workspaces of their own."""
     device = torch.device(device)
     with torch.cuda.device(device):
-        need = int(_ffi.lib().mla_dcp_decode_partial_workspace_size(
-            B, q_len, num_shards, 1 if has_current else 0))
+        lib = _ffi.lib()
+        size = (lib.mla_dcp_decode_partial_fp4_workspace_size if fp4
+                else lib.mla_dcp_decode_partial_workspace_size)
+        need = int(size(B, q_len, num_shards, 1 if has_current else 0))
         s = stream if stream is not None else torch.cuda.current_stream()
     if need == 0:
         return None      # invalid sizes: the call itself reports them
@@ -74,6 +77,11 @@ def is_fp8_cache(kv_cache) -> bool:
     return kv_cache.dtype in (torch.uint8, getattr(torch, "float8_e4m3fn", torch.uint8))
 
 
+def is_fp4_cache(kv_cache) -> bool:
+    """An E2M1 cache: uint8 pages of 324 bytes a token (288 of codes, 36 of scales)."""
+    return kv_cache.dtype == torch.uint8 and kv_cache.shape[-1] == E2M1_ROW
+
+
 def mla_dcp_decode_partial(q_abs, q_pe, kv_cache, block_table, seq_lens, num_shards: int, *,
                            kv_cur=None, scale: float = DEFAULT_SCALE, part_dtype=None,
                            o_part=None, lse_part=None, err_flag=None, stream=None,
@@ -84,7 +92,9 @@ def mla_dcp_decode_partial(q_abs, q_pe, kv_cache, block_table, seq_lens, num_sha
     block_table [B, max_blocks] int32, seq_lens [B] int32 (history lengths),
     kv_cur [B, q, 576] or None.  A kv_cache of E4M3 bytes (torch.uint8 or
     torch.float8_e4m3fn; kv_cur likewise) goes to mla_dcp_decode_partial_fp8
-    with kv_scale (default 1.0).  Returns o_part [B, q, P, H, 512] and
+    with kv_scale (default 1.0); one of E2M1 pages (torch.uint8 [num_blocks,
+    bs, 324]; kv_cur then in the dtype of q_abs) to mla_dcp_decode_partial_fp4.
+    Returns o_part [B, q, P, H, 512] and
     lse_part [B, q, P, H] (float32), P = num_shards + (kv_cur is not None);
     with head_slices = N > 1 they are [N, B*q, P, H/N, 512] and
     [N, B*q, P, H/N] (mla_dcp_decode_partial_sliced: block n is what rank n
@@ -114,8 +124,21 @@ def mla_dcp_decode_partial(q_abs, q_pe, kv_cache, block_table, seq_lens, num_sha
         if workspace != "default":
             raise ValueError("workspace must be 'default', a tensor or None")
         workspace = partial_workspace(q_abs.device, B, q_len, num_shards, kv_cur is not None,
-                                      stream)
+                                      stream, fp4=is_fp4_cache(kv_cache))
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    if is_fp4_cache(kv_cache):
+        if kv_cur is not None:
+            _need(kv_cur, "kv_cur")
+            if kv_cur.dtype != q_abs.dtype or kv_cur.numel() != B * q_len * D_QK:
+                raise TypeError("kv_cur over an E2M1 cache holds 576 values a token in q_abs's dtype")
+        st = _ffi.lib().mla_dcp_decode_partial_fp4(
+            _p(q_abs), _p(q_pe), _p(kv_cache), _p(block_table), _p(seq_lens), _p(kv_cur),
+            B, q_len, H, num_blocks, bs, block_table.shape[1], num_shards, float(scale),
+            float(1.0 if kv_scale is None else kv_scale), _code(q_abs.dtype),
+            _code(o_part.dtype), _p(o_part), _p(lse_part), _p(err_flag), _p(workspace), ws_bytes,
+            int(head_slices), _s(stream))
+        _ffi.check("mla_dcp_decode_partial_fp4", st)
+        return o_part, lse_part
     if is_fp8_cache(kv_cache):
         if kv_cur is not None and not is_fp8_cache(kv_cur):
             raise TypeError("kv_cur must be E4M3 bytes like kv_cache")
@@ -264,6 +287,216 @@ def decode_step(q_abs, q_pe, kv_cache, block_table, seq_lens, W_UV, num_shards: 
         part_dtype=part_dtype, o_part=o_part, lse_part=lse_part, err_flag=err_flag,
         stream=stream, workspace=workspace, kv_scale=kv_scale)
     return mla_lse_combine_vup(o_part, lse_part, W_UV, out=out, err_flag=err_flag, stream=stream)
+
+
+# ---------------------------------------------------------------- cache operators
+def _on(t: torch.Tensor, dev: torch.device, name: str, dtype=None):
+    """A CUDA tensor on `dev` (the call's stream and launches are on that device)."""
+    if not t.is_cuda or t.device != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on {dev}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+
+
+def _ids(t: torch.Tensor, dev: torch.device, name: str, shape):
+    _on(t, dev, name, torch.int32)
+    if not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {tuple(shape)}")
+
+
+def _err(t: Optional[torch.Tensor], dev: torch.device):
+    if t is not None:
+        _on(t, dev, "err_flag", torch.int32)
+        if t.numel() < 1:
+            raise ValueError("err_flag must hold one int32")
+
+
+def _kv_format(kv_cache: torch.Tensor, dtype: torch.dtype) -> str:
+    """Storage of a paged cache [num_blocks, bs, W] for a model dtype."""
+    if kv_cache.dim() != 3 or not kv_cache.is_contiguous():
+        raise ValueError("kv_cache must be a contiguous [num_blocks, block_size, W] tensor")
+    if is_fp4_cache(kv_cache):
+        return "e2m1"
+    if kv_cache.shape[2] == D_QK:
+        if kv_cache.dtype == dtype:
+            return "model"
+        if is_fp8_cache(kv_cache):
+            return "e4m3"
+    raise TypeError(f"no cache format has rows of {kv_cache.shape[2]} x {kv_cache.dtype} for {dtype}")
+
+
+def mla_kv_append(c_kv, k_pe, kv_cache, slots, positions, cos_sin, *, norm_weight=None,
+                  eps: float = 1e-6, q_pe=None, q_out=None, kv_out=None, kv_scale=None,
+                  interleaved: bool = True, sections=None, err_flag=None, stream=None):
+    """Norm, rotate and store new tokens, and rotate their queries, in one launch.
+
+    c_kv [T, 512] and k_pe [T, 64] (rows may be strided: views of one
+    projection), kv_cache [num_blocks, bs, 576] in their dtype or as E4M3
+    bytes, or [num_blocks, bs, 324] uint8 E2M1 pages (kv_scale, default 1.0,
+    for the last two), slots [T] int32 (-1: store nowhere), positions [T] or
+    [axes, T] int32, cos_sin [max_pos, 64] float32 (32 cosines, 32 sines),
+    norm_weight [512] or None (no norm), q_pe [T, H, 64] (strided) or None.
+    sections: pairs of each axis, sum 32 (default: all 32 on one axis).
+    q_out: rotated queries, a new [T, H, 64] tensor if None, may be q_pe.
+    kv_out: None, "new" or a [T, 576] tensor: the rows as the partial call's
+    kv_cur (16-bit; E4M3 bytes for an E4M3 cache; over an E2M1 cache the values
+    that were stored).  Returns (q_out, kv_out)."""
+    dev, dt = c_kv.device, c_kv.dtype
+    T = c_kv.shape[0]
+    for t, n, w in ((c_kv, "c_kv", D_LATENT), (k_pe, "k_pe", D_ROPE)):
+        _on(t, dev, n, dt)
+        if t.dim() != 2 or tuple(t.shape) != (T, w) or t.stride(1) != 1:
+            raise ValueError(f"{n} must be [T, {w}] with unit stride along its rows")
+    _on(kv_cache, dev, "kv_cache")
+    fmt = _kv_format(kv_cache, dt)
+    if fmt == "model" and kv_scale is not None:
+        raise TypeError("kv_scale applies to an E4M3 or E2M1 cache only")
+    positions = positions if positions.dim() == 2 else positions.view(1, -1)
+    axes = positions.shape[0]
+    _ids(slots, dev, "slots", (T,))
+    _ids(positions, dev, "positions", (axes, T))
+    sections = [D_ROPE // 2] if sections is None else [int(x) for x in sections]
+    if len(sections) != axes:
+        raise ValueError(f"{len(sections)} sections for {axes} position axes")
+    _on(cos_sin, dev, "cos_sin", torch.float32)
+    if cos_sin.dim() != 2 or cos_sin.shape[1] != D_ROPE or not cos_sin.is_contiguous():
+        raise ValueError("cos_sin must be a contiguous [max_pos, 64] tensor")
+    if norm_weight is not None:
+        _on(norm_weight, dev, "norm_weight", dt)
+        if tuple(norm_weight.shape) != (D_LATENT,) or not norm_weight.is_contiguous():
+            raise ValueError("norm_weight must be a contiguous [512] tensor")
+    _err(err_flag, dev)
+    H, qs, qos = 0, (0, 0), (0, 0)
+    if q_pe is not None:
+        H = q_pe.shape[1]
+        q_out = torch.empty((T, H, D_ROPE), dtype=dt, device=dev) if q_out is None else q_out
+        for t, n in ((q_pe, "q_pe"), (q_out, "q_out")):
+            _on(t, dev, n, dt)
+            if t.dim() != 3 or tuple(t.shape) != (T, H, D_ROPE) or t.stride(2) != 1:
+                raise ValueError(f"{n} must be [T, H, 64] with unit stride along its heads")
+        qs, qos = (q_pe.stride(0), q_pe.stride(1)), (q_out.stride(0), q_out.stride(1))
+    elif q_out is not None:
+        raise ValueError("q_out without q_pe")
+    kv_dt = kv_cache.dtype if fmt == "e4m3" else dt
+    if isinstance(kv_out, str):
+        if kv_out != "new":
+            raise ValueError("kv_out must be None, 'new' or a tensor")
+        kv_out = torch.empty((T, D_QK), dtype=kv_dt, device=dev)
+    if kv_out is not None:
+        _on(kv_out, dev, "kv_out", kv_dt)
+        if kv_out.numel() != T * D_QK or not kv_out.is_contiguous():
+            raise ValueError("kv_out must be a contiguous [T, 576] tensor")
+    if T == 0:
+        return q_out, kv_out
+    with torch.cuda.device(dev):
+        st = _ffi.lib().mla_kv_append(
+            _p(c_kv), c_kv.stride(0), _p(k_pe), k_pe.stride(0), _p(norm_weight), float(eps),
+            _p(q_pe), qs[0], qs[1], _p(positions), axes, (ctypes.c_int32 * axes)(*sections),
+            _p(cos_sin), cos_sin.shape[0], 1 if interleaved else 0, _p(slots), T, H,
+            kv_cache.shape[0], kv_cache.shape[1], _code(dt), _ffi.KV_FORMAT[fmt],
+            float(1.0 if kv_scale is None else kv_scale), _p(kv_cache), _p(q_out), qos[0], qos[1],
+            _p(kv_out), _p(err_flag), _s(stream))
+    _ffi.check("mla_kv_append", st)
+    return q_out, kv_out
+
+
+def _pools(kv_cache: torch.Tensor, name: str):
+    """(layers, layer stride in bytes, pages, bytes of a page, block size) of a pool
+    [num_blocks, bs, W] or the layers' pools [layers, num_blocks, bs, W]."""
+    if not kv_cache.is_cuda or kv_cache.dim() not in (3, 4):
+        raise ValueError(f"{name} must be a CUDA tensor [(layers,) num_blocks, block_size, W]")
+    pool = kv_cache if kv_cache.dim() == 3 else kv_cache[0]
+    if not pool.is_contiguous():
+        raise ValueError(f"the pages of {name} must be contiguous")
+    size = kv_cache.element_size()
+    layers = 1 if kv_cache.dim() == 3 else kv_cache.shape[0]
+    stride = 0 if kv_cache.dim() == 3 else kv_cache.stride(0) * size
+    if layers > 1 and stride < pool.numel() * size:
+        raise ValueError(f"the layers of {name} overlap")
+    return layers, stride, pool.shape[0], pool.shape[1] * pool.shape[2] * size, pool.shape[1]
+
+
+def mla_kv_copy_pages(src, dst, src_ids, dst_ids, *, err_flag=None, stream=None):
+    """Pages src_ids [n] of the pool(s) `src` to pages dst_ids [n] of `dst`, in every layer.
+    Pools are [num_blocks, bs, W] or [layers, num_blocks, bs, W] of one format.  dst_ids are
+    distinct, and within one pool no page is both source and destination.  Returns dst."""
+    sl, ss, sn, sp, _ = _pools(src, "src")
+    dl, ds, dn, dp, _ = _pools(dst, "dst")
+    if sl != dl or sp != dp or src.dtype != dst.dtype:
+        raise ValueError("src and dst must hold pages of one size and type in as many layers")
+    n = src_ids.numel()
+    _on(dst, src.device, "dst")
+    _ids(src_ids, src.device, "src_ids", (n,))
+    _ids(dst_ids, src.device, "dst_ids", (n,))
+    _err(err_flag, src.device)
+    if n == 0:
+        return dst
+    with torch.cuda.device(src.device):
+        st = _ffi.lib().mla_kv_copy_pages(_p(src), ss, sn, _p(dst), ds, dn, sp, sl, _p(src_ids),
+                                          _p(dst_ids), n, _p(err_flag), _s(stream))
+    _ffi.check("mla_kv_copy_pages", st)
+    return dst
+
+
+def _page_state(block_table, seq_lens, ref_counts):
+    if not block_table.is_cuda or block_table.dim() != 2:
+        raise ValueError("block_table must be a CUDA tensor [rows, max_blocks]")
+    dev, rows = block_table.device, block_table.shape[0]
+    _ids(block_table, dev, "block_table", block_table.shape)
+    _ids(seq_lens, dev, "seq_lens", (rows,))
+    _ids(ref_counts, dev, "ref_counts", (ref_counts.numel(),))
+    return dev, rows
+
+
+def mla_kv_free(block_table, seq_lens, ref_counts, rows, *, block_size: int, err_flag=None,
+                stream=None):
+    """Give the pages of the rows [n] (int32) of block_table [R, max_blocks] back: their
+    ref_counts [num_blocks] go down, their entries become -1 and their seq_lens 0."""
+    dev, R = _page_state(block_table, seq_lens, ref_counts)
+    n = rows.numel()
+    _ids(rows, dev, "rows", (n,))
+    _err(err_flag, dev)
+    if n == 0:
+        return
+    with torch.cuda.device(dev):
+        st = _ffi.lib().mla_kv_free(_p(block_table), _p(seq_lens), _p(ref_counts), _p(rows), n, R,
+                                    ref_counts.numel(), int(block_size), block_table.shape[1],
+                                    _p(err_flag), _s(stream))
+    _ffi.check("mla_kv_free", st)
+
+
+def mla_kv_fork(kv_cache, block_table, seq_lens, ref_counts, parents, children, *,
+                workspace=None, err_flag=None, stream=None):
+    """Fork the sequences of rows parents [n] into the empty rows children [n]: full pages
+    are shared (ref_counts), the last, partly filled page is copied in every layer of
+    kv_cache ([num_blocks, bs, W] or [layers, num_blocks, bs, W]) to the lowest free page.
+    workspace: a tensor of mla_kv_fork_workspace_size(n) bytes for this call alone (default:
+    a new one; give one to keep when capturing into a graph)."""
+    dev, R = _page_state(block_table, seq_lens, ref_counts)
+    layers, stride, pages, page_bytes, bs = _pools(kv_cache, "kv_cache")
+    _on(kv_cache, dev, "kv_cache")
+    if pages != ref_counts.numel():
+        raise ValueError(f"ref_counts of {ref_counts.numel()} pages for a pool of {pages}")
+    n = parents.numel()
+    _ids(parents, dev, "parents", (n,))
+    _ids(children, dev, "children", (n,))
+    _err(err_flag, dev)
+    if n == 0:
+        return
+    with torch.cuda.device(dev):
+        s = stream if stream is not None else torch.cuda.current_stream()
+        need = int(_ffi.lib().mla_kv_fork_workspace_size(n))
+        if workspace is None:
+            with torch.cuda.stream(s):     # freed in the order of the stream that uses it
+                workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        else:
+            _on(workspace, dev, "workspace")
+            _need(workspace, "workspace")
+        st = _ffi.lib().mla_kv_fork(
+            _p(kv_cache), stride, page_bytes, layers, _p(block_table), _p(seq_lens),
+            _p(ref_counts), _p(parents), _p(children), n, R, pages, bs, block_table.shape[1],
+            _p(workspace), workspace.numel() * workspace.element_size(), _p(err_flag), _s(s))
+    _ffi.check("mla_kv_fork", st)
 
 
 def torch_dtype(name: str) -> torch.dtype:

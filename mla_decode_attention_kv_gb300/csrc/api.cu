@@ -8,7 +8,9 @@
 #include <atomic>
 #include <mutex>
 #include "../../include/mla_dcp.h"
+#include "cache_kernels.cuh"
 #include "kernels.cuh"
+#include "partial_fp4.cuh"
 #include "ptx.cuh"
 
 namespace {
@@ -82,6 +84,17 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 bool is_half_dtype(int d) { return d == MLA_BF16 || d == MLA_FP16; }
 bool is_part_dtype(int d) { return d == MLA_BF16 || d == MLA_FP16 || d == MLA_FP32; }
 
+bool is_block_size(int bs) { return bs == 16 || bs == 32 || bs == 64 || bs == 128 || bs == 256; }
+
+// Pages of whole 16-byte pieces, at most 1 GiB each, and fewer than 2^31 copy
+// blocks (each at least 16 KiB of a page) in a launch.
+bool page_layout_ok(uint64_t page_bytes, int num_layers, int n) {
+  if (page_bytes < 16 || page_bytes % 16 != 0 || page_bytes > (uint64_t{1} << 30)) return false;
+  if (num_layers < 1 || num_layers > 65535) return false;
+  const uint64_t per_page = (page_bytes >> 14) + 1;
+  return per_page * num_layers + 1 <= (uint64_t{INT32_MAX}) / static_cast<uint64_t>(n);
+}
+
 int launched(int rc) {
   if (rc != 0) return MLA_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
@@ -130,6 +143,11 @@ const char* mla_device_error_string(int code) {
     case MLA_DEV_BAD_BLOCK_ID: return "block_table entry outside [0, num_blocks)";
     case MLA_DEV_WAIT_TIMEOUT: return "a pipeline wait exceeded its spin budget";
     case MLA_DEV_BAD_SEQ_LEN: return "seq_lens entry outside [0, max_blocks * block_size]";
+    case MLA_DEV_BAD_SLOT: return "slots entry outside [-1, num_blocks * block_size)";
+    case MLA_DEV_BAD_POSITION: return "positions entry outside [0, max_pos)";
+    case MLA_DEV_BAD_ROW: return "a row id out of range, or a fork into a row that is taken";
+    case MLA_DEV_NO_FREE_PAGE: return "fewer free pages than the fork needs";
+    case MLA_DEV_BAD_REF_COUNT: return "a page given back that no row holds";
     default: return "unknown device error";
   }
 }
@@ -304,6 +322,46 @@ int mla_dcp_decode_partial(const void* q_abs, const void* q_pe, const void* kv_c
                                        workspace, workspace_bytes, 1, stream);
 }
 
+int mla_dcp_decode_partial_fp4(const void* q_abs, const void* q_pe, const void* kv_cache,
+                               const int32_t* block_table, const int32_t* seq_lens,
+                               const void* kv_cur, int B, int q_len, int H, int num_blocks,
+                               int block_size, int max_blocks, int num_shards, float scale,
+                               float kv_scale, int in_dtype, int part_dtype, void* o_part,
+                               float* lse_part, int32_t* err_flag, void* workspace,
+                               uint64_t workspace_bytes, int head_slices, mla_stream_t stream) {
+  const int rc = check_partial_args(q_abs, q_pe, kv_cache, block_table, seq_lens, kv_cur, B,
+                                    q_len, H, num_blocks, block_size, max_blocks, num_shards,
+                                    scale, in_dtype, part_dtype, o_part, lse_part);
+  if (rc != MLA_OK) return rc;
+  if (!(kv_scale > 0.f) || !std::isfinite(kv_scale) || !std::isfinite(scale * kv_scale * 1.4426950408889634f))
+    return MLA_ERR_BAD_SHAPE;
+  if (head_slices < 1 || H % head_slices != 0) return MLA_ERR_BAD_SHAPE;
+  if (workspace && reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return MLA_ERR_MISALIGNED;
+  mla::Fp4Params fp;
+  fp.q_abs = q_abs;
+  fp.q_pe = q_pe;
+  fp.kv_cache = static_cast<const uint8_t*>(kv_cache);
+  fp.block_table = block_table;
+  fp.seq_lens = seq_lens;
+  fp.kv_cur = kv_cur;
+  fp.o_part = o_part;
+  fp.lse_part = lse_part;
+  fp.err = err_flag;
+  fp.B = B;
+  fp.q_len = q_len;
+  fp.H = H;
+  fp.num_blocks = num_blocks;
+  fp.bs = block_size;
+  fp.max_blocks = max_blocks;
+  fp.S = num_shards;
+  fp.P = num_shards + (kv_cur ? 1 : 0);
+  fp.head_slices = head_slices;
+  fp.scale_log2 = scale * 1.4426950408889634f;
+  fp.kv_scale = kv_scale;
+  fp.part_dtype = part_dtype;
+  return launched(mla::launch_partial_fp4(fp, in_dtype == MLA_BF16, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 uint64_t mla_dcp_decode_partial_workspace_size(int B, int q_len, int num_shards, int has_current) {
   if (B < 1 || q_len < 1 || q_len > MLA_MAX_Q_LEN || num_shards < 1 || num_shards > MLA_MAX_SHARDS) return 0;
   const int64_t units = static_cast<int64_t>(B) * q_len * (num_shards + (has_current ? 1 : 0));
@@ -311,6 +369,13 @@ uint64_t mla_dcp_decode_partial_workspace_size(int B, int q_len, int num_shards,
   const int clusters = mla::partial_max_clusters();
   if (clusters < 1) return 0;
   return mla::partial_workspace_bytes(clusters);
+}
+
+uint64_t mla_dcp_decode_partial_fp4_workspace_size(int B, int q_len, int num_shards, int has_current) {
+  if (B < 1 || q_len < 1 || q_len > MLA_MAX_Q_LEN || num_shards < 1 || num_shards > MLA_MAX_SHARDS) return 0;
+  const int64_t units = static_cast<int64_t>(B) * q_len * (num_shards + (has_current ? 1 : 0));
+  if (units > INT32_MAX) return 0;
+  return 256;
 }
 
 // ------------------------------------------------------------------ no-alloc variant
@@ -496,6 +561,159 @@ int mla_gather_kv(const void* kv_cache, const int32_t* block_table, const int32_
   return launched(mla::launch_gather(kv_cache, block_table, seq_lens, B, num_blocks, block_size,
                                      max_blocks, max_len, dst, err_flag,
                                      reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// ------------------------------------------------------------------ cache operators
+int mla_kv_append(const void* c_kv, int64_t c_stride, const void* k_pe, int64_t k_stride,
+                  const void* norm_weight, float eps, const void* q_pe, int64_t q_stride,
+                  int64_t q_head_stride, const int32_t* positions, int num_axes,
+                  const int32_t* sections, const float* cos_sin, int max_pos, int interleaved,
+                  const int32_t* slots, int T, int H, int num_blocks, int block_size, int dtype,
+                  int kv_format, float kv_scale, void* kv_cache, void* q_out, int64_t qo_stride,
+                  int64_t qo_head_stride, void* kv_out, int32_t* err_flag, mla_stream_t stream) {
+  if (!c_kv || !k_pe || !positions || !sections || !cos_sin || !slots || !kv_cache)
+    return MLA_ERR_NULL_POINTER;
+  if ((q_pe == nullptr) != (q_out == nullptr)) return MLA_ERR_NULL_POINTER;
+  if (!is_half_dtype(dtype) || kv_format < MLA_KV_MODEL || kv_format > MLA_KV_E2M1)
+    return MLA_ERR_BAD_DTYPE;
+  if (T < 1 || max_pos < 1 || num_blocks < 1 || num_axes < 1 || num_axes > 3 ||
+      (q_pe && (H < 1 || H > MLA_MAX_HEADS)))
+    return MLA_ERR_BAD_SHAPE;
+  if (norm_weight && (!(eps >= 0.f) || !std::isfinite(eps))) return MLA_ERR_BAD_SHAPE;
+  if (!is_block_size(block_size)) return MLA_ERR_BAD_BLOCK;
+  if (static_cast<int64_t>(num_blocks) * block_size > INT32_MAX) return MLA_ERR_BAD_SHAPE;
+  if (kv_format != MLA_KV_MODEL &&
+      (!(kv_scale >= 1e-30f) || !(kv_scale <= 1e30f)))   // 448 * 6 * kv_scale stays finite
+    return MLA_ERR_BAD_SHAPE;
+  int sum = 0;
+  for (int a = 0; a < num_axes; ++a) {
+    if (sections[a] < 0) return MLA_ERR_BAD_SHAPE;
+    sum += sections[a];
+  }
+  if (sum != MLA_D_ROPE / 2) return MLA_ERR_BAD_SHAPE;
+  // rows are read in 16-byte pieces
+  if (c_stride < 0 || c_stride % 8 != 0 || k_stride < 0 || k_stride % 8 != 0) return MLA_ERR_BAD_SHAPE;
+  if (q_pe && (q_stride < 0 || q_stride % 8 != 0 || q_head_stride < 0 || q_head_stride % 8 != 0 ||
+               qo_stride < 0 || qo_stride % 8 != 0 || qo_head_stride < 0 || qo_head_stride % 8 != 0))
+    return MLA_ERR_BAD_SHAPE;
+  if (!aligned16(c_kv) || !aligned16(k_pe) || !aligned16(norm_weight) || !aligned16(q_pe) ||
+      !aligned16(q_out) || !aligned16(cos_sin) || !aligned16(kv_cache) || !aligned16(kv_out))
+    return MLA_ERR_MISALIGNED;
+  mla::AppendParams ap;
+  ap.c_kv = c_kv;
+  ap.k_pe = k_pe;
+  ap.q_pe = q_pe;
+  ap.weight = norm_weight;
+  ap.cos_sin = cos_sin;
+  ap.positions = positions;
+  ap.slots = slots;
+  ap.cache = kv_cache;
+  ap.q_out = q_out;
+  ap.kv_out = kv_out;
+  ap.err = err_flag;
+  ap.c_stride = c_stride;
+  ap.k_stride = k_stride;
+  ap.q_stride = q_stride;
+  ap.q_head_stride = q_head_stride;
+  ap.qo_stride = qo_stride;
+  ap.qo_head_stride = qo_head_stride;
+  ap.T = T;
+  ap.H = H;
+  ap.max_pos = max_pos;
+  ap.bs = block_size;
+  ap.num_slots = num_blocks * block_size;
+  ap.sec1 = num_axes > 1 ? sections[0] : MLA_D_ROPE / 2;
+  ap.sec2 = num_axes > 2 ? sections[0] + sections[1] : MLA_D_ROPE / 2;
+  ap.interleaved = interleaved ? 1 : 0;
+  ap.eps = eps;
+  ap.kv_scale = kv_scale;
+  ap.kv6 = 6.f * kv_scale;
+  ap.row_blocks = 0;
+  return launched(mla::launch_append(ap, kv_format, dtype == MLA_BF16, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int mla_kv_copy_pages(const void* src, uint64_t src_layer_stride, int src_blocks, void* dst,
+                      uint64_t dst_layer_stride, int dst_blocks, uint64_t page_bytes,
+                      int num_layers, const int32_t* src_ids, const int32_t* dst_ids, int n,
+                      int32_t* err_flag, mla_stream_t stream) {
+  if (!src || !dst || !src_ids || !dst_ids) return MLA_ERR_NULL_POINTER;
+  if (n < 1 || src_blocks < 1 || dst_blocks < 1 || !page_layout_ok(page_bytes, num_layers, n) ||
+      src_layer_stride % 16 != 0 || dst_layer_stride % 16 != 0)
+    return MLA_ERR_BAD_SHAPE;
+  if (!aligned16(src) || !aligned16(dst)) return MLA_ERR_MISALIGNED;
+  mla::CopyParams cp;
+  cp.src = static_cast<const char*>(src);
+  cp.dst = static_cast<char*>(dst);
+  cp.src_layer = src_layer_stride;
+  cp.dst_layer = dst_layer_stride;
+  cp.page_bytes = page_bytes;
+  cp.src_ids = src_ids;
+  cp.dst_ids = dst_ids;
+  cp.n = n;
+  cp.layers = num_layers;
+  cp.src_blocks = src_blocks;
+  cp.dst_blocks = dst_blocks;
+  cp.chunks = 0;
+  cp.err = err_flag;
+  return launched(mla::launch_copy_pages(cp, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int mla_kv_free(int32_t* block_table, int32_t* seq_lens, int32_t* ref_counts, const int32_t* rows,
+                int n, int num_rows, int num_blocks, int block_size, int max_blocks,
+                int32_t* err_flag, mla_stream_t stream) {
+  if (!block_table || !seq_lens || !ref_counts || !rows) return MLA_ERR_NULL_POINTER;
+  if (n < 1 || num_rows < 1 || num_blocks < 1 || max_blocks < 1) return MLA_ERR_BAD_SHAPE;
+  if (!is_block_size(block_size)) return MLA_ERR_BAD_BLOCK;
+  mla::FreeParams fp;
+  fp.table = block_table;
+  fp.lens = seq_lens;
+  fp.refs = ref_counts;
+  fp.rows = rows;
+  fp.n = n;
+  fp.num_rows = num_rows;
+  fp.num_blocks = num_blocks;
+  fp.bs = block_size;
+  fp.max_blocks = max_blocks;
+  fp.err = err_flag;
+  return launched(mla::launch_free(fp, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+uint64_t mla_kv_fork_workspace_size(int n) {
+  return n < 1 || n > mla::kMaxForkRows ? 0 : 16 + static_cast<uint64_t>(n) * 8;
+}
+
+int mla_kv_fork(void* kv_cache, uint64_t layer_stride, uint64_t page_bytes, int num_layers,
+                int32_t* block_table, int32_t* seq_lens, int32_t* ref_counts,
+                const int32_t* parents, const int32_t* children, int n, int num_rows,
+                int num_blocks, int block_size, int max_blocks, void* workspace,
+                uint64_t workspace_bytes, int32_t* err_flag, mla_stream_t stream) {
+  if (!kv_cache || !block_table || !seq_lens || !ref_counts || !parents || !children || !workspace)
+    return MLA_ERR_NULL_POINTER;
+  if (n < 1 || num_rows < 1 || num_rows > mla::kMaxForkRows || n > num_rows || num_blocks < 1 ||
+      max_blocks < 1 || !page_layout_ok(page_bytes, num_layers, n) || layer_stride % 16 != 0 ||
+      workspace_bytes < mla_kv_fork_workspace_size(n))
+    return MLA_ERR_BAD_SHAPE;
+  if (!is_block_size(block_size)) return MLA_ERR_BAD_BLOCK;
+  if (!aligned16(kv_cache) || !aligned16(ref_counts) || !aligned16(workspace)) return MLA_ERR_MISALIGNED;
+  mla::ForkParams fp;
+  fp.cache = static_cast<char*>(kv_cache);
+  fp.layer = layer_stride;
+  fp.page_bytes = page_bytes;
+  fp.table = block_table;
+  fp.lens = seq_lens;
+  fp.refs = ref_counts;
+  fp.parents = parents;
+  fp.children = children;
+  fp.n = n;
+  fp.layers = num_layers;
+  fp.rows = num_rows;
+  fp.num_blocks = num_blocks;
+  fp.bs = block_size;
+  fp.max_blocks = max_blocks;
+  fp.chunks = 0;
+  fp.ws = static_cast<int32_t*>(workspace);
+  fp.err = err_flag;
+  return launched(mla::launch_fork(fp, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,446 @@
+// mla_kv_append: what a step's projections leave of a token, made into a
+// cached row and written to its slot, in one launch:
+//   latent   y = c * rsqrt(mean c^2 + eps) * w           (512 values)
+//   key      the 64 RoPE values, rotated pair by pair by their positions
+//   queries  every head's 64 RoPE values, rotated the same way
+// The row goes to the paged cache as 16-bit values, as E4M3 bytes, or as E2M1
+// codes with an E4M3 scale for every 16 values.
+//
+// Mathematics.  A pair (a, b) at position m turns into (a cos - b sin, a sin +
+// b cos) with cos and sin read from a table row of that position; with several
+// axes (time, height, width) a pair reads the row of its section's position.
+//
+// What is stored in 8 or 4 bits is the nearest code of the value itself.  A
+// value computed in one fp32 step is off by 2^-24 or so and lands, once in a
+// few million values, on the wrong side of a border between two 4-bit codes
+// that lie a third of their size apart; the cache would then depend on the
+// order of a sum.  So row values are carried as unevaluated sums hi + lo of
+// two fp32 numbers (sums and products with their exact errors, Dekker and
+// Knuth), about 2^-46 off, and each rounding to fewer bits sees hi with lo
+// folded into its last bit (round to odd), which rounds the same way as hi +
+// lo itself.  It is 15-odd fp32 operations a value, below the memory's time.
+//
+// What bounds it: bytes (the queries' 256 bytes per head and token, read and
+// written once), and the launch for few tokens.  One warp makes a token's row:
+// lane l owns latents 16 l .. 16 l + 15, which are one block of the E2M1 form,
+// so a block's maximum and its 8 bytes of codes stay in a lane; the key's pair
+// l belongs to lane l.  The queries go to blocks of their own, eight lanes a
+// head, 16 bytes a lane.
+#include <cuda_fp4.h>
+#include <cuda_fp8.h>
+#include "cache_kernels.cuh"
+#include "common.cuh"
+
+namespace mla {
+
+namespace {
+
+// hi + lo, |lo| <= ulp(hi) / 2
+struct F2 {
+  float hi, lo;
+};
+
+__device__ __forceinline__ F2 two_sum(float a, float b) {
+  const float s = a + b;
+  const float bb = s - a;
+  return {s, (a - (s - bb)) + (b - bb)};
+}
+
+__device__ __forceinline__ F2 renorm(float hi, float lo) {
+  const float s = hi + lo;
+  return {s, lo - (s - hi)};
+}
+
+// hi + lo rounded to odd: the fp32 neighbour of the value whose last bit is 1
+// (hi itself where lo is 0).  Rounding that to fewer bits gives the nearest
+// code of hi + lo.  NaN and infinities pass.
+__device__ __forceinline__ float to_odd(float hi, float lo) {
+  const uint32_t u = __float_as_uint(hi);
+  const bool neg = (u >> 31) != 0;
+  uint32_t v = u;
+  if ((lo > 0.f && !neg) || (lo < 0.f && neg)) v = u | 1u;
+  if ((lo > 0.f && neg) || (lo < 0.f && !neg)) v = (u - 1u) | 1u;
+  return __uint_as_float(v);
+}
+
+// a / d rounded to odd, a >= 0 and d > 0: the correctly rounded quotient and
+// the sign of its exact remainder say on which side the quotient lies.
+__device__ __forceinline__ float div_odd(float a, float d) {
+  const float q = __fdiv_rn(a, d);
+  const float r = fmaf(-q, d, a);
+  uint32_t u = __float_as_uint(q);
+  if (r > 0.f) u |= 1u;
+  if (r < 0.f) u = (u - 1u) | 1u;
+  return __uint_as_float(u);
+}
+
+// (a, b) turned by (cos, sin): the exact products' sums, as hi + lo
+__device__ __forceinline__ F2 mul_diff(float a, float c, float b, float s) {   // a c - b s
+  const float p1 = a * c, e1 = fmaf(a, c, -p1);
+  const float p2 = b * s, e2 = fmaf(b, s, -p2);
+  const F2 d = two_sum(p1, -p2);
+  const float lo = d.lo + (e1 - e2);
+  return lo == 0.f ? F2{d.hi, 0.f} : renorm(d.hi, lo);   // (a zero keeps the sum's sign)
+}
+
+template <bool BF16>
+__device__ __forceinline__ float2 unpack(uint32_t w) {
+  return unpack2(w, BF16 ? kBF16 : kFP16);
+}
+
+template <bool BF16>
+__device__ __forceinline__ float load1(const void* p, int64_t i) {
+  const uint16_t u = static_cast<const uint16_t*>(p)[i];
+  return unpack<BF16>(u).x;
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint16_t pack1(float a) {
+  return static_cast<uint16_t>(pack2<BF16>(a, 0.f) & 0xFFFFu);
+}
+
+__device__ __forceinline__ uint32_t to_e4m3(float x) {
+  return __nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3);
+}
+
+__device__ __forceinline__ float from_e4m3(uint32_t b) {
+  const __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(b), __NV_E4M3);
+  return __half2float(*reinterpret_cast<const __half*>(&h));
+}
+
+// E4M3 byte of a block's scale, max / (6 kv_scale); NaN where a value is NaN
+__device__ __forceinline__ uint32_t block_scale(float amax, bool nan, float kv6) {
+  return nan ? 0x7Fu : to_e4m3(div_odd(amax, kv6));
+}
+
+// E2M1 codes of two values in a byte (the first in the low half); d = scale *
+// kv_scale of their block.  Values past 6 d saturate, the sign of a zero stays.
+__device__ __forceinline__ uint32_t e2m1_pair(float a, float b, float d) {
+  float x = 0.f, y = 0.f;
+  if (d > 0.f) {
+    x = div_odd(fabsf(a), d);
+    y = div_odd(fabsf(b), d);
+  }
+  const uint32_t m = __nv_cvt_float2_to_fp4x2(make_float2(x, y), __NV_E2M1, cudaRoundNearest);
+  return (m & 0x77u) | ((__float_as_uint(a) >> 28) & 8u) | ((__float_as_uint(b) >> 24) & 0x80u);
+}
+
+// Value of one E2M1 code (the format's eight magnitudes).
+__device__ __forceinline__ float e2m1_value(uint32_t c) {
+  const uint32_t e = (c >> 1) & 3u, m = c & 1u;
+  const float mag = e == 0 ? 0.5f * m : __uint_as_float((126u + e) << 23) * (1.f + 0.5f * m);
+  return (c & 8u) ? -mag : mag;
+}
+
+// Position of RoPE pair i of token t: that of the axis its section belongs to.
+// Out-of-range positions are recorded and read as 0.
+__device__ __forceinline__ int pair_position(const AppendParams& ap, int t, int i) {
+  const int axis = (i >= ap.sec1) + (i >= ap.sec2);
+  int pos = __ldg(ap.positions + static_cast<int64_t>(axis) * ap.T + t);
+  if (pos < 0 || pos >= ap.max_pos) {
+    set_error(ap.err, kDevBadPosition);
+    pos = 0;
+  }
+  return pos;
+}
+
+// One token's row, by one warp.
+template <bool BF16, int KIND>
+__device__ void append_row(const AppendParams& ap, int t, int lane) {
+  // ---- latent: 16 values a lane
+  uint32_t cw[8];
+  {
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(ap.c_kv) +
+                                                      t * ap.c_stride + 16 * lane);
+    const uint4 a = src[0], b = src[1];
+    cw[0] = a.x; cw[1] = a.y; cw[2] = a.z; cw[3] = a.w;
+    cw[4] = b.x; cw[5] = b.y; cw[6] = b.z; cw[7] = b.w;
+  }
+  // ---- key: pair `lane`
+  float ka, kb;
+  if (ap.interleaved) {
+    const float2 f = unpack<BF16>(*reinterpret_cast<const uint32_t*>(
+        static_cast<const uint16_t*>(ap.k_pe) + t * ap.k_stride + 2 * lane));
+    ka = f.x;
+    kb = f.y;
+  } else {
+    ka = load1<BF16>(ap.k_pe, t * ap.k_stride + lane);
+    kb = load1<BF16>(ap.k_pe, t * ap.k_stride + 32 + lane);
+  }
+  const float* cs = ap.cos_sin + static_cast<int64_t>(pair_position(ap, t, lane)) * 64;
+  const float co = __ldg(cs + lane), si = __ldg(cs + 32 + lane);
+  const int slot = __ldg(ap.slots + t);
+
+  float y[16];   // the row's values, rounded to odd
+  if (ap.weight) {
+    uint32_t ww[8];
+    const uint4* wsrc = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(ap.weight) + 16 * lane);
+    const uint4 a = __ldg(wsrc), b = __ldg(wsrc + 1);
+    ww[0] = a.x; ww[1] = a.y; ww[2] = a.z; ww[3] = a.w;
+    ww[4] = b.x; ww[5] = b.y; ww[6] = b.z; ww[7] = b.w;
+    // sum of squares: the squares of 16-bit values are exact in fp32, each
+    // addition's error is kept
+    float s = 0.f, e = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float2 f = unpack<BF16>(cw[k]);
+      F2 u = two_sum(s, f.x * f.x);
+      e += u.lo;
+      u = two_sum(u.hi, f.y * f.y);
+      s = u.hi;
+      e += u.lo;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const float s2 = __shfl_xor_sync(0xffffffffu, s, o), e2 = __shfl_xor_sync(0xffffffffu, e, o);
+      const F2 u = two_sum(s, s2);
+      s = u.hi;
+      e = (e + e2) + u.lo;
+    }
+    F2 m = two_sum(s * (1.f / 512), ap.eps);
+    m = renorm(m.hi, m.lo + e * (1.f / 512));
+    // 1 / sqrt(m): the fp32 estimate and one Newton step on its exact residual
+    const float r0 = rsqrtf(m.hi);
+    const float r2 = r0 * r0, r2e = fmaf(r0, r0, -r2);
+    const float res = fmaf(-m.hi, r2, 1.f) - (m.hi * r2e + m.lo * r2);
+    const float rl = 0.5f * r0 * res;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float2 f = unpack<BF16>(cw[k]), w = unpack<BF16>(ww[k]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float xw = h ? f.y * w.y : f.x * w.x;   // exact
+        const float p = xw * r0;
+        const F2 v = renorm(p, fmaf(xw, r0, -p) + xw * rl);
+        y[2 * k + h] = xw == 0.f ? xw : to_odd(v.hi, v.lo);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float2 f = unpack<BF16>(cw[k]);
+      y[2 * k] = f.x;
+      y[2 * k + 1] = f.y;
+    }
+  }
+  const F2 v0 = mul_diff(ka, co, kb, si), v1 = mul_diff(ka, si, kb, -co);
+  const float r0 = to_odd(v0.hi, v0.lo), r1 = to_odd(v1.hi, v1.lo);
+
+  bool store = slot >= 0;
+  if (slot < -1 || slot >= ap.num_slots) {
+    if (lane == 0) set_error(ap.err, kDevBadSlot);
+    store = false;
+  }
+  // element of the key's two values within the row
+  const int e0 = 512 + (ap.interleaved ? 2 * lane : lane);
+  const int e1 = ap.interleaved ? e0 + 1 : e0 + 32;
+
+  if constexpr (KIND == kKvModel || KIND == kKvE2M1) {
+    uint32_t w[8];
+    float q0 = r0, q1 = r1;
+    if constexpr (KIND == kKvE2M1) {
+      // latent: the lane's 16 values are one block
+      float am = 0.f;
+      bool nan = false;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        am = fmaxf(am, fabsf(y[k]));
+        nan |= y[k] != y[k];
+      }
+      const uint32_t sb = block_scale(am, nan, ap.kv6);
+      const float d = from_e4m3(sb) * ap.kv_scale;
+      uint32_t code[2] = {0, 0};
+#pragma unroll
+      for (int k = 0; k < 8; ++k) code[k >> 2] |= e2m1_pair(y[2 * k], y[2 * k + 1], d) << (8 * (k & 3));
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t c = code[k >> 2] >> (8 * (k & 3));
+        w[k] = pack2<BF16>(e2m1_value(c & 15u) * d, e2m1_value((c >> 4) & 15u) * d);
+      }
+      // key: a block is 8 lanes' pairs (interleaved) or 16 lanes' first or
+      // second values (halves)
+      float a0 = fabsf(r0), a1 = fabsf(r1);
+      bool n0 = r0 != r0, n1 = r1 != r1;
+      if (ap.interleaved) {
+        a0 = a1 = fmaxf(a0, a1);
+        n0 = n1 = n0 || n1;
+      }
+#pragma unroll
+      for (int o = 1; o < 16; o <<= 1) {
+        const float x0 = __shfl_xor_sync(0xffffffffu, a0, o), x1 = __shfl_xor_sync(0xffffffffu, a1, o);
+        const int m0 = __shfl_xor_sync(0xffffffffu, static_cast<int>(n0), o);
+        const int m1 = __shfl_xor_sync(0xffffffffu, static_cast<int>(n1), o);
+        if (o < 8 || !ap.interleaved) {
+          a0 = fmaxf(a0, x0);
+          a1 = fmaxf(a1, x1);
+          n0 |= m0 != 0;
+          n1 |= m1 != 0;
+        }
+      }
+      const uint32_t sb0 = block_scale(a0, n0, ap.kv6), sb1 = block_scale(a1, n1, ap.kv6);
+      const float d0 = from_e4m3(sb0) * ap.kv_scale, d1 = from_e4m3(sb1) * ap.kv_scale;
+      uint32_t kc = ap.interleaved ? e2m1_pair(r0, r1, d0)
+                                   : ((e2m1_pair(r0, 0.f, d0) & 15u) | (e2m1_pair(r1, 0.f, d1) << 4));
+      q0 = e2m1_value(kc & 15u) * d0;
+      q1 = e2m1_value(kc >> 4) * (ap.interleaved ? d0 : d1);
+      // scales of four lanes in a word: lane 4 j writes blocks 4 j .. 4 j + 3
+      uint32_t sw = sb;
+      sw |= __shfl_down_sync(0xffffffffu, sw, 1) << 8;
+      sw |= __shfl_down_sync(0xffffffffu, sw, 2) << 16;
+      // the key's four block scales: one per eighth lane (interleaved), or the
+      // two halves' of lanes 0 and 16
+      const uint32_t ks = ap.interleaved
+                              ? (__shfl_sync(0xffffffffu, sb0, 0) | (__shfl_sync(0xffffffffu, sb0, 8) << 8) |
+                                 (__shfl_sync(0xffffffffu, sb0, 16) << 16) | (__shfl_sync(0xffffffffu, sb0, 24) << 24))
+                              : (__shfl_sync(0xffffffffu, sb0, 0) | (__shfl_sync(0xffffffffu, sb0, 16) << 8) |
+                                 (__shfl_sync(0xffffffffu, sb1, 0) << 16) | (__shfl_sync(0xffffffffu, sb1, 16) << 24));
+      // byte `lane` of the key's 32 (halves: even lanes hold the pair of first
+      // values of lanes l, l + 1, odd ones that of the second values)
+      const uint32_t other = __shfl_xor_sync(0xffffffffu, kc, 1);
+      uint32_t kbyte = kc;
+      int kat = lane;
+      if (!ap.interleaved) {
+        kbyte = (lane & 1) ? ((other >> 4) | (kc & 0xF0u)) : ((kc & 15u) | ((other & 15u) << 4));
+        kat = (lane & 1) * 16 + (lane >> 1);
+      }
+      if (store) {
+        const int page = slot / ap.bs, off = slot - page * ap.bs;
+        uint8_t* base = static_cast<uint8_t*>(ap.cache) + static_cast<int64_t>(page) * ap.bs * kE2m1Row;
+        uint8_t* codes = base + off * kE2m1Codes;
+        uint8_t* scales = base + ap.bs * kE2m1Codes + off * kE2m1Scales;
+        *reinterpret_cast<uint2*>(codes + 8 * lane) = make_uint2(code[0], code[1]);
+        codes[256 + kat] = static_cast<uint8_t>(kbyte);
+        if ((lane & 3) == 0) *reinterpret_cast<uint32_t*>(scales + lane) = sw;
+        if (lane == 0) *reinterpret_cast<uint32_t*>(scales + 32) = ks;
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) w[k] = pack2<BF16>(y[2 * k], y[2 * k + 1]);
+    }
+    auto put = [&](uint16_t* row) {
+      uint4* d4 = reinterpret_cast<uint4*>(row + 16 * lane);
+      d4[0] = make_uint4(w[0], w[1], w[2], w[3]);
+      d4[1] = make_uint4(w[4], w[5], w[6], w[7]);
+      if (ap.interleaved) {
+        *reinterpret_cast<uint32_t*>(row + e0) = pack2<BF16>(q0, q1);
+      } else {
+        row[e0] = pack1<BF16>(q0);
+        row[e1] = pack1<BF16>(q1);
+      }
+    };
+    if (ap.kv_out) put(static_cast<uint16_t*>(ap.kv_out) + static_cast<int64_t>(t) * 576);
+    if (KIND == kKvModel && store) put(static_cast<uint16_t*>(ap.cache) + static_cast<int64_t>(slot) * 576);
+  } else {
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      w[k] = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[k] |= to_e4m3(__fdiv_rn(y[4 * k + j], ap.kv_scale)) << (8 * j);
+    }
+    const uint32_t b0 = to_e4m3(__fdiv_rn(r0, ap.kv_scale)), b1 = to_e4m3(__fdiv_rn(r1, ap.kv_scale));
+    auto put = [&](uint8_t* row) {
+      *reinterpret_cast<uint4*>(row + 16 * lane) = make_uint4(w[0], w[1], w[2], w[3]);
+      if (ap.interleaved) {
+        *reinterpret_cast<uint16_t*>(row + e0) = static_cast<uint16_t>(b0 | (b1 << 8));
+      } else {
+        row[e0] = static_cast<uint8_t>(b0);
+        row[e1] = static_cast<uint8_t>(b1);
+      }
+    };
+    if (ap.kv_out) put(static_cast<uint8_t*>(ap.kv_out) + static_cast<int64_t>(t) * 576);
+    if (store) put(static_cast<uint8_t*>(ap.cache) + static_cast<int64_t>(slot) * 576);
+  }
+}
+
+// Four RoPE pairs of one head's query: pairs 4 j .. 4 j + 3 for lane j of the
+// head's eight.
+template <bool BF16>
+__device__ void rotate_query(const AppendParams& ap, int64_t item, int j) {
+  const int t = static_cast<int>(item / ap.H), h = static_cast<int>(item - static_cast<int64_t>(t) * ap.H);
+  const uint16_t* src = static_cast<const uint16_t*>(ap.q_pe) + t * ap.q_stride + h * ap.q_head_stride;
+  uint16_t* dst = static_cast<uint16_t*>(ap.q_out) + t * ap.qo_stride + h * ap.qo_head_stride;
+  float a[4], b[4];
+  if (ap.interleaved) {
+    const uint4 x = *reinterpret_cast<const uint4*>(src + 8 * j);
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 f = unpack<BF16>(w[k]);
+      a[k] = f.x;
+      b[k] = f.y;
+    }
+  } else {
+    const uint2 x = *reinterpret_cast<const uint2*>(src + 4 * j);
+    const uint2 z = *reinterpret_cast<const uint2*>(src + 32 + 4 * j);
+    const float2 x0 = unpack<BF16>(x.x), x1 = unpack<BF16>(x.y), z0 = unpack<BF16>(z.x), z1 = unpack<BF16>(z.y);
+    a[0] = x0.x; a[1] = x0.y; a[2] = x1.x; a[3] = x1.y;
+    b[0] = z0.x; b[1] = z0.y; b[2] = z1.x; b[3] = z1.y;
+  }
+  float4 co, si;
+  const int i0 = 4 * j;
+  // the four pairs read one row unless a section ends among them
+  const bool cut = (ap.sec1 > i0 && ap.sec1 < i0 + 4) || (ap.sec2 > i0 && ap.sec2 < i0 + 4);
+  if (!cut) {
+    const float* cs = ap.cos_sin + static_cast<int64_t>(pair_position(ap, t, i0)) * 64 + i0;
+    co = __ldg(reinterpret_cast<const float4*>(cs));
+    si = __ldg(reinterpret_cast<const float4*>(cs + 32));
+  } else {
+    float c[4], s[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float* cs = ap.cos_sin + static_cast<int64_t>(pair_position(ap, t, i0 + k)) * 64 + i0 + k;
+      c[k] = __ldg(cs);
+      s[k] = __ldg(cs + 32);
+    }
+    co = make_float4(c[0], c[1], c[2], c[3]);
+    si = make_float4(s[0], s[1], s[2], s[3]);
+  }
+  const float c[4] = {co.x, co.y, co.z, co.w}, s[4] = {si.x, si.y, si.z, si.w};
+  float u[4], v[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    u[k] = fmaf(a[k], c[k], -(b[k] * s[k]));
+    v[k] = fmaf(a[k], s[k], b[k] * c[k]);
+  }
+  if (ap.interleaved) {
+    *reinterpret_cast<uint4*>(dst + 8 * j) =
+        make_uint4(pack2<BF16>(u[0], v[0]), pack2<BF16>(u[1], v[1]), pack2<BF16>(u[2], v[2]), pack2<BF16>(u[3], v[3]));
+  } else {
+    *reinterpret_cast<uint2*>(dst + 4 * j) = make_uint2(pack2<BF16>(u[0], u[1]), pack2<BF16>(u[2], u[3]));
+    *reinterpret_cast<uint2*>(dst + 32 + 4 * j) = make_uint2(pack2<BF16>(v[0], v[1]), pack2<BF16>(v[2], v[3]));
+  }
+}
+
+}  // namespace
+
+template <bool BF16, int KIND>
+__global__ void __launch_bounds__(kAppendThreads) mla_kv_append_kernel(const AppendParams ap) {
+  const int blk = static_cast<int>(blockIdx.x);
+  if (blk < ap.row_blocks) {
+    const int t = blk * (kAppendThreads / 32) + (threadIdx.x >> 5);
+    if (t < ap.T) append_row<BF16, KIND>(ap, t, threadIdx.x & 31);
+  } else {
+    const int64_t item = static_cast<int64_t>(blk - ap.row_blocks) * (kAppendThreads / 8) + (threadIdx.x >> 3);
+    if (item < static_cast<int64_t>(ap.T) * ap.H) rotate_query<BF16>(ap, item, threadIdx.x & 7);
+  }
+}
+
+template <bool BF16>
+static int launch_append_t(const AppendParams& ap, int kind, unsigned blocks, cudaStream_t stream) {
+  switch (kind) {
+    case kKvModel: mla_kv_append_kernel<BF16, kKvModel><<<blocks, kAppendThreads, 0, stream>>>(ap); return 0;
+    case kKvE4M3: mla_kv_append_kernel<BF16, kKvE4M3><<<blocks, kAppendThreads, 0, stream>>>(ap); return 0;
+    default: mla_kv_append_kernel<BF16, kKvE2M1><<<blocks, kAppendThreads, 0, stream>>>(ap); return 0;
+  }
+}
+
+int launch_append(AppendParams ap, int kind, bool bf16, cudaStream_t stream) {
+  ap.row_blocks = ceil_div(ap.T, kAppendThreads / 32);
+  const int64_t heads = ap.q_pe ? static_cast<int64_t>(ap.T) * ap.H : 0;
+  const int64_t blocks = ap.row_blocks + (heads + kAppendThreads / 8 - 1) / (kAppendThreads / 8);
+  return bf16 ? launch_append_t<true>(ap, kind, static_cast<unsigned>(blocks), stream)
+              : launch_append_t<false>(ap, kind, static_cast<unsigned>(blocks), stream);
+}
+
+}  // namespace mla
