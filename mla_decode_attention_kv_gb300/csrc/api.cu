@@ -333,13 +333,21 @@ int mla_dcp_decode_partial_fp4(const void* q_abs, const void* q_pe, const void* 
                                     q_len, H, num_blocks, block_size, max_blocks, num_shards,
                                     scale, in_dtype, part_dtype, o_part, lse_part);
   if (rc != MLA_OK) return rc;
-  if (!(kv_scale > 0.f) || !std::isfinite(kv_scale) || !std::isfinite(scale * kv_scale * 1.4426950408889634f))
+  if (!(kv_scale > 0.f) || !std::isfinite(kv_scale) || !std::isfinite(scale * 1.4426950408889634f * kv_scale))
     return MLA_ERR_BAD_SHAPE;
   if (head_slices < 1 || H % head_slices != 0) return MLA_ERR_BAD_SHAPE;
   if (workspace && reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return MLA_ERR_MISALIGNED;
-  mla::Fp4Params fp;
-  fp.q_abs = q_abs;
-  fp.q_pe = q_pe;
+  const bool bf16 = in_dtype == MLA_BF16;
+  const int64_t R = static_cast<int64_t>(q_len) * H;
+  const int rows = mla::fp4_unit_rows(R);
+  const int64_t G = (R + rows - 1) / rows;
+  const int P = num_shards + (kv_cur ? 1 : 0);
+  if (G * B * P > INT32_MAX) return MLA_ERR_BAD_SHAPE;
+  CUtensorMap tm_qlat, tm_qpe;
+  if (!make_map(&tm_qlat, q_abs, 512, B * R, 1024, 64, rows, bf16) ||
+      !make_map(&tm_qpe, q_pe, 64, B * R, 128, 64, rows, bf16))
+    return MLA_ERR_CUDA;
+  mla::Fp4Params fp = {};
   fp.kv_cache = static_cast<const uint8_t*>(kv_cache);
   fp.block_table = block_table;
   fp.seq_lens = seq_lens;
@@ -354,12 +362,30 @@ int mla_dcp_decode_partial_fp4(const void* q_abs, const void* q_pe, const void* 
   fp.bs = block_size;
   fp.max_blocks = max_blocks;
   fp.S = num_shards;
-  fp.P = num_shards + (kv_cur ? 1 : 0);
+  fp.P = P;
   fp.head_slices = head_slices;
+  fp.T = B * q_len;
+  fp.R = static_cast<int>(R);
+  fp.G = static_cast<int>(G);
+  fp.num_units = static_cast<int>(G * B * P);
+  fp.box = block_size < 64 ? block_size : 64;
+  for (int bs = block_size; bs > 1; bs >>= 1) ++fp.bs_shift;
   fp.scale_log2 = scale * 1.4426950408889634f;
   fp.kv_scale = kv_scale;
   fp.part_dtype = part_dtype;
-  return launched(mla::launch_partial_fp4(fp, in_dtype == MLA_BF16, reinterpret_cast<cudaStream_t>(stream)));
+  fp.spin_limit = mla::partial_spin_limit();
+  if (workspace) {
+    const int ctas = mla::fp4_max_ctas();
+    if (ctas < 1) return MLA_ERR_CUDA;
+    if (workspace_bytes < mla::fp4_workspace_bytes(ctas)) return MLA_ERR_BAD_SHAPE;
+    char* w = static_cast<char*>(workspace);
+    fp.split = ctas;
+    fp.ws_units = reinterpret_cast<int4*>(w);
+    fp.ws_bounds = reinterpret_cast<int*>(w + static_cast<size_t>(ctas) * 16);
+    fp.ws_lse = reinterpret_cast<float*>(w + mla::fp4_workspace_recs(ctas));
+    fp.ws_o = w + mla::fp4_workspace_recs(ctas) + 2 * static_cast<size_t>(ctas) * mla::kFp4MaxRows * 4;
+  }
+  return launched(mla::launch_partial_fp4(tm_qlat, tm_qpe, fp, rows, bf16, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 uint64_t mla_dcp_decode_partial_workspace_size(int B, int q_len, int num_shards, int has_current) {
@@ -375,7 +401,8 @@ uint64_t mla_dcp_decode_partial_fp4_workspace_size(int B, int q_len, int num_sha
   if (B < 1 || q_len < 1 || q_len > MLA_MAX_Q_LEN || num_shards < 1 || num_shards > MLA_MAX_SHARDS) return 0;
   const int64_t units = static_cast<int64_t>(B) * q_len * (num_shards + (has_current ? 1 : 0));
   if (units > INT32_MAX) return 0;
-  return 256;
+  const int ctas = mla::fp4_max_ctas();
+  return ctas < 1 ? 0 : mla::fp4_workspace_bytes(ctas);
 }
 
 // ------------------------------------------------------------------ no-alloc variant

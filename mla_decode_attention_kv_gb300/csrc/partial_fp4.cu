@@ -1,6 +1,46 @@
 // Partial attention per context shard over a 4-bit (E2M1) latent cache:
-// mla_dcp_decode_partial_fp4.  The attention is the one of the 16-bit kernel
-// on the decoded values e * s * kv_scale.
+// mla_dcp_decode_partial_fp4.
+//
+// A cached value is code * s * kv_scale: a 4-bit code, an E4M3 scale s for
+// every 16 values.  code * s has at most six significant bits, so it is a
+// value of either 16-bit type, and the tensor cores multiply the cache as it
+// is stored by the query as it is given.  The attention is that of the 16-bit
+// kernel (units, shards, CURRENT part, lazily rescaled online softmax).
+//
+// What bounds it.  A token is 324 bytes against 1152, and its codes have to
+// become 16-bit operands in shared memory before an MMA can read them, so an
+// SM's shared memory (and the unpacking) is what a token costs, not HBM.  So
+// each token is unpacked once per SM and used for both products, and the
+// MMAs' cost is made to follow the number of query rows:
+//   S^T = K Q^T     A = K tile [64 tokens x 576] (K-major), B = Q [rows x 576]
+//   O^T += V^T P^T  A = the same tile read MN-major [latent x 64 tokens],
+//                   B = P^T [64 tokens x rows] (MN-major)
+// The tokens and the latents fill the MMAs' M, the rows (query tokens x heads
+// of one sequence, 16, 32 or 64 a unit) are N: 16 heads cost a quarter of 64,
+// where M = heads would cost the same for any number.  O^T [512 x rows] is 4
+// x rows columns of tensor memory, at most half of it, so one CTA holds all of
+// a unit, and several query tokens' rows share one pass over the history.
+//
+// One persistent CTA per SM, 640 threads:
+//   w0      producer: raw pages (codes, scales) by bulk copies, queries by TMA
+//   w1      QK issuer            w2  PV issuer           w3  empty parts
+//   w4-11   softmax: two groups of four warps with half of the rows each; a
+//           token (16 TMEM lanes a warp in an M = 64 accumulator) has two
+//           threads of a group, one for each half of its rows.  O rescale and
+//           epilogue (thread = latent)
+//   w12-19  unpacking: codes and scales to 128-byte-swizzled 16-bit chunks
+// A tile's 576 columns are unpacked as one RoPE chunk (64) and four latent
+// pairs (128 each, one M block of the PV product), through a ring of pair
+// slots: a slot is free when its PV MMAs are done.
+//
+// The softmax keeps its reference maximum per row in shared memory and tests
+// each tile against it; only a tile that exceeds it by 2^8 (and the first of a
+// piece) reduces the maximum over the tokens (the lanes) and rescales O.  Row
+// sums stay in registers, one partial sum per token lane and row, and are
+// reduced once per piece.
+//
+// Every wait is bounded, as in the 16-bit kernel.
+#include <mutex>
 #include "cache_kernels.cuh"
 #include "partial_fp4.cuh"
 #include "partial_sched.cuh"
@@ -8,104 +48,1111 @@
 namespace mla {
 
 namespace {
-constexpr int kTok = 16;   // tokens per tile
 
-__device__ __forceinline__ float e2m1_f32(uint32_t c) {
-  const uint32_t e = (c >> 1) & 3u, m = c & 1u;
-  const float mag = e == 0 ? 0.5f * m : __uint_as_float((126u + e) << 23) * (1.f + 0.5f * m);
-  return (c & 8u) ? -mag : mag;
-}
-}  // namespace
+constexpr int kTile4 = 64;                       // tokens
+constexpr int kThreads4 = 640;
+constexpr int kSoftWarp = 4, kUnpackWarp = 12;   // first warp of the softmax and of the unpacking
+constexpr int kRawCodes = kTile4 * kE2m1Codes;   // 18432
+constexpr int kRawStage = kTile4 * kE2m1Row;     // 20736
+constexpr int kPair = 2 * kTile4 * 128;          // 16 KB: 128 latents of a tile
+constexpr int kRope = kTile4 * 128;              // 8 KB
+constexpr int kUnits4 = 8;                       // units whose geometry is kept in shared memory
 
-// One block per (sequence, query token, part, 8 heads), a warp per head.
-template <bool BF16>
-__global__ void __launch_bounds__(256) mla_partial_fp4_kernel(const Fp4Params fp) {
-  __shared__ float tile[kTok][576];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int u = blockIdx.x;
-  const int p = u % fp.P, i = (u / fp.P) % fp.q_len, b = u / (fp.P * fp.q_len);
-  const int h = blockIdx.y * 8 + warp;
-  const bool cur = p == fp.S;
-  int lo = 0, hi = i + 1;
-  if (!cur) {
-    int L = fp.seq_lens[b];
+struct Unit4 {
+  int b, g, p, lo, hi;
+};
+
+template <int N>
+struct Smem4 {
+  static constexpr int kNP = N == 64 ? 6 : 8;    // pair slots (a tile takes four)
+  static constexpr int kNR = N == 64 ? 1 : 2;    // RoPE slots
+  static constexpr int kQ = N * 128 * 9;
+  static constexpr int kPairOff = 0;
+  static constexpr int kRopeOff = kPairOff + kNP * kPair;
+  static constexpr int kQOff = kRopeOff + kNR * kRope;
+  static constexpr int kPOff = kQOff + kQ;
+  static constexpr int kP = kTile4 * N * 2;
+  static constexpr int kRawOff = kPOff + kP;
+  static constexpr int kMOff = kRawOff + 2 * kRawStage;      // reference maxima [N]
+  static constexpr int kRedOff = kMOff + N * 4;              // reductions over the warps [2 groups][4][N / 2]
+  static constexpr int kUnitOff = kRedOff + N * 16;
+  static constexpr int kBarOff = kUnitOff + ((kUnits4 * 20 + 8 + 15) / 16) * 16;
+  // barrier slots
+  enum : int {
+    B_RAW_FULL = 0,
+    B_RAW_EMPTY = 2,
+    B_PAIR_FULL = 4,
+    B_PAIR_EMPTY = B_PAIR_FULL + kNP,
+    B_ROPE_FULL = B_PAIR_EMPTY + kNP,
+    B_ROPE_EMPTY = B_ROPE_FULL + kNR,
+    B_Q_FULL = B_ROPE_EMPTY + kNR,
+    B_Q_EMPTY,
+    B_S_FULL,
+    B_S_EMPTY = B_S_FULL + 2,
+    B_P_FULL = B_S_EMPTY + 2,
+    B_P_EMPTY,
+    B_DONE_QK,
+    B_DONE_PV,
+    B_COUNT
+  };
+  static constexpr int kTotal = kBarOff + (B_COUNT + 2) * 8;   // (from a 1024-aligned base)
+  static constexpr int kTmemO = 0;
+  static constexpr int kTmemS = 4 * N;
+  static constexpr int kTmemCols = N == 64 ? 512 : N == 32 ? 256 : 128;   // 6 N, a power of two
+};
+static_assert(Smem4<64>::kTotal <= 232448 && Smem4<32>::kTotal <= 232448, "shared memory budget");
+
+// ---------------------------------------------------------------- units
+// u = (g * B + b) * P + p: the row groups outermost, so that the CTAs of
+// several groups stream the same histories at the same time (as the query
+// tokens of the 16-bit kernel).
+template <int N>
+__device__ __noinline__ Unit4 unit4(const Fp4Params& fp, int u) {
+  Unit4 ui;
+  ui.p = u % fp.P;
+  const int gb = u / fp.P;
+  ui.b = gb % fp.B;
+  ui.g = gb / fp.B;
+  if (ui.p == fp.S) {
+    // CURRENT: the tokens that the group's last row sees (one tile)
+    ui.lo = 0;
+    ui.hi = (min(fp.R, (ui.g + 1) * N) - 1) / fp.H + 1;
+  } else {
+    int L = fp.seq_lens[ui.b];
     const int cap = fp.max_blocks * fp.bs;
     if (L < 0 || L > cap) {
       set_error(fp.err, kDevBadSeqLen);
       L = max(0, min(L, cap));
     }
     const int chunk = fp.S * fp.bs;
-    const int len = fp.bs * ((L + chunk - 1) / chunk);
-    lo = min(L, p * len);
-    hi = min(L, (p + 1) * len);
+    const int len = L > 0 ? fp.bs * ((L + chunk - 1) / chunk) : 0;
+    ui.lo = min(L, ui.p * len);
+    ui.hi = min(L, (ui.p + 1) * len);
   }
-  const int64_t row = (static_cast<int64_t>(b) * fp.q_len + i) * fp.H + min(h, fp.H - 1);
-  float q[18], o[16];
-  const uint16_t* qa = static_cast<const uint16_t*>(fp.q_abs) + row * 512;
-  const uint16_t* qp = static_cast<const uint16_t*>(fp.q_pe) + row * 64;
-  for (int k = 0; k < 18; ++k) {
-    const int c = lane + 32 * k;
-    q[k] = unpack2(c < 512 ? qa[c] : qp[c - 512], BF16 ? kBF16 : kFP16).x;
-  }
-  for (int k = 0; k < 16; ++k) o[k] = 0.f;
-  float m = -INFINITY, l = 0.f;
-  for (int t0 = lo; t0 < hi; t0 += kTok) {
-    const int n = min(kTok, hi - t0);
-    __syncthreads();
-    for (int x = threadIdx.x; x < n * 36; x += 256) {
-      const int t = x / 36, g = x - t * 36, tok = t0 + t;
-      if (cur) {
-        const uint16_t* src = static_cast<const uint16_t*>(fp.kv_cur) +
-                              (static_cast<int64_t>(b) * fp.q_len + tok) * 576 + g * 16;
-        for (int e = 0; e < 16; ++e) tile[t][g * 16 + e] = unpack2(src[e], BF16 ? kBF16 : kFP16).x;
-      } else {
-        int id = fp.block_table[static_cast<int64_t>(b) * fp.max_blocks + tok / fp.bs];
-        if (id < 0 || id >= fp.num_blocks) {
-          set_error(fp.err, kDevBadBlockId);
-          id = 0;
-        }
-        const uint8_t* page = fp.kv_cache + static_cast<int64_t>(id) * fp.bs * kE2m1Row;
-        const int off = tok & (fp.bs - 1);
-        const uint8_t* codes = page + off * kE2m1Codes + g * 8;
-        const __half_raw hr = __nv_cvt_fp8_to_halfraw(page[fp.bs * kE2m1Codes + off * kE2m1Scales + g], __NV_E4M3);
-        const float s = __half2float(*reinterpret_cast<const __half*>(&hr)) * fp.kv_scale;
-        for (int e = 0; e < 8; ++e) {
-          tile[t][g * 16 + 2 * e] = e2m1_f32(codes[e] & 15u) * s;
-          tile[t][g * 16 + 2 * e + 1] = e2m1_f32(codes[e] >> 4) * s;
-        }
-      }
-    }
-    __syncthreads();
-    for (int t = 0; t < n; ++t) {
-      float s = 0.f;
-      for (int k = 0; k < 18; ++k) s = fmaf(q[k], tile[t][lane + 32 * k], s);
-      for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-      s *= fp.scale_log2;
-      const float mn = fmaxf(m, s);
-      const float a = exp2f(m - mn), w = exp2f(s - mn);
-      m = mn;
-      l = l * a + w;
-      for (int k = 0; k < 16; ++k) o[k] = fmaf(o[k], a, w * tile[t][lane + 32 * k]);
-    }
-  }
-  if (h >= fp.H) return;
-  const int hs = fp.H / fp.head_slices, sl = h / hs;
-  const int64_t out = ((static_cast<int64_t>(sl) * fp.B * fp.q_len + static_cast<int64_t>(b) * fp.q_len + i) * fp.P + p) * hs + (h - sl * hs);
-  const float inv = hi > lo ? 1.f / l : 0.f;
-  for (int k = 0; k < 16; ++k) {
-    const float v = o[k] * inv;
-    const int64_t e = out * 512 + lane + 32 * k;
-    if (fp.part_dtype == kFP32) static_cast<float*>(fp.o_part)[e] = v;
-    else static_cast<uint16_t*>(fp.o_part)[e] = static_cast<uint16_t>(pack2_dt(v, 0.f, fp.part_dtype) & 0xFFFFu);
-  }
-  if (lane == 0) fp.lse_part[out] = hi > lo ? (m + log2f(l)) * kLn2 : -INFINITY;
+  return ui;
 }
 
-int launch_partial_fp4(const Fp4Params& fp, bool bf16, cudaStream_t stream) {
-  const dim3 grid(fp.B * fp.q_len * fp.P, (fp.H + 7) / 8);
-  if (bf16) mla_partial_fp4_kernel<true><<<grid, 256, 0, stream>>>(fp);
-  else mla_partial_fp4_kernel<false><<<grid, 256, 0, stream>>>(fp);
-  return 0;
+__device__ __forceinline__ int tiles4(const Unit4& ui) { return (ui.hi - ui.lo + kTile4 - 1) / kTile4; }
+
+struct UnitTable {
+  int first, n;
+  Unit4 u[kUnits4];
+};
+
+template <int N>
+__device__ __noinline__ Unit4 unit4_get(const Fp4Params& fp, const UnitTable* tab, int u) {
+  const unsigned k = static_cast<unsigned>(u - tab->first);
+  if (k < static_cast<unsigned>(tab->n)) return tab->u[k];
+  return unit4<N>(fp, u);
+}
+
+struct Range4 {
+  int u_begin, j_begin, u_last, j_stop;
+};
+
+// The tiles of a CTA's range as one stream; a piece is the part of one unit in it.
+template <int N>
+struct Iter4 {
+  int u, j, jfirst, jend, u_last, j_stop, key, nq;
+  bool valid, newq;
+  Unit4 ui;
+  const UnitTable* tab;
+  __device__ __forceinline__ void start(const Fp4Params& fp, const UnitTable* t, const Range4& r) {
+    tab = t;
+    u_last = r.u_last;
+    j_stop = r.j_stop;
+    key = nq = -1;
+    valid = r.u_begin <= r.u_last;
+    if (!valid) return;
+    u = r.u_begin;
+    ui = unit4_get<N>(fp, tab, u);
+    enter(fp, r.j_begin);
+  }
+  __device__ __forceinline__ void enter(const Fp4Params& fp, int j0) {
+    j = jfirst = j0;
+    jend = u == u_last ? j_stop : tiles4(ui);
+    const int k = ui.g * fp.B + ui.b;
+    newq = k != key;
+    if (newq) {
+      ++nq;
+      key = k;
+    }
+  }
+  __device__ __forceinline__ void advance(const Fp4Params& fp) {
+    if (++j < jend) return;
+    while (u < u_last) {
+      ++u;
+      ui = unit4_get<N>(fp, tab, u);
+      if (ui.hi > ui.lo) {
+        enter(fp, 0);
+        return;
+      }
+    }
+    valid = false;
+  }
+  __device__ __forceinline__ bool first() const { return j == jfirst; }
+  __device__ __forceinline__ bool last() const { return j == jend - 1; }
+  __device__ __forceinline__ bool whole() const { return jfirst == 0 && jend == tiles4(ui); }
+  __device__ __forceinline__ int tok0() const { return ui.lo + j * kTile4; }
+  // whether the next tile (if any) reads another query
+  __device__ __forceinline__ bool last_of_q(const Fp4Params& fp) const {
+    if (!last()) return false;
+    Iter4 n = *this;
+    n.advance(fp);
+    return !n.valid || n.newq;
+  }
+};
+
+// ---------------------------------------------------------------- partition
+// Equal shares of cost, as partition_tiles of the 16-bit kernel: a tile costs
+// kCostTile, a unit kCostUnit besides (its first tile's latency, the epilogue).
+// With a workspace the shares are exact (units are cut where whole ones would
+// leave the busiest CTA above the even share by more than max(3 tiles, 1/8)),
+// without one a CTA takes the whole units whose first tile lies in its share.
+constexpr int kCostTile = 1;
+constexpr int kCostUnit = 2;
+
+struct PartScratch {
+  unsigned long long scan[32];
+  int load[kFp4MaxCtas];
+  int bound[kFp4MaxCtas + 1];
+  int rng[4];
+  int nt[8192];
+};
+
+template <int N>
+__device__ __forceinline__ Range4 partition4(const Fp4Params& fp, PartScratch* ps, int cid, int ncta) {
+  constexpr int kWarps = kThreads4 / 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int U = fp.num_units;
+  const int per = (U + kThreads4 - 1) / kThreads4;
+  const int a = min(U, static_cast<int>(threadIdx.x) * per), e = min(U, a + per);
+  int cnt = 0, cost = 0;
+  for (int u = a; u < e; ++u) {
+    const int nt = tiles4(unit4<N>(fp, u));
+    if (u < 8192) ps->nt[u] = nt;
+    cnt += nt;
+    cost += nt > 0 ? kCostTile * nt + kCostUnit : 0;
+  }
+  auto unit_tiles = [&](int u) { return u < 8192 ? ps->nt[u] : tiles4(unit4<N>(fp, u)); };
+  const unsigned long long mine = (static_cast<unsigned long long>(cost) << 32) | static_cast<unsigned>(cnt);
+  unsigned long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned long long y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) ps->scan[warp] = incl;
+  if (threadIdx.x == 0) {
+    ps->rng[0] = INT_MAX;
+    ps->rng[1] = 0;
+    ps->rng[2] = -1;
+    ps->rng[3] = 0;
+  }
+  for (int c = threadIdx.x; c < ncta; c += kThreads4) ps->load[c] = 0;
+  __syncthreads();
+  unsigned long long base = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const unsigned long long t = ps->scan[w];
+    base += w < warp ? t : 0;
+    all += t;
+  }
+  const unsigned long long before = base + incl - mine;
+  const int tstart = static_cast<int>(before & 0xffffffffu);
+  const int64_t cstart = static_cast<int64_t>(before >> 32);
+  const int total = static_cast<int>(all & 0xffffffffu);
+  const int64_t all_cost = static_cast<int64_t>(all >> 32);
+  if (all_cost > 0) {
+    int64_t crun = cstart;
+    int trun = tstart;
+    for (int u = a; u < e; ++u) {
+      const int nt = unit_tiles(u);
+      if (nt == 0) continue;
+      const int64_t cend = crun + kCostTile * nt + kCostUnit;
+      for (int c = max(1, static_cast<int>((crun * ncta + all_cost - 1) / all_cost)); c < ncta; ++c) {
+        const int64_t tc = static_cast<int64_t>(c) * all_cost / ncta;
+        if (tc >= cend) break;
+        const int64_t into = tc - crun - kCostUnit;
+        const int64_t j = into <= 0 ? 0 : min(static_cast<int64_t>(nt), (into + kCostTile - 1) / kCostTile);
+        ps->bound[c] = trun + static_cast<int>(j);
+      }
+      trun += nt;
+      crun = cend;
+    }
+  } else {
+    for (int c = threadIdx.x; c <= ncta; c += kThreads4) ps->bound[c] = 0;
+  }
+  if (threadIdx.x == 0) {
+    ps->bound[0] = 0;
+    ps->bound[ncta] = total;
+  }
+  __syncthreads();
+  auto cta_of = [&](int t) {   // the last CTA whose share starts at or before tile t
+    int lo = 0, hi = ncta - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (ps->bound[mid] <= t) lo = mid;
+      else hi = mid - 1;
+    }
+    return lo;
+  };
+  bool split = false;
+  if (fp.split && total > 0) {
+    int run = tstart;
+    for (int u = a; u < e; ++u) {
+      const int nt = unit_tiles(u);
+      if (nt > 0) atomicAdd(&ps->load[cta_of(run)], kCostTile * nt + kCostUnit);
+      run += nt;
+    }
+    __syncthreads();
+    int mx = 0;
+    for (int c = threadIdx.x; c < ncta; c += kThreads4) mx = max(mx, ps->load[c]);
+    const int64_t even = (all_cost + ncta - 1) / ncta;
+    split = __syncthreads_or(mx > even + max(int64_t{3 * kCostTile}, even / 8)) != 0;
+  }
+  const int lo = ps->bound[cid], hi = ps->bound[cid + 1];
+  int run = tstart;
+  for (int u = a; u < e; ++u) {
+    const int nt = unit_tiles(u);
+    if (nt > 0 && lo < hi) {
+      if (split) {
+        if (lo >= run && lo < run + nt) {
+          ps->rng[0] = u;
+          ps->rng[1] = lo - run;
+        }
+        if (hi - 1 >= run && hi - 1 < run + nt) {
+          ps->rng[2] = u;
+          ps->rng[3] = hi - run;
+        }
+      } else if (run >= lo && run < hi) {
+        atomicMin(&ps->rng[0], u);
+        atomicMax(&ps->rng[2], u);
+      }
+    }
+    run += nt;
+  }
+  __syncthreads();
+  Range4 r;
+  r.u_begin = ps->rng[0];
+  r.j_begin = ps->rng[1];
+  r.u_last = ps->rng[2];
+  r.j_stop = split ? ps->rng[3] : (r.u_last < 0 ? 0 : unit_tiles(r.u_last));
+  // the record of the unit that was cut before this share and ends inside it
+  if (fp.split && threadIdx.x == 0) {
+    int4 rec = make_int4(-1, 0, 0, 0);
+    if (split && r.u_begin <= r.u_last && r.j_begin > 0 &&
+        (r.u_begin < r.u_last || r.j_stop == unit_tiles(r.u_begin))) {
+      const int ustart = lo - r.j_begin;
+      rec = make_int4(r.u_begin, ustart, cta_of(ustart), cid);
+    }
+    fp.ws_units[cid] = rec;
+    fp.ws_bounds[cid] = lo;
+    if (cid == 0) fp.ws_bounds[ncta] = total;
+  }
+  return r;
+}
+
+// Row of o_part / lse_part of query row r (of R) of sequence b in part p.
+__device__ __forceinline__ int64_t out_row4(const Fp4Params& fp, int b, int r, int p) {
+  const int i = r / fp.H, h = r - i * fp.H;
+  const int hs = fp.H / fp.head_slices, s = h / hs;
+  return ((static_cast<int64_t>(s) * fp.T + static_cast<int64_t>(b) * fp.q_len + i) * fp.P + p) * hs + (h - s * hs);
+}
+
+// ---------------------------------------------------------------- pieces of PTX
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(__cvta_generic_to_global(src)), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+// Columns [c, c + NC) of an M = 64 accumulator for lanes 0-15 of the warp and
+// [c + NC, c + 2 NC) for lanes 16-31, both of the rows in TMEM lanes 0-15.
+__device__ __forceinline__ void tmem_half(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x32bx2.x4.b32 {%0,%1,%2,%3}, [%4], 4;\n tcgen05.wait::ld.sync.aligned;"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_half(uint32_t a, uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x32bx2.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8], 8;\n tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "r"(a)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_half(uint32_t a, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x32bx2.x16.b32"
+      " {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16], 16;\n tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(a)
+      : "memory");
+}
+
+// 8, 16 or 32 columns of this warp's 32 lanes, loaded and waited for
+__device__ __forceinline__ void tmem_get(uint32_t a, uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "r"(a)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_get(uint32_t a, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32"
+      " {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(a)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_get(uint32_t a, uint32_t (&r)[32]) {
+  tmem_ld32(a, r);
+  tmem_wait_ld(r);
+}
+__device__ __forceinline__ void tmem_put(uint32_t a, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(a), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_put(uint32_t a, const uint32_t (&r)[16]) { tmem_st16(a, r); }
+__device__ __forceinline__ void tmem_put(uint32_t a, const uint32_t (&r)[32]) { tmem_st32(a, r); }
+
+// MN-major operand of N columns (rows of N 16-bit values, one per k): the
+// swizzle as wide as the row, 8-row groups one after another.
+template <int N>
+__device__ __forceinline__ uint64_t desc_mn(uint32_t addr) {
+  constexpr uint64_t type = N == 64 ? 2 : N == 32 ? 4 : 6;   // 128-, 64-, 32-byte swizzle
+  constexpr uint32_t sbo = 8 * N * 2;
+  return static_cast<uint64_t>((addr >> 4) & 0x3FFF) | (uint64_t{1} << 16) |
+         (static_cast<uint64_t>(sbo >> 4) << 32) | (uint64_t{1} << 46) | (type << 61);
+}
+
+// Byte offset of 16-byte unit k of row t in that layout.
+template <int N>
+__device__ __forceinline__ uint32_t p_offset(int t, int k) {
+  const int x = N == 64 ? (t & 7) : N == 32 ? ((t >> 1) & 3) : ((t >> 2) & 1);
+  return t * (N * 2) + ((k ^ x) << 4);
+}
+
+// Reduction over the 16 lanes of a half warp of NC columns held one row per
+// lane: every step halves the columns a lane keeps, so 16 columns take 15
+// shuffles.  Lane l ends with column (l & 15) / (16 / NC).
+template <int NC, bool MAX>
+__device__ __forceinline__ float col_reduce(float (&v)[NC], int lane) {
+  auto op = [](float x, float y) { return MAX ? fmaxf(x, y) : x + y; };
+  int n = NC;
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) {
+    if (n > 1) {
+      n >>= 1;
+      const bool up = (lane & o) != 0;
+#pragma unroll
+      for (int k = 0; k < NC / 2; ++k) {
+        if (k < n) {
+          const float send = up ? v[k] : v[k + n], keep = up ? v[k + n] : v[k];
+          v[k] = op(keep, __shfl_xor_sync(0xffffffffu, send, o));
+        }
+      }
+    } else {
+      v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
+    }
+  }
+  return v[0];
+}
+
+// ---------------------------------------------------------------- unpacking
+// Eight codes (a word of the page) times their block's scale -> four 16-bit
+// pairs.  One conversion makes an fp16 pair of a byte's two codes; the product
+// with the scale, an fp16 number too, is exact in fp16 (2^-10 to 2688, six
+// significant bits) and, through fp32, in bf16.
+template <bool BF16>
+__device__ __forceinline__ void unpack8(uint32_t w, uint32_t mul, uint32_t (&out)[4]) {
+  uint32_t h[4];
+  // (as one block: the conversions then read the word's bytes in place; through
+  // cuda_fp4.h's byte arguments the same work takes three times the time)
+  asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %4;\n"
+      " cvt.rn.f16x2.e2m1x2 %0, a;\n cvt.rn.f16x2.e2m1x2 %1, b;\n"
+      " cvt.rn.f16x2.e2m1x2 %2, c;\n cvt.rn.f16x2.e2m1x2 %3, d;\n}\n"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (BF16) {
+      float lo, hi;
+      asm("{\n .reg .b16 a, b, c, d;\n mov.b32 {a, b}, %2;\n mov.b32 {c, d}, %3;\n"
+          " fma.rn.f32.f16 %0, a, c, 0f00000000;\n fma.rn.f32.f16 %1, b, d, 0f00000000;\n}\n"
+          : "=f"(lo), "=f"(hi)
+          : "r"(h[j]), "r"(mul));
+      out[j] = pack2<true>(lo, hi);
+    } else {
+      const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&h[j]), *reinterpret_cast<const __half2*>(&mul));
+      out[j] = *reinterpret_cast<const uint32_t*>(&r);
+    }
+  }
+}
+
+// fp16 pairs (s, s) of two block scales (E4M3 bytes); 0 for a token past the
+// end, whatever its bytes.
+__device__ __forceinline__ void multipliers(uint32_t s2, bool valid, uint32_t& m0, uint32_t& m1) {
+  uint32_t x;
+  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %1;\n cvt.rn.f16x2.e4m3x2 %0, a;\n}\n" : "=r"(x) : "r"(s2));
+  x = valid ? x : 0u;
+  m0 = __byte_perm(x, 0, 0x1010);
+  m1 = __byte_perm(x, 0, 0x3232);
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------- the kernel
+template <bool BF16, int N>
+__global__ void __launch_bounds__(kThreads4, 1)
+    mla_partial_fp4_kernel(const __grid_constant__ CUtensorMap tm_qlat, const __grid_constant__ CUtensorMap tm_qpe,
+                           const Fp4Params fp) {
+  using L = Smem4<N>;
+  constexpr int NP = L::kNP, NR = L::kNR;
+  constexpr float kThresh = 8.f;               // lazy rescale: weights stay below 2^8
+
+  // (the kernel has no static shared memory, so the block starts where the
+  // alignment puts it; the 128-byte swizzle needs 1024)
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + L::B_COUNT);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bar + L::B_COUNT + 1);
+  UnitTable* tab = reinterpret_cast<UnitTable*>(smem + L::kUnitOff);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int cid = blockIdx.x, ncta = gridDim.x;
+  int* err = fp.err;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bar[L::B_RAW_FULL + s], 1);
+      mbar_init(&bar[L::B_RAW_EMPTY + s], 8);
+      mbar_init(&bar[L::B_S_FULL + s], 1);
+      mbar_init(&bar[L::B_S_EMPTY + s], 8);
+    }
+    for (int s = 0; s < NP; ++s) {
+      mbar_init(&bar[L::B_PAIR_FULL + s], 2);
+      mbar_init(&bar[L::B_PAIR_EMPTY + s], 1);
+    }
+    for (int s = 0; s < NR; ++s) {
+      mbar_init(&bar[L::B_ROPE_FULL + s], 8);
+      mbar_init(&bar[L::B_ROPE_EMPTY + s], 1);
+    }
+    mbar_init(&bar[L::B_Q_FULL], 1);
+    mbar_init(&bar[L::B_Q_EMPTY], 1);
+    mbar_init(&bar[L::B_P_FULL], 8);
+    mbar_init(&bar[L::B_P_EMPTY], 1);
+    mbar_init(&bar[L::B_DONE_QK], 1);
+    mbar_init(&bar[L::B_DONE_PV], 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, L::kTmemCols);
+    tmem_relinquish();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&tm_qlat);
+    prefetch_tmap(&tm_qpe);
+  }
+  griddep_launch_dependents();   // the merge grid may be scheduled as CTAs retire; it waits for this one
+  const Range4 rng = partition4<N>(fp, reinterpret_cast<PartScratch*>(smem), cid, ncta);
+  {
+    const int n = rng.u_begin <= rng.u_last ? min(rng.u_last - rng.u_begin + 1, kUnits4) : 0;
+    if (static_cast<int>(threadIdx.x) < n) tab->u[threadIdx.x] = unit4<N>(fp, rng.u_begin + threadIdx.x);
+    if (threadIdx.x == 0) {
+      tab->first = rng.u_begin;
+      tab->n = n;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();   // barriers, TMEM address, table; the scratch is free
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const Waits waits{fp.spin_limit, abort_flag, err};
+
+  if (warp == 0) {
+    // ------------------------------------------------ producer
+    Iter4<N> it;
+    it.start(fp, tab, rng);
+    const int nbox = kTile4 / fp.box;
+    int rs = 0, qloads = 0;
+    // (the id of a lane's page is loaded one tile ahead)
+    auto fetch = [&](const Iter4<N>& t) {
+      if (!t.valid || t.ui.p == fp.S || lane >= nbox) return 0;
+      const int tk = min(t.tok0() + lane * fp.box, t.ui.hi - 1);
+      return __ldg(fp.block_table + static_cast<int64_t>(t.ui.b) * fp.max_blocks + (tk >> fp.bs_shift));
+    };
+    int id_cur = fetch(it);
+    while (it.valid) {
+      Iter4<N> nx = it;
+      nx.advance(fp);
+      const int id_next = fetch(nx);
+      if (it.ui.p != fp.S) {
+        const int st = rs & 1;
+        if (rs >= 2 && !__all_sync(0xffffffffu, waits.wait(&bar[L::B_RAW_EMPTY + st], ((rs >> 1) - 1) & 1))) break;
+        uint8_t* raw = smem + L::kRawOff + st * kRawStage;
+        if (lane == 0) mbar_arrive_expect_tx(&bar[L::B_RAW_FULL + st], kRawStage);
+        __syncwarp();
+        if (lane < nbox) {
+          int tk = it.tok0() + lane * fp.box;
+          const bool past = tk >= it.ui.hi;   // a box past the end reads the last one again (masked)
+          if (past) tk = it.ui.hi - 1;
+          int id = id_cur;
+          if (id < 0 || id >= fp.num_blocks) {
+            set_error(err, kDevBadBlockId);
+            id = 0;
+          }
+          int off = tk & (fp.bs - 1);
+          if (past) off &= ~(fp.box - 1);
+          const uint8_t* page = fp.kv_cache + (static_cast<int64_t>(id) << fp.bs_shift) * kE2m1Row;
+          bulk_load(raw + lane * fp.box * kE2m1Codes, page + off * kE2m1Codes, fp.box * kE2m1Codes,
+                    &bar[L::B_RAW_FULL + st]);
+          bulk_load(raw + kRawCodes + lane * fp.box * kE2m1Scales,
+                    page + fp.bs * kE2m1Codes + off * kE2m1Scales, fp.box * kE2m1Scales, &bar[L::B_RAW_FULL + st]);
+        }
+        ++rs;
+      }
+      if (it.first() && it.newq) {
+        if (it.nq >= 1 && !__all_sync(0xffffffffu, waits.wait(&bar[L::B_Q_EMPTY], (it.nq - 1) & 1))) break;
+        if (lane == 0) mbar_arrive_expect_tx(&bar[L::B_Q_FULL], L::kQ);
+        __syncwarp();
+        const int qrow = it.ui.b * fp.R + it.ui.g * N;
+        if (lane < 9)
+          tma_load_2d(smem + L::kQOff + lane * (N * 128), lane < 8 ? &tm_qlat : &tm_qpe, &bar[L::B_Q_FULL],
+                      lane < 8 ? lane * 64 : 0, qrow);
+        ++qloads;
+      }
+      id_cur = id_next;
+      it = nx;
+    }
+    if (lane == 0) {   // what was issued has landed before the CTA ends
+      for (int s = 0; s < 2 && s < rs; ++s) {
+        const int last = rs - 1 - ((rs - 1 - s) & 1);
+        mbar_wait(&bar[L::B_RAW_FULL + s], (last >> 1) & 1, err);
+      }
+      if (qloads > 0) mbar_wait(&bar[L::B_Q_FULL], (qloads - 1) & 1, err);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------ QK issuer: S^T = K Q^T
+    // The warp runs converged and one elected lane issues: the descriptors
+    // then live in uniform registers.  (Issued from a branch of one lane, an
+    // MMA of 16 rows cost 45 cycles of issue, against 25 of execution.)
+    const bool leader = elect_one();
+    constexpr uint32_t idesc = make_idesc_f16(64, N, BF16, false, false);
+    const uint32_t pair0 = smem_u32(smem + L::kPairOff), rope0 = smem_u32(smem + L::kRopeOff);
+    const uint32_t q0 = smem_u32(smem + L::kQOff);
+    auto wait = [&](uint64_t* b, uint32_t parity) { return __all_sync(0xffffffffu, waits.wait(b, parity)) != 0; };
+    Iter4<N> it;
+    it.start(fp, tab, rng);
+    int g = 0, pc = 0;
+    bool ok = true;
+    while (ok && it.valid) {
+      if (it.first() && it.newq && !wait(&bar[L::B_Q_FULL], it.nq & 1)) break;
+      const int sb = g & 1;
+      if (g >= 2 && !wait(&bar[L::B_S_EMPTY + sb], ((g >> 1) - 1) & 1)) break;
+      const uint32_t d = tmem + L::kTmemS + sb * N;
+      const int rsl = g % NR;
+      if (!wait(&bar[L::B_ROPE_FULL + rsl], (g / NR) & 1)) break;
+      tc_fence_after();
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+        if (leader)
+          umma_ss(d, make_desc_sw128(rope0 + rsl * kRope + kk * 32, 16, 1024),
+                  make_desc_sw128(q0 + 8 * (N * 128) + kk * 32, 16, 1024), idesc, kk ? 1u : 0u);
+      if (leader) umma_commit(&bar[L::B_ROPE_EMPTY + rsl]);
+      for (int p = 0; p < 4; ++p, ++pc) {
+        const int sl = pc % NP;
+        if (!wait(&bar[L::B_PAIR_FULL + sl], (pc / NP) & 1)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          if (leader)
+            umma_ss(d, make_desc_sw128(pair0 + sl * kPair + (kk >> 2) * kRope + (kk & 3) * 32, 16, 1024),
+                    make_desc_sw128(q0 + (2 * p + (kk >> 2)) * (N * 128) + (kk & 3) * 32, 16, 1024), idesc, 1u);
+      }
+      if (!ok) break;
+      const bool lastq = it.last_of_q(fp);
+      if (leader) {
+        umma_commit(&bar[L::B_S_FULL + sb]);
+        if (lastq) umma_commit(&bar[L::B_Q_EMPTY]);
+      }
+      it.advance(fp);
+      ++g;
+    }
+    if (leader) umma_commit(&bar[L::B_DONE_QK]);
+    __syncwarp();
+    mbar_wait(&bar[L::B_DONE_QK], 0, err);
+  } else if (warp == 2) {
+    // ------------------------------------------------ PV issuer: O^T += V^T P^T
+    const bool leader = elect_one();
+    constexpr uint32_t idesc = make_idesc_f16(128, N, BF16, true, true);
+    const uint32_t pair0 = smem_u32(smem + L::kPairOff), p0 = smem_u32(smem + L::kPOff);
+    auto wait = [&](uint64_t* b, uint32_t parity) { return __all_sync(0xffffffffu, waits.wait(b, parity)) != 0; };
+    Iter4<N> it;
+    it.start(fp, tab, rng);
+    int g = 0, pc = 0;
+    bool ok = true;
+    while (ok && it.valid) {
+      if (!wait(&bar[L::B_P_FULL], g & 1)) break;
+      const uint32_t fresh = it.first() ? 0u : 1u;
+      for (int p = 0; p < 4; ++p, ++pc) {
+        const int sl = pc % NP;
+        if (!wait(&bar[L::B_PAIR_FULL + sl], (pc / NP) & 1)) {   // (complete since this tile's QK)
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          if (leader)
+            umma_ss(tmem + L::kTmemO + p * N, make_desc_sw128(pair0 + sl * kPair + kk * 2048, kRope, 1024),
+                    desc_mn<N>(p0 + kk * (16 * N * 2)), idesc, kk ? 1u : fresh);
+        if (leader) umma_commit(&bar[L::B_PAIR_EMPTY + sl]);
+      }
+      if (!ok) break;
+      if (leader) umma_commit(&bar[L::B_P_EMPTY]);
+      it.advance(fp);
+      ++g;
+    }
+    if (leader) umma_commit(&bar[L::B_DONE_PV]);
+    __syncwarp();
+    mbar_wait(&bar[L::B_DONE_PV], 0, err);
+  } else if (warp == 3) {
+    // ------------------------------------------------ parts without tokens: o = 0, lse = -inf
+    for (int u = cid; u < fp.num_units; u += ncta) {
+      const Unit4 ui = unit4<N>(fp, u);
+      if (ui.hi > ui.lo) continue;
+      const int r1 = min(fp.R, (ui.g + 1) * N);
+      for (int r = ui.g * N; r < r1; ++r) {
+        const int64_t row = out_row4(fp, ui.b, r, ui.p);
+        if (lane == 0) fp.lse_part[row] = -INFINITY;
+        uint4* o = reinterpret_cast<uint4*>(static_cast<char*>(fp.o_part) + row * (fp.part_dtype == kFP32 ? 2048 : 1024));
+        for (int c = lane; c < (fp.part_dtype == kFP32 ? 128 : 64); c += 32) o[c] = make_uint4(0, 0, 0, 0);
+      }
+    }
+  } else if (warp < kUnpackWarp) {
+    // ------------------------------------------------ softmax, O rescale, epilogue
+    // Two groups of four warps, each with half of the rows (columns of S^T)
+    // and nothing shared between them.
+    constexpr int NG = N / 2, NC = N / 4;      // columns of a group, of a thread
+    constexpr int NO = NG < 16 ? NG : 16;      // columns of O at a time
+    const int grp = (warp - kSoftWarp) >> 2, wq = warp & 3;
+    const int gtid = threadIdx.x - kSoftWarp * 32 - grp * 128;
+    const int barid = 1 + grp;
+    const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
+    const int tok = wq * 16 + (lane & 15);     // token of the tile
+    const int c0 = grp * NG + (lane >> 4) * NC;   // first column of this thread
+    const int cr = (lane >> 4) * NC + (lane & 15) / (16 / NC);   // column (of the group) that col_reduce leaves here
+    uint8_t* sP = smem + L::kPOff;
+    float* s_m = reinterpret_cast<float*>(smem + L::kMOff) + grp * NG;
+    float* red = reinterpret_cast<float*>(smem + L::kRedOff) + grp * (4 * NG);   // [4][NG]
+    float l[NC], m[NC];
+#pragma unroll
+    for (int k = 0; k < NC; ++k) l[k] = m[k] = 0.f;
+    Iter4<N> it;
+    it.start(fp, tab, rng);
+    int g = 0;
+    bool ok = true;
+    while (it.valid) {
+      const Unit4 ui = it.ui;
+      const int sb = g & 1;
+      const bool cur = ui.p == fp.S, first = it.first();
+      const float sl = cur ? fp.scale_log2 : fp.scale_log2 * fp.kv_scale;
+      // columns below nmin are masked for this thread's token: all of a token
+      // past the end; in the CURRENT part the rows of earlier query tokens
+      int nmin = N;
+      if (it.tok0() + tok < ui.hi) nmin = cur ? min(N, max(0, tok * fp.H - ui.g * N)) : 0;
+      nmin -= c0;
+      ok = ok && waits.lazy(&bar[L::B_S_FULL + sb], (g >> 1) & 1);
+      __syncwarp();
+      tc_fence_after();
+      uint32_t v[NC];
+      tmem_half(tmem + lanes + L::kTmemS + sb * N + grp * NG, v);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar[L::B_S_EMPTY + sb]);
+      // scores in the log2 domain, relative to the reference maximum
+      float x[NC];
+      float top = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < NC; ++k) {
+        x[k] = k >= nmin ? __uint_as_float(v[k]) * sl : -INFINITY;
+        top = fmaxf(top, x[k] - m[k]);
+      }
+      // does every score stay below the reference maximum + 8?
+      if (!named_bar_and(barid, 128, ok && !first && top <= kThresh)) {
+        if (!named_bar_and(barid, 128, ok)) break;
+        // ---- new reference maxima: each row's maximum over the tile's tokens
+        float y[NC];
+#pragma unroll
+        for (int k = 0; k < NC; ++k) y[k] = x[k];
+        const float mx = col_reduce<NC, true>(y, lane);
+        red[wq * NG + cr] = mx;
+        named_bar_sync(barid, 128);
+        float a[NC];
+#pragma unroll
+        for (int k = 0; k < NC; ++k) {
+          const float* r = red + (c0 - grp * NG) + k;
+          const float t = fmaxf(fmaxf(r[0], r[NG]), fmaxf(r[2 * NG], r[3 * NG]));
+          a[k] = 1.f;
+          if (first) {
+            m[k] = t == -INFINITY ? 0.f : t;
+            l[k] = 0.f;
+          } else if (t > m[k] + kThresh) {
+            a[k] = fast_exp2(m[k] - t);
+            m[k] = t;
+            l[k] *= a[k];
+          }
+        }
+        named_bar_sync(barid, 128);   // red has been read
+        if (wq == 0 && (lane & 15) == 0) {
+#pragma unroll
+          for (int k = 0; k < NC; ++k) {
+            s_m[c0 - grp * NG + k] = m[k];
+            red[c0 - grp * NG + k] = a[k];
+          }
+        }
+        if (!first) {
+          // O *= alpha, once the PV product of the tile before is done
+          if (g >= 1) ok = waits.lazy(&bar[L::B_P_EMPTY], (g - 1) & 1);
+          if (!named_bar_and(barid, 128, ok)) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < 4 * NG; c += NO) {
+            uint32_t o[NO];
+            const uint32_t oa = tmem + lanes + L::kTmemO + (c / NG) * N + grp * NG + c % NG;
+            tmem_get(oa, o);
+#pragma unroll
+            for (int k = 0; k < NO; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * red[c % NG + k]);
+            tmem_put(oa, o);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+        }
+        named_bar_sync(barid, 128);   // alpha has been read
+      }
+      // ---- weights, row sums, P^T
+      uint32_t pk[NC / 2];
+#pragma unroll
+      for (int k = 0; k < NC; k += 2) {
+        const float p = fast_exp2(x[k] - m[k]), q = fast_exp2(x[k + 1] - m[k + 1]);   // masked: exp2(-inf) = 0
+        l[k] += p;
+        l[k + 1] += q;
+        pk[k / 2] = pack2<BF16>(p, q);
+      }
+      if (g >= 1) ok = ok && waits.lazy(&bar[L::B_P_EMPTY], (g - 1) & 1);
+      ok = __all_sync(0xffffffffu, ok);
+      if (ok) {
+        if constexpr (NC == 4) {
+          *reinterpret_cast<uint2*>(sP + p_offset<N>(tok, c0 / 8) + (c0 & 4) * 2) = make_uint2(pk[0], pk[1]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < NC / 8; ++k)
+            *reinterpret_cast<uint4*>(sP + p_offset<N>(tok, c0 / 8 + k)) =
+                make_uint4(pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar[L::B_P_FULL]);
+      }
+      if (it.last()) {
+        // ---- epilogue of the piece: row sums over the tokens, O / l, LSE
+        ok = ok && waits.lazy(&bar[L::B_P_EMPTY], g & 1);
+        if (!named_bar_and(barid, 128, ok)) break;
+        tc_fence_after();
+        const float part = col_reduce<NC, false>(l, lane);
+        red[wq * NG + cr] = part;
+        named_bar_sync(barid, 128);
+        const bool whole = it.whole();
+        const int slot = 2 * cid + (it.u == rng.u_begin ? 0 : 1);
+        // lane k has row k of the group
+        float inv = 0.f;
+        int64_t dst = -1;
+        if (lane < NG) {
+          const float sum = (red[lane] + red[NG + lane]) + (red[2 * NG + lane] + red[3 * NG + lane]);
+          const float lse2 = s_m[lane] + log2f(sum);
+          inv = (cur ? 1.f : fp.kv_scale) / sum;
+          const int n = grp * NG + lane, r = ui.g * N + n;
+          if (r < fp.R) {
+            dst = whole ? out_row4(fp, ui.b, r, ui.p) : static_cast<int64_t>(slot) * N + n;
+            if (wq == 0) {
+              if (whole) fp.lse_part[dst] = lse2 * kLn2;
+              else fp.ws_lse[dst] = lse2;
+            }
+          }
+        }
+        char* out = static_cast<char*>(whole ? fp.o_part : fp.ws_o);
+        const bool odd = (lane & 1) != 0;
+#pragma unroll 1
+        for (int c = 0; c < 4 * NG; c += NO) {
+          uint32_t o[NO];
+          const int n0 = c % NG;
+          tmem_get(tmem + lanes + L::kTmemO + (c / NG) * N + grp * NG + n0, o);
+          const int lat = (c / NG) * 128 + wq * 32 + lane;
+#pragma unroll
+          for (int k = 0; k < NO; k += 2) {
+            const float f0 = __uint_as_float(o[k]) * __shfl_sync(0xffffffffu, inv, n0 + k);
+            const float f1 = __uint_as_float(o[k + 1]) * __shfl_sync(0xffffffffu, inv, n0 + k + 1);
+            const int64_t d0 = __shfl_sync(0xffffffffu, dst, n0 + k), d1 = __shfl_sync(0xffffffffu, dst, n0 + k + 1);
+            if (fp.part_dtype == kFP32) {
+              if (d0 >= 0) reinterpret_cast<float*>(out)[d0 * 512 + lat] = f0;
+              if (d1 >= 0) reinterpret_cast<float*>(out)[d1 * 512 + lat] = f1;
+            } else {
+              // two rows at a time: an even lane takes its neighbour's value
+              // of the first row, an odd lane that of the second: 4 bytes a store
+              const float got = __shfl_xor_sync(0xffffffffu, odd ? f0 : f1, 1);
+              const uint32_t w = odd ? pack2_dt(got, f1, fp.part_dtype) : pack2_dt(f0, got, fp.part_dtype);
+              const int64_t d = odd ? d1 : d0;
+              if (d >= 0) *reinterpret_cast<uint32_t*>(out + (d * 512 + (lat & ~1)) * 2) = w;
+            }
+          }
+        }
+        tc_fence_before();
+        named_bar_sync(barid, 128);   // red and s_m have been read
+      }
+      it.advance(fp);
+      ++g;
+    }
+  } else {
+    // ------------------------------------------------ unpacking
+    // Two warps a pair, one lane a token: its 128 columns and 16 of the RoPE
+    // columns, one fence and one arrival a tile.
+    const int w = warp - kUnpackWarp;
+    const int t = (w & 1) * 32 + lane, p = w >> 1;
+    uint8_t* rope0 = smem + L::kRopeOff;
+    uint8_t* pair0 = smem + L::kPairOff;
+    Iter4<N> it;
+    it.start(fp, tab, rng);
+    int g = 0, rs = 0;
+    while (it.valid) {
+      const bool cur = it.ui.p == fp.S;
+      const bool valid = it.tok0() + t < it.ui.hi;
+      uint4 c[4] = {}, rc = make_uint4(0, 0, 0, 0);
+      uint32_t sc[2] = {0, 0}, rsc = 0;
+      const uint4* row = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(fp.kv_cur) +
+                                                        (static_cast<int64_t>(it.ui.b) * fp.q_len + t) * 576);
+      if (!cur) {
+        const int st = rs & 1;
+        if (!__all_sync(0xffffffffu, waits.wait(&bar[L::B_RAW_FULL + st], (rs >> 1) & 1))) break;
+        const uint8_t* codes = smem + L::kRawOff + st * kRawStage + t * kE2m1Codes;
+        const uint8_t* scales = smem + L::kRawOff + st * kRawStage + kRawCodes + t * kE2m1Scales;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) c[q] = *reinterpret_cast<const uint4*>(codes + p * 64 + q * 16);
+        sc[0] = *reinterpret_cast<const uint32_t*>(scales + p * 8);
+        sc[1] = *reinterpret_cast<const uint32_t*>(scales + p * 8 + 4);
+        const uint2 r2 = *reinterpret_cast<const uint2*>(codes + 256 + p * 8);
+        rc.x = r2.x;
+        rc.y = r2.y;
+        rsc = scales[32 + p];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar[L::B_RAW_EMPTY + st]);
+        ++rs;
+      }
+      const int pc = g * 4 + p, sl = pc % NP, rsl = g % NR;
+      if (pc >= NP && !__all_sync(0xffffffffu, waits.wait(&bar[L::B_PAIR_EMPTY + sl], ((pc / NP) - 1) & 1))) break;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint4 x[4];
+        if (cur) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) x[k] = valid ? row[p * 16 + q * 4 + k] : make_uint4(0, 0, 0, 0);
+        } else {
+          uint32_t m0, m1, a[4];
+          multipliers(sc[q >> 1] >> ((q & 1) * 16), valid, m0, m1);
+          unpack8<BF16>(c[q].x, m0, a);
+          x[0] = make_uint4(a[0], a[1], a[2], a[3]);
+          unpack8<BF16>(c[q].y, m0, a);
+          x[1] = make_uint4(a[0], a[1], a[2], a[3]);
+          unpack8<BF16>(c[q].z, m1, a);
+          x[2] = make_uint4(a[0], a[1], a[2], a[3]);
+          unpack8<BF16>(c[q].w, m1, a);
+          x[3] = make_uint4(a[0], a[1], a[2], a[3]);
+        }
+        uint8_t* d = pair0 + sl * kPair + (q >> 1) * kRope;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4*>(d + sw128_offset(t, (q & 1) * 4 + k)) = x[k];
+      }
+      if (g >= NR && !__all_sync(0xffffffffu, waits.wait(&bar[L::B_ROPE_EMPTY + rsl], ((g / NR) - 1) & 1))) break;
+      {
+        uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0;
+        if (cur) {
+          if (valid) {
+            x0 = row[64 + 2 * p];
+            x1 = row[64 + 2 * p + 1];
+          }
+        } else {
+          uint32_t m0, m1, a[4];
+          multipliers(rsc, valid, m0, m1);
+          unpack8<BF16>(rc.x, m0, a);
+          x0 = make_uint4(a[0], a[1], a[2], a[3]);
+          unpack8<BF16>(rc.y, m0, a);
+          x1 = make_uint4(a[0], a[1], a[2], a[3]);
+        }
+        uint8_t* d = rope0 + rsl * kRope;
+        *reinterpret_cast<uint4*>(d + sw128_offset(t, 2 * p)) = x0;
+        *reinterpret_cast<uint4*>(d + sw128_offset(t, 2 * p + 1)) = x1;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&bar[L::B_PAIR_FULL + sl]);
+        mbar_arrive(&bar[L::B_ROPE_FULL + rsl]);
+      }
+      it.advance(fp);
+      ++g;
+    }
+  }
+
+  __syncwarp();
+  tmem_wait_st();
+  tmem_wait_ld();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tmem_dealloc(tmem, L::kTmemCols);
+  }
+}
+
+// ---------------------------------------------------------------- merge of cut units
+// One block per (CTA, 32 rows): merges the pieces of the cut unit whose last
+// tile that CTA held by their LSEs, eight threads a row (64 columns each).
+__global__ void __launch_bounds__(256, 2) mla_partial_fp4_merge_kernel(const Fp4Params fp, int rows) {
+  griddep_wait();
+  const int4 rec = fp.ws_units[blockIdx.x];
+  const int u = rec.x;
+  const int n = blockIdx.y * 32 + (threadIdx.x >> 3);
+  if (u < 0 || n >= rows) return;
+  const int p = u % fp.P, gb = u / fp.P, b = gb % fp.B, r = (gb / fp.B) * rows + n;
+  if (r >= fp.R) return;
+  const int sub = threadIdx.x & 7;
+  const bool f32 = fp.part_dtype == kFP32;
+  float acc[64];
+#pragma unroll
+  for (int t = 0; t < 64; ++t) acc[t] = 0.f;
+  float m = -INFINITY, wsum = 0.f;
+  for (int c = rec.z; c <= rec.w; ++c) {
+    const int s0 = fp.ws_bounds[c], s1 = fp.ws_bounds[c + 1];
+    if (s1 <= s0) continue;                             // CTA without tiles
+    const int64_t row = static_cast<int64_t>(2 * c + (s0 >= rec.y ? 0 : 1)) * rows + n;   // its first or last piece
+    const float l = fp.ws_lse[row];
+    if (l > m) {
+      const float sc = exp2f(m - l);
+#pragma unroll
+      for (int t = 0; t < 64; ++t) acc[t] *= sc;
+      wsum *= sc;
+      m = l;
+    }
+    const float w = l == m ? 1.f : exp2f(l - m);
+    wsum += w;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int64_t e0 = row * 512 + sub * 64 + 32 * half;
+      float x[32];
+      if (f32) {
+        const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(fp.ws_o) + e0);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float4 f = src[k];
+          x[4 * k] = f.x;
+          x[4 * k + 1] = f.y;
+          x[4 * k + 2] = f.z;
+          x[4 * k + 3] = f.w;
+        }
+      } else {
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(fp.ws_o) + e0);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint4 h = src[k];
+          const uint32_t hw[4] = {h.x, h.y, h.z, h.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 f2 = unpack2(hw[j], fp.part_dtype);
+            x[8 * k + 2 * j] = f2.x;
+            x[8 * k + 2 * j + 1] = f2.y;
+          }
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < 32; ++t) acc[32 * half + t] = fmaf(w, x[t], acc[32 * half + t]);
+    }
+  }
+  const float inv = 1.f / wsum;
+  const int64_t row = out_row4(fp, b, r, p);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t v[32];
+#pragma unroll
+    for (int t = 0; t < 32; ++t) v[t] = __float_as_uint(acc[32 * h + t]);
+    store_row32(fp.o_part, row * 512 + sub * 64 + 32 * h, v, inv, fp.part_dtype);
+  }
+  if (sub == 0) fp.lse_part[row] = (m + log2f(wsum)) * kLn2;
+}
+
+// ---------------------------------------------------------------- launcher
+template <bool BF16, int N>
+static bool prepare4(int dev) {
+  static bool done[64] = {false};
+  static std::mutex mu;
+  std::lock_guard<std::mutex> lock(mu);
+  if (!done[dev]) {
+    if (cudaFuncSetAttribute(mla_partial_fp4_kernel<BF16, N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Smem4<N>::kTotal) != cudaSuccess)
+      return false;
+    done[dev] = true;
+  }
+  return true;
+}
+
+int fp4_max_ctas() {
+  static int cache[64] = {0};
+  static std::mutex mu;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return -1;
+  std::lock_guard<std::mutex> lock(mu);
+  if (cache[dev] == 0) {
+    int n = 0;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return -1;
+    cache[dev] = std::min(n, kFp4MaxCtas);
+  }
+  return cache[dev];
+}
+
+template <bool BF16, int N>
+static int launch4(const CUtensorMap& qlat, const CUtensorMap& qpe, const Fp4Params& fp, cudaStream_t stream) {
+  int dev = 0;
+  const int most = fp4_max_ctas();
+  if (most < 1 || cudaGetDevice(&dev) != cudaSuccess || !prepare4<BF16, N>(dev)) return -1;
+  const int ctas = fp.split ? fp.split : std::max(1, std::min(fp.num_units, most));
+  mla_partial_fp4_kernel<BF16, N><<<ctas, kThreads4, Smem4<N>::kTotal, stream>>>(qlat, qpe, fp);
+  if (!fp.split) return 0;
+  if (cudaPeekAtLastError() != cudaSuccess) return -1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas, (N + 31) / 32, 1);
+  cfg.blockDim = dim3(256, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, mla_partial_fp4_merge_kernel, fp, N) != cudaSuccess ? -1 : 0;
+}
+
+int launch_partial_fp4(const CUtensorMap& qlat, const CUtensorMap& qpe, const Fp4Params& fp, int rows,
+                       bool bf16, cudaStream_t stream) {
+  if (rows == 16) return bf16 ? launch4<true, 16>(qlat, qpe, fp, stream) : launch4<false, 16>(qlat, qpe, fp, stream);
+  if (rows == 32) return bf16 ? launch4<true, 32>(qlat, qpe, fp, stream) : launch4<false, 32>(qlat, qpe, fp, stream);
+  return bf16 ? launch4<true, 64>(qlat, qpe, fp, stream) : launch4<false, 64>(qlat, qpe, fp, stream);
 }
 
 }  // namespace mla
