@@ -30,8 +30,8 @@
 //           epilogue (thread = latent)
 //   w12-19  unpacking: codes and scales to 128-byte-swizzled 16-bit chunks
 // A tile's 576 columns are unpacked as one RoPE chunk (64) and four latent
-// pairs (128 each, one M block of the PV product), through a ring of pair
-// slots: a slot is free when its PV MMAs are done.
+// pairs (128 each, one M block of the PV product), in two tile buffers (one for
+// 64 rows, whose queries take 72 KB); a buffer is free when its PV MMAs are done.
 //
 // The softmax keeps its reference maximum per row in shared memory and tests
 // each tile against it; only a tile that exceeds it by 2^8 (and the first of a
@@ -64,12 +64,14 @@ struct Unit4 {
 
 template <int N>
 struct Smem4 {
-  static constexpr int kNP = N == 64 ? 6 : 8;    // pair slots (a tile takes four)
-  static constexpr int kNR = N == 64 ? 1 : 2;    // RoPE slots
+  static constexpr int kNT = N == 64 ? 1 : 2;    // tile buffers
+  static __device__ __forceinline__ int buffer(int g) { return g % kNT; }
+  static __device__ __forceinline__ uint32_t phase(int g) { return (g / kNT) & 1; }
+  static __device__ __forceinline__ int pair_slot(int g, int p) { return (g % kNT) * 4 + p; }
   static constexpr int kQ = N * 128 * 9;
   static constexpr int kPairOff = 0;
-  static constexpr int kRopeOff = kPairOff + kNP * kPair;
-  static constexpr int kQOff = kRopeOff + kNR * kRope;
+  static constexpr int kRopeOff = kPairOff + kNT * 4 * kPair;
+  static constexpr int kQOff = kRopeOff + kNT * kRope;
   static constexpr int kPOff = kQOff + kQ;
   static constexpr int kP = kTile4 * N * 2;
   static constexpr int kRawOff = kPOff + kP;
@@ -81,11 +83,9 @@ struct Smem4 {
   enum : int {
     B_RAW_FULL = 0,
     B_RAW_EMPTY = 2,
-    B_PAIR_FULL = 4,
-    B_PAIR_EMPTY = B_PAIR_FULL + kNP,
-    B_ROPE_FULL = B_PAIR_EMPTY + kNP,
-    B_ROPE_EMPTY = B_ROPE_FULL + kNR,
-    B_Q_FULL = B_ROPE_EMPTY + kNR,
+    B_FULL = 4,
+    B_EMPTY = B_FULL + kNT,
+    B_Q_FULL = B_EMPTY + kNT,
     B_Q_EMPTY,
     B_S_FULL,
     B_S_EMPTY = B_S_FULL + 2,
@@ -190,17 +190,14 @@ struct Iter4 {
     }
     valid = false;
   }
+  __device__ __forceinline__ void next_piece(const Fp4Params& fp) {
+    j = jend - 1;
+    advance(fp);
+  }
   __device__ __forceinline__ bool first() const { return j == jfirst; }
   __device__ __forceinline__ bool last() const { return j == jend - 1; }
   __device__ __forceinline__ bool whole() const { return jfirst == 0 && jend == tiles4(ui); }
   __device__ __forceinline__ int tok0() const { return ui.lo + j * kTile4; }
-  // whether the next tile (if any) reads another query
-  __device__ __forceinline__ bool last_of_q(const Fp4Params& fp) const {
-    if (!last()) return false;
-    Iter4 n = *this;
-    n.advance(fp);
-    return !n.valid || n.newq;
-  }
 };
 
 // ---------------------------------------------------------------- partition
@@ -514,7 +511,6 @@ __global__ void __launch_bounds__(kThreads4, 1)
     mla_partial_fp4_kernel(const __grid_constant__ CUtensorMap tm_qlat, const __grid_constant__ CUtensorMap tm_qpe,
                            const Fp4Params fp) {
   using L = Smem4<N>;
-  constexpr int NP = L::kNP, NR = L::kNR;
   constexpr float kThresh = 8.f;               // lazy rescale: weights stay below 2^8
 
   // (the kernel has no static shared memory, so the block starts where the
@@ -535,13 +531,9 @@ __global__ void __launch_bounds__(kThreads4, 1)
       mbar_init(&bar[L::B_S_FULL + s], 1);
       mbar_init(&bar[L::B_S_EMPTY + s], 8);
     }
-    for (int s = 0; s < NP; ++s) {
-      mbar_init(&bar[L::B_PAIR_FULL + s], 2);
-      mbar_init(&bar[L::B_PAIR_EMPTY + s], 1);
-    }
-    for (int s = 0; s < NR; ++s) {
-      mbar_init(&bar[L::B_ROPE_FULL + s], 8);
-      mbar_init(&bar[L::B_ROPE_EMPTY + s], 1);
+    for (int s = 0; s < L::kNT; ++s) {
+      mbar_init(&bar[L::B_FULL + s], 8);
+      mbar_init(&bar[L::B_EMPTY + s], 1);
     }
     mbar_init(&bar[L::B_Q_FULL], 1);
     mbar_init(&bar[L::B_Q_EMPTY], 1);
@@ -642,51 +634,53 @@ __global__ void __launch_bounds__(kThreads4, 1)
     // ------------------------------------------------ QK issuer: S^T = K Q^T
     // The warp runs converged and one elected lane issues: the descriptors
     // then live in uniform registers.  (Issued from a branch of one lane, an
-    // MMA of 16 rows cost 45 cycles of issue, against 25 of execution.)
+    // MMA of 16 rows cost 45 cycles of issue, against 25 of execution.)  What
+    // changes at a unit's end is worked out once per piece, not per tile.
     const bool leader = elect_one();
     constexpr uint32_t idesc = make_idesc_f16(64, N, BF16, false, false);
-    const uint32_t pair0 = smem_u32(smem + L::kPairOff), rope0 = smem_u32(smem + L::kRopeOff);
-    const uint32_t q0 = smem_u32(smem + L::kQOff);
+    const uint64_t a0 = make_desc_sw128(smem_u32(smem + L::kPairOff), 16, 1024);
+    const uint64_t r0 = make_desc_sw128(smem_u32(smem + L::kRopeOff), 16, 1024);
+    const uint64_t q0 = make_desc_sw128(smem_u32(smem + L::kQOff), 16, 1024);
     auto wait = [&](uint64_t* b, uint32_t parity) { return __all_sync(0xffffffffu, waits.wait(b, parity)) != 0; };
     Iter4<N> it;
     it.start(fp, tab, rng);
-    int g = 0, pc = 0;
+    int g = 0;
     bool ok = true;
     while (ok && it.valid) {
-      if (it.first() && it.newq && !wait(&bar[L::B_Q_FULL], it.nq & 1)) break;
-      const int sb = g & 1;
-      if (g >= 2 && !wait(&bar[L::B_S_EMPTY + sb], ((g >> 1) - 1) & 1)) break;
-      const uint32_t d = tmem + L::kTmemS + sb * N;
-      const int rsl = g % NR;
-      if (!wait(&bar[L::B_ROPE_FULL + rsl], (g / NR) & 1)) break;
-      tc_fence_after();
-#pragma unroll
-      for (int kk = 0; kk < 4; ++kk)
-        if (leader)
-          umma_ss(d, make_desc_sw128(rope0 + rsl * kRope + kk * 32, 16, 1024),
-                  make_desc_sw128(q0 + 8 * (N * 128) + kk * 32, 16, 1024), idesc, kk ? 1u : 0u);
-      if (leader) umma_commit(&bar[L::B_ROPE_EMPTY + rsl]);
-      for (int p = 0; p < 4; ++p, ++pc) {
-        const int sl = pc % NP;
-        if (!wait(&bar[L::B_PAIR_FULL + sl], (pc / NP) & 1)) {
+      const int n = it.jend - it.j;
+      if (it.newq && !wait(&bar[L::B_Q_FULL], it.nq & 1)) break;
+      it.next_piece(fp);
+      const bool lastq = !it.valid || it.newq;
+      for (int k = 0; k < n; ++k, ++g) {
+        const int sb = g & 1;
+        if (g >= 2 && !wait(&bar[L::B_S_EMPTY + sb], ((g >> 1) - 1) & 1)) {
+          ok = false;
+          break;
+        }
+        const uint32_t d = tmem + L::kTmemS + sb * N;
+        const int tb = L::buffer(g);
+        if (!wait(&bar[L::B_FULL + tb], L::phase(g))) {
           ok = false;
           break;
         }
         tc_fence_after();
+        const uint64_t a = a0 + L::pair_slot(g, 0) * (kPair >> 4), r = r0 + tb * (kRope >> 4);
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          if (leader)
-            umma_ss(d, make_desc_sw128(pair0 + sl * kPair + (kk >> 2) * kRope + (kk & 3) * 32, 16, 1024),
-                    make_desc_sw128(q0 + (2 * p + (kk >> 2)) * (N * 128) + (kk & 3) * 32, 16, 1024), idesc, 1u);
+        for (int kk = 0; kk < 4; ++kk)
+          if (leader) umma_ss(d, r + kk * 2, q0 + 8 * (N * 8) + kk * 2, idesc, kk ? 1u : 0u);
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            if (leader)
+              umma_ss(d, a + p * (kPair >> 4) + (kk >> 2) * (kRope >> 4) + (kk & 3) * 2,
+                      q0 + (2 * p + (kk >> 2)) * (N * 8) + (kk & 3) * 2, idesc, 1u);
+        }
+        if (leader) {
+          umma_commit(&bar[L::B_S_FULL + sb]);
+          if (lastq && k == n - 1) umma_commit(&bar[L::B_Q_EMPTY]);
+        }
       }
-      if (!ok) break;
-      const bool lastq = it.last_of_q(fp);
-      if (leader) {
-        umma_commit(&bar[L::B_S_FULL + sb]);
-        if (lastq) umma_commit(&bar[L::B_Q_EMPTY]);
-      }
-      it.advance(fp);
-      ++g;
     }
     if (leader) umma_commit(&bar[L::B_DONE_QK]);
     __syncwarp();
@@ -695,33 +689,37 @@ __global__ void __launch_bounds__(kThreads4, 1)
     // ------------------------------------------------ PV issuer: O^T += V^T P^T
     const bool leader = elect_one();
     constexpr uint32_t idesc = make_idesc_f16(128, N, BF16, true, true);
-    const uint32_t pair0 = smem_u32(smem + L::kPairOff), p0 = smem_u32(smem + L::kPOff);
+    const uint64_t v0 = make_desc_sw128(smem_u32(smem + L::kPairOff), kRope, 1024);
+    const uint64_t p0 = desc_mn<N>(smem_u32(smem + L::kPOff));
     auto wait = [&](uint64_t* b, uint32_t parity) { return __all_sync(0xffffffffu, waits.wait(b, parity)) != 0; };
     Iter4<N> it;
     it.start(fp, tab, rng);
-    int g = 0, pc = 0;
+    int g = 0;
     bool ok = true;
     while (ok && it.valid) {
-      if (!wait(&bar[L::B_P_FULL], g & 1)) break;
-      const uint32_t fresh = it.first() ? 0u : 1u;
-      for (int p = 0; p < 4; ++p, ++pc) {
-        const int sl = pc % NP;
-        if (!wait(&bar[L::B_PAIR_FULL + sl], (pc / NP) & 1)) {   // (complete since this tile's QK)
+      const int n = it.jend - it.j;
+      for (int k = 0; k < n; ++k, ++g) {
+        if (!wait(&bar[L::B_P_FULL], g & 1)) {
           ok = false;
           break;
         }
         tc_fence_after();
+        const uint32_t more = k > 0 ? 1u : 0u;
+        const uint64_t v = v0 + L::pair_slot(g, 0) * (kPair >> 4);
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          if (leader)
-            umma_ss(tmem + L::kTmemO + p * N, make_desc_sw128(pair0 + sl * kPair + kk * 2048, kRope, 1024),
-                    desc_mn<N>(p0 + kk * (16 * N * 2)), idesc, kk ? 1u : fresh);
-        if (leader) umma_commit(&bar[L::B_PAIR_EMPTY + sl]);
+        for (int p = 0; p < 4; ++p) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            if (leader)
+              umma_ss(tmem + L::kTmemO + p * N, v + p * (kPair >> 4) + kk * 128, p0 + kk * (N * 2), idesc,
+                      kk ? 1u : more);
+        }
+        if (leader) {
+          umma_commit(&bar[L::B_EMPTY + L::buffer(g)]);
+          umma_commit(&bar[L::B_P_EMPTY]);
+        }
       }
-      if (!ok) break;
-      if (leader) umma_commit(&bar[L::B_P_EMPTY]);
-      it.advance(fp);
-      ++g;
+      it.next_piece(fp);
     }
     if (leader) umma_commit(&bar[L::B_DONE_PV]);
     __syncwarp();
@@ -957,8 +955,8 @@ __global__ void __launch_bounds__(kThreads4, 1)
         if (lane == 0) mbar_arrive(&bar[L::B_RAW_EMPTY + st]);
         ++rs;
       }
-      const int pc = g * 4 + p, sl = pc % NP, rsl = g % NR;
-      if (pc >= NP && !__all_sync(0xffffffffu, waits.wait(&bar[L::B_PAIR_EMPTY + sl], ((pc / NP) - 1) & 1))) break;
+      const int tb = L::buffer(g);
+      if (g >= L::kNT && !__all_sync(0xffffffffu, waits.wait(&bar[L::B_EMPTY + tb], L::phase(g) ^ 1))) break;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         uint4 x[4];
@@ -977,11 +975,10 @@ __global__ void __launch_bounds__(kThreads4, 1)
           unpack8<BF16>(c[q].w, m1, a);
           x[3] = make_uint4(a[0], a[1], a[2], a[3]);
         }
-        uint8_t* d = pair0 + sl * kPair + (q >> 1) * kRope;
+        uint8_t* d = pair0 + L::pair_slot(g, p) * kPair + (q >> 1) * kRope;
 #pragma unroll
         for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4*>(d + sw128_offset(t, (q & 1) * 4 + k)) = x[k];
       }
-      if (g >= NR && !__all_sync(0xffffffffu, waits.wait(&bar[L::B_ROPE_EMPTY + rsl], ((g / NR) - 1) & 1))) break;
       {
         uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0;
         if (cur) {
@@ -997,16 +994,13 @@ __global__ void __launch_bounds__(kThreads4, 1)
           unpack8<BF16>(rc.y, m0, a);
           x1 = make_uint4(a[0], a[1], a[2], a[3]);
         }
-        uint8_t* d = rope0 + rsl * kRope;
+        uint8_t* d = rope0 + tb * kRope;
         *reinterpret_cast<uint4*>(d + sw128_offset(t, 2 * p)) = x0;
         *reinterpret_cast<uint4*>(d + sw128_offset(t, 2 * p + 1)) = x1;
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&bar[L::B_PAIR_FULL + sl]);
-        mbar_arrive(&bar[L::B_ROPE_FULL + rsl]);
-      }
+      if (lane == 0) mbar_arrive(&bar[L::B_FULL + tb]);
       it.advance(fp);
       ++g;
     }
