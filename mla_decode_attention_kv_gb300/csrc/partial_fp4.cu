@@ -21,17 +21,19 @@
 // x rows columns of tensor memory, at most half of it, so one CTA holds all of
 // a unit, and several query tokens' rows share one pass over the history.
 //
-// One persistent CTA per SM, 640 threads:
+// One persistent CTA per SM, 896 threads (640 for 64 rows, whose softmax takes
+// more registers a thread):
 //   w0      producer: raw pages (codes, scales) by bulk copies, queries by TMA
 //   w1      QK issuer            w2  PV issuer           w3  empty parts
 //   w4-11   softmax: two groups of four warps with half of the rows each; a
 //           token (16 TMEM lanes a warp in an M = 64 accumulator) has two
 //           threads of a group, one for each half of its rows.  O rescale and
 //           epilogue (thread = latent)
-//   w12-19  unpacking: codes and scales to 128-byte-swizzled 16-bit chunks
-// A tile's 576 columns are unpacked as one RoPE chunk (64) and four latent
-// pairs (128 each, one M block of the PV product), in two tile buffers (one for
-// 64 rows, whose queries take 72 KB); a buffer is free when its PV MMAs are done.
+//   w12-    unpacking: codes and scales to 128-byte-swizzled 16-bit chunks
+// A tile's 512 latents are unpacked as two halves through a ring of half slots
+// (two tiles; one and a half for 64 rows, whose queries take 72 KB), its RoPE
+// columns with the second: the QK MMAs of a half start while the other is
+// unpacked, and a slot is free when its PV MMAs are done.
 //
 // The softmax keeps its reference maximum per row in shared memory and tests
 // each tile against it; only a tile that exceeds it by 2^8 (and the first of a
@@ -50,12 +52,11 @@ namespace mla {
 namespace {
 
 constexpr int kTile4 = 64;                       // tokens
-constexpr int kThreads4 = 640;
 constexpr int kSoftWarp = 4, kUnpackWarp = 12;   // first warp of the softmax and of the unpacking
 constexpr int kRawCodes = kTile4 * kE2m1Codes;   // 18432
 constexpr int kRawStage = kTile4 * kE2m1Row;     // 20736
-constexpr int kPair = 2 * kTile4 * 128;          // 16 KB: 128 latents of a tile
-constexpr int kRope = kTile4 * 128;              // 8 KB
+constexpr int kChunk = kTile4 * 128;             // 8 KB: 64 columns of a tile
+constexpr int kHalf = 4 * kChunk;                // 32 KB: 256 latents of a tile, two M blocks of the PV product
 constexpr int kUnits4 = 8;                       // units whose geometry is kept in shared memory
 
 struct Unit4 {
@@ -64,14 +65,14 @@ struct Unit4 {
 
 template <int N>
 struct Smem4 {
-  static constexpr int kNT = N == 64 ? 1 : 2;    // tile buffers
-  static __device__ __forceinline__ int buffer(int g) { return g % kNT; }
-  static __device__ __forceinline__ uint32_t phase(int g) { return (g / kNT) & 1; }
-  static __device__ __forceinline__ int pair_slot(int g, int p) { return (g % kNT) * 4 + p; }
+  static constexpr int kNH = N == 64 ? 3 : 4;    // half slots (a tile takes two)
+  static constexpr int kNR = N == 64 ? 1 : 2;    // RoPE slots
+  static constexpr int kUW = N == 64 ? 8 : 16;   // unpacking warps
+  static constexpr int kThreads = (kUnpackWarp + kUW) * 32;
   static constexpr int kQ = N * 128 * 9;
-  static constexpr int kPairOff = 0;
-  static constexpr int kRopeOff = kPairOff + kNT * 4 * kPair;
-  static constexpr int kQOff = kRopeOff + kNT * kRope;
+  static constexpr int kHalfOff = 0;
+  static constexpr int kRopeOff = kHalfOff + kNH * kHalf;
+  static constexpr int kQOff = kRopeOff + kNR * kChunk;
   static constexpr int kPOff = kQOff + kQ;
   static constexpr int kP = kTile4 * N * 2;
   static constexpr int kRawOff = kPOff + kP;
@@ -84,8 +85,8 @@ struct Smem4 {
     B_RAW_FULL = 0,
     B_RAW_EMPTY = 2,
     B_FULL = 4,
-    B_EMPTY = B_FULL + kNT,
-    B_Q_FULL = B_EMPTY + kNT,
+    B_EMPTY = B_FULL + kNH,
+    B_Q_FULL = B_EMPTY + kNH,
     B_Q_EMPTY,
     B_S_FULL,
     B_S_EMPTY = B_S_FULL + 2,
@@ -217,7 +218,7 @@ struct PartScratch {
   int nt[8192];
 };
 
-template <int N>
+template <int N, int kThreads4>
 __device__ __forceinline__ Range4 partition4(const Fp4Params& fp, PartScratch* ps, int cid, int ncta) {
   constexpr int kWarps = kThreads4 / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -507,7 +508,7 @@ __device__ __forceinline__ void multipliers(uint32_t s2, bool valid, uint32_t& m
 
 // ---------------------------------------------------------------- the kernel
 template <bool BF16, int N>
-__global__ void __launch_bounds__(kThreads4, 1)
+__global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
     mla_partial_fp4_kernel(const __grid_constant__ CUtensorMap tm_qlat, const __grid_constant__ CUtensorMap tm_qpe,
                            const Fp4Params fp) {
   using L = Smem4<N>;
@@ -527,12 +528,12 @@ __global__ void __launch_bounds__(kThreads4, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bar[L::B_RAW_FULL + s], 1);
-      mbar_init(&bar[L::B_RAW_EMPTY + s], 8);
+      mbar_init(&bar[L::B_RAW_EMPTY + s], L::kUW);
       mbar_init(&bar[L::B_S_FULL + s], 1);
       mbar_init(&bar[L::B_S_EMPTY + s], 8);
     }
-    for (int s = 0; s < L::kNT; ++s) {
-      mbar_init(&bar[L::B_FULL + s], 8);
+    for (int s = 0; s < L::kNH; ++s) {
+      mbar_init(&bar[L::B_FULL + s], L::kUW);
       mbar_init(&bar[L::B_EMPTY + s], 1);
     }
     mbar_init(&bar[L::B_Q_FULL], 1);
@@ -553,7 +554,7 @@ __global__ void __launch_bounds__(kThreads4, 1)
     prefetch_tmap(&tm_qpe);
   }
   griddep_launch_dependents();   // the merge grid may be scheduled as CTAs retire; it waits for this one
-  const Range4 rng = partition4<N>(fp, reinterpret_cast<PartScratch*>(smem), cid, ncta);
+  const Range4 rng = partition4<N, L::kThreads>(fp, reinterpret_cast<PartScratch*>(smem), cid, ncta);
   {
     const int n = rng.u_begin <= rng.u_last ? min(rng.u_last - rng.u_begin + 1, kUnits4) : 0;
     if (static_cast<int>(threadIdx.x) < n) tab->u[threadIdx.x] = unit4<N>(fp, rng.u_begin + threadIdx.x);
@@ -638,7 +639,7 @@ __global__ void __launch_bounds__(kThreads4, 1)
     // changes at a unit's end is worked out once per piece, not per tile.
     const bool leader = elect_one();
     constexpr uint32_t idesc = make_idesc_f16(64, N, BF16, false, false);
-    const uint64_t a0 = make_desc_sw128(smem_u32(smem + L::kPairOff), 16, 1024);
+    const uint64_t a0 = make_desc_sw128(smem_u32(smem + L::kHalfOff), 16, 1024);
     const uint64_t r0 = make_desc_sw128(smem_u32(smem + L::kRopeOff), 16, 1024);
     const uint64_t q0 = make_desc_sw128(smem_u32(smem + L::kQOff), 16, 1024);
     auto wait = [&](uint64_t* b, uint32_t parity) { return __all_sync(0xffffffffu, waits.wait(b, parity)) != 0; };
@@ -658,24 +659,26 @@ __global__ void __launch_bounds__(kThreads4, 1)
           break;
         }
         const uint32_t d = tmem + L::kTmemS + sb * N;
-        const int tb = L::buffer(g);
-        if (!wait(&bar[L::B_FULL + tb], L::phase(g))) {
-          ok = false;
-          break;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int hc = 2 * g + h, sl = hc % L::kNH;
+          if (!wait(&bar[L::B_FULL + sl], (hc / L::kNH) & 1)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t a = a0 + sl * (kHalf >> 4);
+#pragma unroll
+          for (int kk = 0; kk < 16; ++kk)
+            if (leader)
+              umma_ss(d, a + (kk >> 2) * (kChunk >> 4) + (kk & 3) * 2, q0 + (4 * h + (kk >> 2)) * (N * 8) + (kk & 3) * 2,
+                      idesc, (h | kk) ? 1u : 0u);
         }
-        tc_fence_after();
-        const uint64_t a = a0 + L::pair_slot(g, 0) * (kPair >> 4), r = r0 + tb * (kRope >> 4);
+        if (!ok) break;
+        const uint64_t r = r0 + (g % L::kNR) * (kChunk >> 4);   // (full with the second half)
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          if (leader) umma_ss(d, r + kk * 2, q0 + 8 * (N * 8) + kk * 2, idesc, kk ? 1u : 0u);
-#pragma unroll
-        for (int p = 0; p < 4; ++p) {
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            if (leader)
-              umma_ss(d, a + p * (kPair >> 4) + (kk >> 2) * (kRope >> 4) + (kk & 3) * 2,
-                      q0 + (2 * p + (kk >> 2)) * (N * 8) + (kk & 3) * 2, idesc, 1u);
-        }
+          if (leader) umma_ss(d, r + kk * 2, q0 + 8 * (N * 8) + kk * 2, idesc, 1u);
         if (leader) {
           umma_commit(&bar[L::B_S_FULL + sb]);
           if (lastq && k == n - 1) umma_commit(&bar[L::B_Q_EMPTY]);
@@ -689,7 +692,7 @@ __global__ void __launch_bounds__(kThreads4, 1)
     // ------------------------------------------------ PV issuer: O^T += V^T P^T
     const bool leader = elect_one();
     constexpr uint32_t idesc = make_idesc_f16(128, N, BF16, true, true);
-    const uint64_t v0 = make_desc_sw128(smem_u32(smem + L::kPairOff), kRope, 1024);
+    const uint64_t v0 = make_desc_sw128(smem_u32(smem + L::kHalfOff), kChunk, 1024);
     const uint64_t p0 = desc_mn<N>(smem_u32(smem + L::kPOff));
     auto wait = [&](uint64_t* b, uint32_t parity) { return __all_sync(0xffffffffu, waits.wait(b, parity)) != 0; };
     Iter4<N> it;
@@ -705,19 +708,21 @@ __global__ void __launch_bounds__(kThreads4, 1)
         }
         tc_fence_after();
         const uint32_t more = k > 0 ? 1u : 0u;
-        const uint64_t v = v0 + L::pair_slot(g, 0) * (kPair >> 4);
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
+        for (int h = 0; h < 2; ++h) {
+          const int sl = (2 * g + h) % L::kNH;
+          const uint64_t v = v0 + sl * (kHalf >> 4);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            if (leader)
-              umma_ss(tmem + L::kTmemO + p * N, v + p * (kPair >> 4) + kk * 128, p0 + kk * (N * 2), idesc,
-                      kk ? 1u : more);
+          for (int p = 0; p < 2; ++p) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              if (leader)
+                umma_ss(tmem + L::kTmemO + (2 * h + p) * N, v + p * (2 * kChunk >> 4) + kk * 128, p0 + kk * (N * 2), idesc,
+                        kk ? 1u : more);
+          }
+          if (leader) umma_commit(&bar[L::B_EMPTY + sl]);
         }
-        if (leader) {
-          umma_commit(&bar[L::B_EMPTY + L::buffer(g)]);
-          umma_commit(&bar[L::B_P_EMPTY]);
-        }
+        if (leader) umma_commit(&bar[L::B_P_EMPTY]);
       }
       it.next_piece(fp);
     }
@@ -922,20 +927,22 @@ __global__ void __launch_bounds__(kThreads4, 1)
     }
   } else {
     // ------------------------------------------------ unpacking
-    // Two warps a pair, one lane a token: its 128 columns and 16 of the RoPE
-    // columns, one fence and one arrival a tile.
+    // A lane is a token; the two halves of the latents one after the other, a
+    // half's eight 32-column units spread over the warps, the RoPE columns
+    // with the second.  One fence and one arrival a half.
+    constexpr int GP = L::kUW / 2, NU = 8 / GP;     // column groups; units of a half per lane
     const int w = warp - kUnpackWarp;
-    const int t = (w & 1) * 32 + lane, p = w >> 1;
-    uint8_t* rope0 = smem + L::kRopeOff;
-    uint8_t* pair0 = smem + L::kPairOff;
+    const int t = (w & 1) * 32 + lane, grp = w >> 1;
+    uint8_t* half0 = smem + L::kHalfOff;
     Iter4<N> it;
     it.start(fp, tab, rng);
     int g = 0, rs = 0;
-    while (it.valid) {
+    bool ok = true;
+    while (ok && it.valid) {
       const bool cur = it.ui.p == fp.S;
       const bool valid = it.tok0() + t < it.ui.hi;
-      uint4 c[4] = {}, rc = make_uint4(0, 0, 0, 0);
-      uint32_t sc[2] = {0, 0}, rsc = 0;
+      uint4 c[2 * NU] = {};
+      uint32_t sc[2 * NU] = {}, rc[2] = {0, 0}, rsc = 0;
       const uint4* row = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(fp.kv_cur) +
                                                         (static_cast<int64_t>(it.ui.b) * fp.q_len + t) * 576);
       if (!cur) {
@@ -944,63 +951,76 @@ __global__ void __launch_bounds__(kThreads4, 1)
         const uint8_t* codes = smem + L::kRawOff + st * kRawStage + t * kE2m1Codes;
         const uint8_t* scales = smem + L::kRawOff + st * kRawStage + kRawCodes + t * kE2m1Scales;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) c[q] = *reinterpret_cast<const uint4*>(codes + p * 64 + q * 16);
-        sc[0] = *reinterpret_cast<const uint32_t*>(scales + p * 8);
-        sc[1] = *reinterpret_cast<const uint32_t*>(scales + p * 8 + 4);
-        const uint2 r2 = *reinterpret_cast<const uint2*>(codes + 256 + p * 8);
-        rc.x = r2.x;
-        rc.y = r2.y;
-        rsc = scales[32 + p];
+        for (int k = 0; k < 2 * NU; ++k) {
+          const int u = (k / NU) * 8 + (k % NU) * GP + grp;   // 32-column unit of the 16
+          c[k] = *reinterpret_cast<const uint4*>(codes + u * 16);
+          sc[k] = *reinterpret_cast<const uint16_t*>(scales + u * 2);
+        }
+        if constexpr (GP == 8) {
+          rc[0] = *reinterpret_cast<const uint32_t*>(codes + 256 + grp * 4);
+          rsc = scales[32 + grp / 2];
+        } else {
+          const uint2 x = *reinterpret_cast<const uint2*>(codes + 256 + grp * 8);
+          rc[0] = x.x;
+          rc[1] = x.y;
+          rsc = scales[32 + grp];
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar[L::B_RAW_EMPTY + st]);
         ++rs;
       }
-      const int tb = L::buffer(g);
-      if (g >= L::kNT && !__all_sync(0xffffffffu, waits.wait(&bar[L::B_EMPTY + tb], L::phase(g) ^ 1))) break;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint4 x[4];
-        if (cur) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) x[k] = valid ? row[p * 16 + q * 4 + k] : make_uint4(0, 0, 0, 0);
-        } else {
-          uint32_t m0, m1, a[4];
-          multipliers(sc[q >> 1] >> ((q & 1) * 16), valid, m0, m1);
-          unpack8<BF16>(c[q].x, m0, a);
-          x[0] = make_uint4(a[0], a[1], a[2], a[3]);
-          unpack8<BF16>(c[q].y, m0, a);
-          x[1] = make_uint4(a[0], a[1], a[2], a[3]);
-          unpack8<BF16>(c[q].z, m1, a);
-          x[2] = make_uint4(a[0], a[1], a[2], a[3]);
-          unpack8<BF16>(c[q].w, m1, a);
-          x[3] = make_uint4(a[0], a[1], a[2], a[3]);
+      for (int h = 0; h < 2; ++h) {
+        const int hc = 2 * g + h, sl = hc % L::kNH;
+        if (hc >= L::kNH && !__all_sync(0xffffffffu, waits.wait(&bar[L::B_EMPTY + sl], ((hc / L::kNH) - 1) & 1))) {
+          ok = false;
+          break;
         }
-        uint8_t* d = pair0 + L::pair_slot(g, p) * kPair + (q >> 1) * kRope;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4*>(d + sw128_offset(t, (q & 1) * 4 + k)) = x[k];
-      }
-      {
-        uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0;
-        if (cur) {
-          if (valid) {
-            x0 = row[64 + 2 * p];
-            x1 = row[64 + 2 * p + 1];
+        for (int k = h * NU; k < (h + 1) * NU; ++k) {
+          const int u = (k % NU) * GP + grp;                  // unit of the half
+          uint4 x[4];
+          if (cur) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[j] = valid ? row[h * 32 + u * 4 + j] : make_uint4(0, 0, 0, 0);
+          } else {
+            uint32_t m0, m1, a[4];
+            multipliers(sc[k], valid, m0, m1);
+            unpack8<BF16>(c[k].x, m0, a);
+            x[0] = make_uint4(a[0], a[1], a[2], a[3]);
+            unpack8<BF16>(c[k].y, m0, a);
+            x[1] = make_uint4(a[0], a[1], a[2], a[3]);
+            unpack8<BF16>(c[k].z, m1, a);
+            x[2] = make_uint4(a[0], a[1], a[2], a[3]);
+            unpack8<BF16>(c[k].w, m1, a);
+            x[3] = make_uint4(a[0], a[1], a[2], a[3]);
           }
-        } else {
+          uint8_t* d = half0 + sl * kHalf + (u >> 1) * kChunk;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(d + sw128_offset(t, (u & 1) * 4 + j)) = x[j];
+        }
+        if (h == 1) {
+          // (the RoPE slot's last readers were done before this half slot's)
+          uint8_t* d = smem + L::kRopeOff + (g % L::kNR) * kChunk;
           uint32_t m0, m1, a[4];
           multipliers(rsc, valid, m0, m1);
-          unpack8<BF16>(rc.x, m0, a);
-          x0 = make_uint4(a[0], a[1], a[2], a[3]);
-          unpack8<BF16>(rc.y, m0, a);
-          x1 = make_uint4(a[0], a[1], a[2], a[3]);
+#pragma unroll
+          for (int j = 0; j < 8 / GP; ++j) {
+            const int u = grp * (8 / GP) + j;                 // 16-byte unit of the chunk
+            uint4 x;
+            if (cur) {
+              x = valid ? row[64 + u] : make_uint4(0, 0, 0, 0);
+            } else {
+              unpack8<BF16>(rc[j], m0, a);
+              x = make_uint4(a[0], a[1], a[2], a[3]);
+            }
+            *reinterpret_cast<uint4*>(d + sw128_offset(t, u)) = x;
+          }
         }
-        uint8_t* d = rope0 + tb * kRope;
-        *reinterpret_cast<uint4*>(d + sw128_offset(t, 2 * p)) = x0;
-        *reinterpret_cast<uint4*>(d + sw128_offset(t, 2 * p + 1)) = x1;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar[L::B_FULL + sl]);
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar[L::B_FULL + tb]);
       it.advance(fp);
       ++g;
     }
@@ -1127,7 +1147,7 @@ static int launch4(const CUtensorMap& qlat, const CUtensorMap& qpe, const Fp4Par
   const int most = fp4_max_ctas();
   if (most < 1 || cudaGetDevice(&dev) != cudaSuccess || !prepare4<BF16, N>(dev)) return -1;
   const int ctas = fp.split ? fp.split : std::max(1, std::min(fp.num_units, most));
-  mla_partial_fp4_kernel<BF16, N><<<ctas, kThreads4, Smem4<N>::kTotal, stream>>>(qlat, qpe, fp);
+  mla_partial_fp4_kernel<BF16, N><<<ctas, Smem4<N>::kThreads, Smem4<N>::kTotal, stream>>>(qlat, qpe, fp);
   if (!fp.split) return 0;
   if (cudaPeekAtLastError() != cudaSuccess) return -1;
   cudaLaunchConfig_t cfg = {};
