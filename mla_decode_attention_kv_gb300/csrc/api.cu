@@ -342,7 +342,10 @@ int mla_dcp_decode_partial_fp4(const void* q_abs, const void* q_pe, const void* 
   const int rows = mla::fp4_unit_rows(R);
   const int64_t G = (R + rows - 1) / rows;
   const int P = num_shards + (kv_cur ? 1 : 0);
-  if (G * B * P > INT32_MAX) return MLA_ERR_BAD_SHAPE;
+  // the kernel counts tokens, units and the cost of its tiles in 32 bits
+  const int64_t tokens = static_cast<int64_t>(max_blocks) * block_size;
+  if (tokens > INT32_MAX || G * B * P > INT32_MAX / 4 || G * B * (tokens / 64 + 1) > INT32_MAX / 2)
+    return MLA_ERR_BAD_SHAPE;
   CUtensorMap tm_qlat, tm_qpe;
   if (!make_map(&tm_qlat, q_abs, 512, B * R, 1024, 64, rows, bf16) ||
       !make_map(&tm_qpe, q_pe, 64, B * R, 128, 64, rows, bf16))

@@ -75,7 +75,8 @@ struct Smem4 {
   static constexpr int kQOff = kRopeOff + kNR * kChunk;
   static constexpr int kPOff = kQOff + kQ;
   static constexpr int kP = kTile4 * N * 2;
-  static constexpr int kRawOff = kPOff + kP;
+  static constexpr int kStageOff = kPOff + kP;               // 16 rows: the epilogue's staging
+  static constexpr int kRawOff = kStageOff + (N == 16 ? 4096 : 0);
   static constexpr int kMOff = kRawOff + 2 * kRawStage;      // reference maxima [N]
   static constexpr int kRedOff = kMOff + N * 4;              // reductions over the warps [2 groups][4][N / 2]
   static constexpr int kUnitOff = kRedOff + N * 16;
@@ -212,143 +213,135 @@ constexpr int kCostUnit = 2;
 
 struct PartScratch {
   unsigned long long scan[32];
-  int load[kFp4MaxCtas];
-  int bound[kFp4MaxCtas + 1];
-  int rng[4];
-  int nt[8192];
+  int2 pre[1024];                  // tiles and cost before each thread's units
+  int bound[kFp4MaxCtas + 1];      // first tile of each CTA's share
+  int whole[kFp4MaxCtas + 1];      // cost before the first unit that starts at or behind it
+  int4 rng;
 };
 
-template <int N, int kThreads4>
+template <int N, int NT>
 __device__ __forceinline__ Range4 partition4(const Fp4Params& fp, PartScratch* ps, int cid, int ncta) {
-  constexpr int kWarps = kThreads4 / 32;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kWarps = NT / 32;
+  static_assert(NT <= 1024 && NT > kFp4MaxCtas, "block size");
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int U = fp.num_units;
-  const int per = (U + kThreads4 - 1) / kThreads4;
-  const int a = min(U, static_cast<int>(threadIdx.x) * per), e = min(U, a + per);
-  int cnt = 0, cost = 0;
-  for (int u = a; u < e; ++u) {
-    const int nt = tiles4(unit4<N>(fp, u));
-    if (u < 8192) ps->nt[u] = nt;
-    cnt += nt;
-    cost += nt > 0 ? kCostTile * nt + kCostUnit : 0;
-  }
-  auto unit_tiles = [&](int u) { return u < 8192 ? ps->nt[u] : tiles4(unit4<N>(fp, u)); };
-  const unsigned long long mine = (static_cast<unsigned long long>(cost) << 32) | static_cast<unsigned>(cnt);
-  unsigned long long incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const unsigned long long y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
-  }
-  if (lane == 31) ps->scan[warp] = incl;
-  if (threadIdx.x == 0) {
-    ps->rng[0] = INT_MAX;
-    ps->rng[1] = 0;
-    ps->rng[2] = -1;
-    ps->rng[3] = 0;
-  }
-  for (int c = threadIdx.x; c < ncta; c += kThreads4) ps->load[c] = 0;
-  __syncthreads();
-  unsigned long long base = 0, all = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    const unsigned long long t = ps->scan[w];
-    base += w < warp ? t : 0;
-    all += t;
-  }
-  const unsigned long long before = base + incl - mine;
-  const int tstart = static_cast<int>(before & 0xffffffffu);
-  const int64_t cstart = static_cast<int64_t>(before >> 32);
-  const int total = static_cast<int>(all & 0xffffffffu);
-  const int64_t all_cost = static_cast<int64_t>(all >> 32);
-  if (all_cost > 0) {
-    int64_t crun = cstart;
-    int trun = tstart;
+  const int per = (U + NT - 1) / NT;
+  auto cost_of = [](int nt) { return nt > 0 ? kCostTile * nt + kCostUnit : 0; };
+  {
+    int cnt = 0, cost = 0;
+    const int a = min(U, tid * per), e = min(U, a + per);
     for (int u = a; u < e; ++u) {
-      const int nt = unit_tiles(u);
-      if (nt == 0) continue;
-      const int64_t cend = crun + kCostTile * nt + kCostUnit;
-      for (int c = max(1, static_cast<int>((crun * ncta + all_cost - 1) / all_cost)); c < ncta; ++c) {
-        const int64_t tc = static_cast<int64_t>(c) * all_cost / ncta;
-        if (tc >= cend) break;
-        const int64_t into = tc - crun - kCostUnit;
-        const int64_t j = into <= 0 ? 0 : min(static_cast<int64_t>(nt), (into + kCostTile - 1) / kCostTile);
-        ps->bound[c] = trun + static_cast<int>(j);
-      }
-      trun += nt;
-      crun = cend;
+      const int nt = tiles4(unit4<N>(fp, u));
+      cnt += nt;
+      cost += cost_of(nt);
     }
-  } else {
-    for (int c = threadIdx.x; c <= ncta; c += kThreads4) ps->bound[c] = 0;
+    const unsigned long long mine = (static_cast<unsigned long long>(cost) << 32) | static_cast<unsigned>(cnt);
+    unsigned long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) ps->scan[warp] = incl;
+    if (tid == 0) ps->rng = make_int4(0, 0, -1, 0);
+    __syncthreads();
+    unsigned long long base = 0;
+    for (int w = 0; w < warp; ++w) base += ps->scan[w];
+    const unsigned long long before = base + incl - mine;
+    ps->pre[tid] = make_int2(static_cast<int>(before & 0xffffffffu), static_cast<int>(before >> 32));
   }
-  if (threadIdx.x == 0) {
-    ps->bound[0] = 0;
-    ps->bound[ncta] = total;
-  }
+  unsigned long long all = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) all += ps->scan[w];
+  const int total = static_cast<int>(all & 0xffffffffu), all_cost = static_cast<int>(all >> 32);
   __syncthreads();
-  auto cta_of = [&](int t) {   // the last CTA whose share starts at or before tile t
-    int lo = 0, hi = ncta - 1;
+  if (total == 0) {
+    if (fp.split && tid == 0) {
+      fp.ws_units[cid] = make_int4(-1, 0, 0, 0);
+      fp.ws_bounds[cid] = 0;
+      if (cid == 0) fp.ws_bounds[ncta] = 0;
+    }
+    return {0, 0, -1, 0};
+  }
+  // The unit with tiles that holds tile (COST false) or cost (true) x: the
+  // thread whose units hold it, by bisection, then a walk along them.
+  struct Found {
+    int u, nt, t0, c0;   // unit, its tiles, tiles and cost before it
+  };
+  auto find = [&](int x, bool by_cost) {
+    int lo = 0, hi = NT - 1;   // the last thread with pre <= x
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (ps->bound[mid] <= t) lo = mid;
+      if ((by_cost ? ps->pre[mid].y : ps->pre[mid].x) <= x) lo = mid;
       else hi = mid - 1;
     }
-    return lo;
+    Found f{lo * per, 0, ps->pre[lo].x, ps->pre[lo].y};
+    for (;; ++f.u) {
+      f.nt = tiles4(unit4<N>(fp, f.u));
+      const int c = cost_of(f.nt);
+      if (by_cost ? x < f.c0 + c : x < f.t0 + f.nt) return f;
+      f.t0 += f.nt;
+      f.c0 += c;
+    }
   };
-  bool split = false;
-  if (fp.split && total > 0) {
-    int run = tstart;
-    for (int u = a; u < e; ++u) {
-      const int nt = unit_tiles(u);
-      if (nt > 0) atomicAdd(&ps->load[cta_of(run)], kCostTile * nt + kCostUnit);
-      run += nt;
+  // boundary c: the tiles that start below the cost c * all_cost / ncta
+  if (tid <= ncta) {
+    const int tc = static_cast<int>(static_cast<int64_t>(tid) * all_cost / ncta);
+    int bound = total, whole = all_cost;
+    if (tid < ncta) {
+      const Found f = find(tc, true);
+      const int into = tc - f.c0 - kCostUnit;
+      const int j = tid == 0 || into <= 0 ? 0 : min(f.nt, (into + kCostTile - 1) / kCostTile);
+      bound = tid == 0 ? 0 : f.t0 + j;
+      whole = tid == 0 ? 0 : j == 0 ? f.c0 : f.c0 + cost_of(f.nt);
     }
-    __syncthreads();
-    int mx = 0;
-    for (int c = threadIdx.x; c < ncta; c += kThreads4) mx = max(mx, ps->load[c]);
-    const int64_t even = (all_cost + ncta - 1) / ncta;
-    split = __syncthreads_or(mx > even + max(int64_t{3 * kCostTile}, even / 8)) != 0;
-  }
-  const int lo = ps->bound[cid], hi = ps->bound[cid + 1];
-  int run = tstart;
-  for (int u = a; u < e; ++u) {
-    const int nt = unit_tiles(u);
-    if (nt > 0 && lo < hi) {
-      if (split) {
-        if (lo >= run && lo < run + nt) {
-          ps->rng[0] = u;
-          ps->rng[1] = lo - run;
-        }
-        if (hi - 1 >= run && hi - 1 < run + nt) {
-          ps->rng[2] = u;
-          ps->rng[3] = hi - run;
-        }
-      } else if (run >= lo && run < hi) {
-        atomicMin(&ps->rng[0], u);
-        atomicMax(&ps->rng[2], u);
-      }
-    }
-    run += nt;
+    ps->bound[tid] = bound;
+    ps->whole[tid] = whole;
   }
   __syncthreads();
-  Range4 r;
-  r.u_begin = ps->rng[0];
-  r.j_begin = ps->rng[1];
-  r.u_last = ps->rng[2];
-  r.j_stop = split ? ps->rng[3] : (r.u_last < 0 ? 0 : unit_tiles(r.u_last));
-  // the record of the unit that was cut before this share and ends inside it
-  if (fp.split && threadIdx.x == 0) {
-    int4 rec = make_int4(-1, 0, 0, 0);
-    if (split && r.u_begin <= r.u_last && r.j_begin > 0 &&
-        (r.u_begin < r.u_last || r.j_stop == unit_tiles(r.u_begin))) {
-      const int ustart = lo - r.j_begin;
-      rec = make_int4(r.u_begin, ustart, cta_of(ustart), cid);
+  bool split = false;
+  if (fp.split) {
+    const int even = (all_cost + ncta - 1) / ncta;
+    const bool over = tid < ncta && ps->whole[tid + 1] - ps->whole[tid] > even + max(3 * kCostTile, even / 8);
+    split = __syncthreads_or(over) != 0;
+  }
+  const int lo = ps->bound[cid], hi = ps->bound[cid + 1];
+  if (lo < hi && tid < 2) {
+    // thread 0 finds the first piece, thread 1 the last
+    Found f = find(tid == 0 ? lo : hi - 1, false);
+    if (tid == 0) {
+      if (!split && f.t0 < lo) {   // the first unit that starts in the share
+        f.t0 += f.nt;
+        do f.nt = ++f.u < U ? tiles4(unit4<N>(fp, f.u)) : 1;
+        while (f.nt == 0);
+      }
+      ps->rng.x = f.u;
+      ps->rng.y = split ? lo - f.t0 : 0;
+      // the record of a unit cut before this share that ends inside it
+      int4 rec = make_int4(-1, 0, 0, 0);
+      if (split && lo > f.t0 && f.t0 + f.nt <= hi) {
+        int a = 0, e = ncta - 1;   // the CTA that holds the unit's first tile: the last with bound <= t0
+        while (a < e) {
+          const int mid = (a + e + 1) >> 1;
+          if (ps->bound[mid] <= f.t0) a = mid;
+          else e = mid - 1;
+        }
+        rec = make_int4(f.u, f.t0, a, cid);
+      }
+      if (fp.split) fp.ws_units[cid] = rec;
+    } else {
+      ps->rng.z = f.u;
+      ps->rng.w = split ? hi - f.t0 : f.nt;
     }
-    fp.ws_units[cid] = rec;
+  } else if (fp.split && tid == 0) {
+    fp.ws_units[cid] = make_int4(-1, 0, 0, 0);
+  }
+  if (fp.split && tid == 0) {
     fp.ws_bounds[cid] = lo;
     if (cid == 0) fp.ws_bounds[ncta] = total;
   }
-  return r;
+  __syncthreads();
+  return {ps->rng.x, ps->rng.y, ps->rng.z, ps->rng.w};
 }
 
 // Row of o_part / lse_part of query row r (of R) of sequence b in part p.
@@ -420,22 +413,26 @@ __device__ __forceinline__ void tmem_put(uint32_t a, const uint32_t (&r)[8]) {
 __device__ __forceinline__ void tmem_put(uint32_t a, const uint32_t (&r)[16]) { tmem_st16(a, r); }
 __device__ __forceinline__ void tmem_put(uint32_t a, const uint32_t (&r)[32]) { tmem_st32(a, r); }
 
-// MN-major operand of N columns (rows of N 16-bit values, one per k): the
-// swizzle as wide as the row, 8-row groups one after another.
+// P^T, the MN-major B operand: a row of 16-bit columns per token (k).  For 32
+// and 64 rows the two softmax groups' columns are blocks of their own, [64
+// tokens][N / 2] with the swizzle as wide as a row (32 or 64 bytes), LBO from
+// block to block; for 16 rows one block holds both groups' eight columns.
 template <int N>
-__device__ __forceinline__ uint64_t desc_mn(uint32_t addr) {
-  constexpr uint64_t type = N == 64 ? 2 : N == 32 ? 4 : 6;   // 128-, 64-, 32-byte swizzle
-  constexpr uint32_t sbo = 8 * N * 2;
-  return static_cast<uint64_t>((addr >> 4) & 0x3FFF) | (uint64_t{1} << 16) |
-         (static_cast<uint64_t>(sbo >> 4) << 32) | (uint64_t{1} << 46) | (type << 61);
-}
-
-// Byte offset of 16-byte unit k of row t in that layout.
-template <int N>
-__device__ __forceinline__ uint32_t p_offset(int t, int k) {
-  const int x = N == 64 ? (t & 7) : N == 32 ? ((t >> 1) & 3) : ((t >> 2) & 1);
-  return t * (N * 2) + ((k ^ x) << 4);
-}
+struct PLayout {
+  static constexpr int kCols = N == 16 ? 16 : N / 2;        // columns of a block
+  static constexpr int kRow = kCols * 2;                    // bytes
+  static constexpr int kBlock = kTile4 * kRow;
+  static constexpr int kStep = 16 * kRow;                   // bytes from one k-step (16 tokens) to the next
+  static __device__ __forceinline__ uint64_t desc(uint32_t addr) {
+    constexpr uint64_t type = kCols == 32 ? 4 : 6;          // 64-, 32-byte swizzle
+    return static_cast<uint64_t>((addr >> 4) & 0x3FFF) | (static_cast<uint64_t>(kBlock >> 4) << 16) |
+           (static_cast<uint64_t>(8 * kRow >> 4) << 32) | (uint64_t{1} << 46) | (type << 61);
+  }
+  // byte offset of 16-byte unit k of token t in a block
+  static __device__ __forceinline__ uint32_t offset(int t, int k) {
+    return t * kRow + ((k ^ (kCols == 32 ? (t >> 1) & 3 : (t >> 2) & 1)) << 4);
+  }
+};
 
 // Reduction over the 16 lanes of a half warp of NC columns held one row per
 // lane: every step halves the columns a lane keeps, so 16 columns take 15
@@ -693,7 +690,7 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
     const bool leader = elect_one();
     constexpr uint32_t idesc = make_idesc_f16(128, N, BF16, true, true);
     const uint64_t v0 = make_desc_sw128(smem_u32(smem + L::kHalfOff), kChunk, 1024);
-    const uint64_t p0 = desc_mn<N>(smem_u32(smem + L::kPOff));
+    const uint64_t p0 = PLayout<N>::desc(smem_u32(smem + L::kPOff));
     auto wait = [&](uint64_t* b, uint32_t parity) { return __all_sync(0xffffffffu, waits.wait(b, parity)) != 0; };
     Iter4<N> it;
     it.start(fp, tab, rng);
@@ -717,7 +714,7 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
               if (leader)
-                umma_ss(tmem + L::kTmemO + (2 * h + p) * N, v + p * (2 * kChunk >> 4) + kk * 128, p0 + kk * (N * 2), idesc,
+                umma_ss(tmem + L::kTmemO + (2 * h + p) * N, v + p * (2 * kChunk >> 4) + kk * 128, p0 + kk * (PLayout<N>::kStep >> 4), idesc,
                         kk ? 1u : more);
           }
           if (leader) umma_commit(&bar[L::B_EMPTY + sl]);
@@ -747,7 +744,8 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
     // Two groups of four warps, each with half of the rows (columns of S^T)
     // and nothing shared between them.
     constexpr int NG = N / 2, NC = N / 4;      // columns of a group, of a thread
-    constexpr int NO = NG < 16 ? NG : 16;      // columns of O at a time
+    constexpr int NO = N == 64 ? 16 : 8;       // columns of O at a time
+    using PL = PLayout<N>;
     const int grp = (warp - kSoftWarp) >> 2, wq = warp & 3;
     const int gtid = threadIdx.x - kSoftWarp * 32 - grp * 128;
     const int barid = 1 + grp;
@@ -755,7 +753,10 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
     const int tok = wq * 16 + (lane & 15);     // token of the tile
     const int c0 = grp * NG + (lane >> 4) * NC;   // first column of this thread
     const int cr = (lane >> 4) * NC + (lane & 15) / (16 / NC);   // column (of the group) that col_reduce leaves here
-    uint8_t* sP = smem + L::kPOff;
+    uint8_t* sP = smem + L::kPOff + (N == 16 ? 0 : grp * PL::kBlock);   // this group's block
+    // a warp's staging of the epilogue: its share of the group's block of P, which no
+    // MMA reads then (16 rows: a region of its own)
+    uint8_t* stage = N == 16 ? smem + L::kStageOff + (warp - kSoftWarp) * 512 : sP + wq * (PL::kBlock / 4);
     float* s_m = reinterpret_cast<float*>(smem + L::kMOff) + grp * NG;
     float* red = reinterpret_cast<float*>(smem + L::kRedOff) + grp * (4 * NG);   // [4][NG]
     float l[NC], m[NC];
@@ -855,12 +856,13 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
       if (g >= 1) ok = ok && waits.lazy(&bar[L::B_P_EMPTY], (g - 1) & 1);
       ok = __all_sync(0xffffffffu, ok);
       if (ok) {
+        const int hw = lane >> 4;
         if constexpr (NC == 4) {
-          *reinterpret_cast<uint2*>(sP + p_offset<N>(tok, c0 / 8) + (c0 & 4) * 2) = make_uint2(pk[0], pk[1]);
+          *reinterpret_cast<uint2*>(sP + PL::offset(tok, grp) + hw * 8) = make_uint2(pk[0], pk[1]);
         } else {
 #pragma unroll
           for (int k = 0; k < NC / 8; ++k)
-            *reinterpret_cast<uint4*>(sP + p_offset<N>(tok, c0 / 8 + k)) =
+            *reinterpret_cast<uint4*>(sP + PL::offset(tok, hw * (NC / 8) + k)) =
                 make_uint4(pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]);
         }
         fence_proxy_async_smem();
@@ -877,45 +879,63 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
         named_bar_sync(barid, 128);
         const bool whole = it.whole();
         const int slot = 2 * cid + (it.u == rng.u_begin ? 0 : 1);
-        // lane k has row k of the group
-        float inv = 0.f;
-        int64_t dst = -1;
-        if (lane < NG) {
-          const float sum = (red[lane] + red[NG + lane]) + (red[2 * NG + lane] + red[3 * NG + lane]);
+        // row k of the group in lane k
+        const int esz = fp.part_dtype == kFP32 ? 4 : 2;
+        float sum = 1.f;
+        if (lane < NG) sum = (red[lane] + red[NG + lane]) + (red[2 * NG + lane] + red[3 * NG + lane]);
+        named_bar_sync(barid, 128);
+        float* inv = red;                                        // [NG]
+        int64_t* dst = reinterpret_cast<int64_t*>(red + NG);     // [NG] byte offset of the row, -1: none
+        if (wq == 0 && lane < NG) {
           const float lse2 = s_m[lane] + log2f(sum);
-          inv = (cur ? 1.f : fp.kv_scale) / sum;
           const int n = grp * NG + lane, r = ui.g * N + n;
+          int64_t row = -1;
           if (r < fp.R) {
-            dst = whole ? out_row4(fp, ui.b, r, ui.p) : static_cast<int64_t>(slot) * N + n;
-            if (wq == 0) {
-              if (whole) fp.lse_part[dst] = lse2 * kLn2;
-              else fp.ws_lse[dst] = lse2;
-            }
+            row = whole ? out_row4(fp, ui.b, r, ui.p) : static_cast<int64_t>(slot) * N + n;
+            if (whole) fp.lse_part[row] = lse2 * kLn2;
+            else fp.ws_lse[row] = lse2;
           }
+          inv[lane] = (cur ? 1.f : fp.kv_scale) / sum;
+          dst[lane] = row < 0 ? -1 : row * 512 * esz;
         }
+        named_bar_sync(barid, 128);
+        // NO rows of 32 latents at a time through the warp's staging: written a
+        // latent per lane, read back and stored 16 bytes per lane along the rows
         char* out = static_cast<char*>(whole ? fp.o_part : fp.ws_o);
-        const bool odd = (lane & 1) != 0;
 #pragma unroll 1
         for (int c = 0; c < 4 * NG; c += NO) {
           uint32_t o[NO];
           const int n0 = c % NG;
           tmem_get(tmem + lanes + L::kTmemO + (c / NG) * N + grp * NG + n0, o);
-          const int lat = (c / NG) * 128 + wq * 32 + lane;
+          const int lat0 = (c / NG) * 128 + wq * 32;
 #pragma unroll
-          for (int k = 0; k < NO; k += 2) {
-            const float f0 = __uint_as_float(o[k]) * __shfl_sync(0xffffffffu, inv, n0 + k);
-            const float f1 = __uint_as_float(o[k + 1]) * __shfl_sync(0xffffffffu, inv, n0 + k + 1);
-            const int64_t d0 = __shfl_sync(0xffffffffu, dst, n0 + k), d1 = __shfl_sync(0xffffffffu, dst, n0 + k + 1);
-            if (fp.part_dtype == kFP32) {
-              if (d0 >= 0) reinterpret_cast<float*>(out)[d0 * 512 + lat] = f0;
-              if (d1 >= 0) reinterpret_cast<float*>(out)[d1 * 512 + lat] = f1;
-            } else {
-              // two rows at a time: an even lane takes its neighbour's value
-              // of the first row, an odd lane that of the second: 4 bytes a store
-              const float got = __shfl_xor_sync(0xffffffffu, odd ? f0 : f1, 1);
-              const uint32_t w = odd ? pack2_dt(got, f1, fp.part_dtype) : pack2_dt(f0, got, fp.part_dtype);
-              const int64_t d = odd ? d1 : d0;
-              if (d >= 0) *reinterpret_cast<uint32_t*>(out + (d * 512 + (lat & ~1)) * 2) = w;
+          for (int k = 0; k < NO; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * inv[n0 + k]);
+          if (esz == 2) {
+#pragma unroll
+            for (int k = 0; k < NO; ++k)
+              reinterpret_cast<uint16_t*>(stage)[k * 32 + lane] =
+                  static_cast<uint16_t>(pack2_dt(__uint_as_float(o[k]), 0.f, fp.part_dtype));
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < NO; k += 8) {
+              const uint4 x = *reinterpret_cast<const uint4*>(stage + k * 64 + lane * 16);
+              const int64_t d = dst[n0 + k + (lane >> 2)];
+              if (d >= 0) *reinterpret_cast<uint4*>(out + d + lat0 * 2 + (lane & 3) * 16) = x;
+            }
+            __syncwarp();
+          } else {
+#pragma unroll
+            for (int h = 0; h < NO; h += NO / 2) {
+#pragma unroll
+              for (int k = 0; k < NO / 2; ++k) reinterpret_cast<uint32_t*>(stage)[k * 32 + lane] = o[h + k];
+              __syncwarp();
+#pragma unroll
+              for (int k = 0; k < NO / 2; k += 4) {
+                const uint4 x = *reinterpret_cast<const uint4*>(stage + k * 128 + lane * 16);
+                const int64_t d = dst[n0 + h + k + (lane >> 3)];
+                if (d >= 0) *reinterpret_cast<uint4*>(out + d + lat0 * 4 + (lane & 7) * 16) = x;
+              }
+              __syncwarp();
             }
           }
         }
