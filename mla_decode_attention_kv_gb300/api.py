@@ -48,19 +48,17 @@ _WORKSPACES = {}
 
 
 def partial_workspace(device, B: int, q_len: int, num_shards: int, has_current: bool,
-                      stream=None, fp4: bool = False):
-    """The default workspace of mla_dcp_decode_partial (fp4: of
-    mla_dcp_decode_partial_fp4) on `device` for calls on `stream` (one per (device, stream), grown as needed), or None for sizes
+                      stream=None):
+    """The default workspace of mla_dcp_decode_partial on `device` for calls on
+    `stream` (one per (device, stream), grown as needed), or None for sizes
     the library rejects.  Calls on one stream run one after another, so they
     can share it; calls on different streams get different workspaces.  Two
     calls that may overlap in time on the same stream handle (graphs replayed
     concurrently, say) must pass workspaces of their own."""
     device = torch.device(device)
     with torch.cuda.device(device):
-        lib = _ffi.lib()
-        size = (lib.mla_dcp_decode_partial_fp4_workspace_size if fp4
-                else lib.mla_dcp_decode_partial_workspace_size)
-        need = int(size(B, q_len, num_shards, 1 if has_current else 0))
+        need = int(_ffi.lib().mla_dcp_decode_partial_workspace_size(
+            B, q_len, num_shards, 1 if has_current else 0))
         s = stream if stream is not None else torch.cuda.current_stream()
     if need == 0:
         return None      # invalid sizes: the call itself reports them
@@ -103,6 +101,10 @@ def mla_dcp_decode_partial(q_abs, q_pe, kv_cache, block_table, seq_lens, num_sha
     partial_workspace), a uint8 CUDA tensor of at least
     mla_dcp_decode_partial_workspace_size bytes, or None (pairs of CTAs then
     take whole shards)."""
+    if is_fp4_cache(kv_cache):
+        return _partial_fp4(q_abs, q_pe, kv_cache, block_table, seq_lens, num_shards, kv_cur, scale,
+                            part_dtype, o_part, lse_part, err_flag, stream, workspace, head_slices,
+                            1.0 if kv_scale is None else kv_scale)
     B, q_len, H, _ = q_abs.shape
     num_blocks, bs, _ = kv_cache.shape
     P = num_shards + (1 if kv_cur is not None else 0)
@@ -124,21 +126,8 @@ def mla_dcp_decode_partial(q_abs, q_pe, kv_cache, block_table, seq_lens, num_sha
         if workspace != "default":
             raise ValueError("workspace must be 'default', a tensor or None")
         workspace = partial_workspace(q_abs.device, B, q_len, num_shards, kv_cur is not None,
-                                      stream, fp4=is_fp4_cache(kv_cache))
+                                      stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    if is_fp4_cache(kv_cache):
-        if kv_cur is not None:
-            _need(kv_cur, "kv_cur")
-            if kv_cur.dtype != q_abs.dtype or kv_cur.numel() != B * q_len * D_QK:
-                raise TypeError("kv_cur over an E2M1 cache holds 576 values a token in q_abs's dtype")
-        st = _ffi.lib().mla_dcp_decode_partial_fp4(
-            _p(q_abs), _p(q_pe), _p(kv_cache), _p(block_table), _p(seq_lens), _p(kv_cur),
-            B, q_len, H, num_blocks, bs, block_table.shape[1], num_shards, float(scale),
-            float(1.0 if kv_scale is None else kv_scale), _code(q_abs.dtype),
-            _code(o_part.dtype), _p(o_part), _p(lse_part), _p(err_flag), _p(workspace), ws_bytes,
-            int(head_slices), _s(stream))
-        _ffi.check("mla_dcp_decode_partial_fp4", st)
-        return o_part, lse_part
     if is_fp8_cache(kv_cache):
         if kv_cur is not None and not is_fp8_cache(kv_cur):
             raise TypeError("kv_cur must be E4M3 bytes like kv_cache")
@@ -290,25 +279,117 @@ def decode_step(q_abs, q_pe, kv_cache, block_table, seq_lens, W_UV, num_shards: 
 
 
 # ---------------------------------------------------------------- cache operators
-def _on(t: torch.Tensor, dev: torch.device, name: str, dtype=None):
-    """A CUDA tensor on `dev` (the call's stream and launches are on that device)."""
-    if not t.is_cuda or t.device != dev:
-        raise ValueError(f"{name} must be a CUDA tensor on {dev}")
+# Their calls can be as short as a launch, so their host side is kept short: raw
+# pointers and stream handles, device ordinals instead of device objects, and
+# the words of an error only once there is one.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+
+
+def _call(name: str, i: int, stream, *args):
+    """Library call `name` on device i, on `stream` (default: the device's current one)."""
+    fn = getattr(_ffi.lib(), name)
+    s = _raw_stream(i) if stream is None else stream.cuda_stream
+    if _current_device() == i:
+        st = fn(*args, s)
+    else:
+        with torch.cuda.device(i):
+            st = fn(*args, s)
+    if st != 0:
+        raise _ffi.MlaError(name, st)
+
+
+def _ptr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _device(t: torch.Tensor, name: str) -> int:
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.get_device()
+
+
+def _on(t: torch.Tensor, i: int, name: str, dtype=None):
+    """A tensor on device i (the call's stream and launches are on that device)."""
+    if t.get_device() != i:
+        raise ValueError(f"{name} must be a CUDA tensor on device {i}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
 
 
-def _ids(t: torch.Tensor, dev: torch.device, name: str, shape):
-    _on(t, dev, name, torch.int32)
-    if not t.is_contiguous() or tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {tuple(shape)}")
+def _dense(t: torch.Tensor, i: int, name: str, dtype, *shape):
+    """A contiguous tensor of one shape and type on device i."""
+    if t.get_device() != i or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        _on(t, i, name, dtype)
+        raise ValueError(f"{name} must be a contiguous tensor of shape {shape}, not {tuple(t.shape)}")
 
 
-def _err(t: Optional[torch.Tensor], dev: torch.device):
+def _err(t: Optional[torch.Tensor], i: int):
     if t is not None:
-        _on(t, dev, "err_flag", torch.int32)
+        _on(t, i, "err_flag", torch.int32)
         if t.numel() < 1:
             raise ValueError("err_flag must hold one int32")
+
+
+def _partial_fp4(q_abs, q_pe, kv_cache, block_table, seq_lens, num_shards, kv_cur, scale,
+                 part_dtype, o_part, lse_part, err_flag, stream, workspace, head_slices, kv_scale):
+    """mla_dcp_decode_partial over E2M1 pages."""
+    B, q_len, H, _ = q_abs.shape
+    i, dt = _device(q_abs, "q_abs"), q_abs.dtype
+    _dense(q_abs, i, "q_abs", dt, B, q_len, H, D_LATENT)
+    _dense(q_pe, i, "q_pe", dt, B, q_len, H, D_ROPE)
+    num_blocks, bs, _ = kv_cache.shape
+    _dense(kv_cache, i, "kv_cache", torch.uint8, num_blocks, bs, E2M1_ROW)
+    max_blocks = block_table.shape[-1]
+    _dense(block_table, i, "block_table", torch.int32, B, max_blocks)
+    _dense(seq_lens, i, "seq_lens", torch.int32, B)
+    if kv_cur is not None:
+        _dense(kv_cur, i, "kv_cur", dt, B, q_len, D_QK)
+    _err(err_flag, i)
+    P = num_shards + (kv_cur is not None)
+    o_rows = ((B, q_len, P, H) if head_slices == 1
+              else (head_slices, B * q_len, P, H // max(1, head_slices)))
+    if o_part is None:
+        o_part = q_abs.new_empty(o_rows + (D_LATENT,), dtype=part_dtype or dt)
+    else:
+        _dense(o_part, i, "o_part", part_dtype or o_part.dtype, *o_rows, D_LATENT)
+    if lse_part is None:
+        lse_part = q_abs.new_empty(o_rows, dtype=torch.float32)
+    else:
+        _dense(lse_part, i, "lse_part", torch.float32, *o_rows)
+    if isinstance(workspace, str):
+        if workspace != "default":
+            raise ValueError("workspace must be 'default', a tensor or None")
+        workspace = _fp4_workspace(i, B, q_len, num_shards, kv_cur is not None, stream)
+    elif workspace is not None:
+        _on(workspace, i, "workspace")
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+    _call("mla_dcp_decode_partial_fp4", i, stream, q_abs.data_ptr(), q_pe.data_ptr(),
+          kv_cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), _ptr(kv_cur), B, q_len, H,
+          num_blocks, bs, max_blocks, num_shards, scale, kv_scale, _code(dt), _code(o_part.dtype),
+          o_part.data_ptr(), lse_part.data_ptr(), _ptr(err_flag), _ptr(workspace),
+          0 if workspace is None else workspace.numel() * workspace.element_size(), head_slices)
+    return o_part, lse_part
+
+
+_FP4_WORKSPACES = {}
+
+
+def _fp4_workspace(i: int, B: int, q_len: int, num_shards: int, has_current: bool, stream):
+    """The default workspace of mla_dcp_decode_partial_fp4 (see partial_workspace): one per
+    (device, stream); its size depends on the device alone."""
+    key = (i, _raw_stream(i) if stream is None else stream.cuda_stream)
+    ws = _FP4_WORKSPACES.get(key)
+    if ws is None:
+        with torch.cuda.device(i):
+            need = int(_ffi.lib().mla_dcp_decode_partial_fp4_workspace_size(
+                B, q_len, num_shards, 1 if has_current else 0))
+            if need == 0:
+                return None      # invalid sizes: the call itself reports them
+            ws = torch.empty(need, dtype=torch.uint8, device=f"cuda:{i}")
+        _FP4_WORKSPACES[key] = ws
+    return ws
 
 
 def _kv_format(kv_cache: torch.Tensor, dtype: torch.dtype) -> str:
@@ -325,9 +406,12 @@ def _kv_format(kv_cache: torch.Tensor, dtype: torch.dtype) -> str:
     raise TypeError(f"no cache format has rows of {kv_cache.shape[2]} x {kv_cache.dtype} for {dtype}")
 
 
+_SECTIONS = {}     # position sections as C arrays
+
+
 def mla_kv_append(c_kv, k_pe, kv_cache, slots, positions, cos_sin, *, norm_weight=None,
                   eps: float = 1e-6, q_pe=None, q_out=None, kv_out=None, kv_scale=None,
-                  interleaved: bool = True, sections=None, err_flag=None, stream=None):
+                  interleaved: bool = True, sections=(D_ROPE // 2,), err_flag=None, stream=None):
     """Norm, rotate and store new tokens, and rotate their queries, in one launch.
 
     c_kv [T, 512] and k_pe [T, 64] (rows may be strided: views of one
@@ -341,128 +425,122 @@ def mla_kv_append(c_kv, k_pe, kv_cache, slots, positions, cos_sin, *, norm_weigh
     kv_out: None, "new" or a [T, 576] tensor: the rows as the partial call's
     kv_cur (16-bit; E4M3 bytes for an E4M3 cache; over an E2M1 cache the values
     that were stored).  Returns (q_out, kv_out)."""
-    dev, dt = c_kv.device, c_kv.dtype
+    i, dt = _device(c_kv, "c_kv"), c_kv.dtype
     T = c_kv.shape[0]
-    for t, n, w in ((c_kv, "c_kv", D_LATENT), (k_pe, "k_pe", D_ROPE)):
-        _on(t, dev, n, dt)
-        if t.dim() != 2 or tuple(t.shape) != (T, w) or t.stride(1) != 1:
-            raise ValueError(f"{n} must be [T, {w}] with unit stride along its rows")
-    _on(kv_cache, dev, "kv_cache")
+    if (c_kv.shape != (T, D_LATENT) or k_pe.shape != (T, D_ROPE) or c_kv.stride(1) != 1
+            or k_pe.stride(1) != 1):
+        raise ValueError("c_kv must be [T, 512] and k_pe [T, 64] with unit stride along their rows")
+    _on(k_pe, i, "k_pe", dt)
+    _on(kv_cache, i, "kv_cache")
     fmt = _kv_format(kv_cache, dt)
     if fmt == "model" and kv_scale is not None:
         raise TypeError("kv_scale applies to an E4M3 or E2M1 cache only")
-    positions = positions if positions.dim() == 2 else positions.view(1, -1)
-    axes = positions.shape[0]
-    _ids(slots, dev, "slots", (T,))
-    _ids(positions, dev, "positions", (axes, T))
-    sections = [D_ROPE // 2] if sections is None else [int(x) for x in sections]
-    if len(sections) != axes:
-        raise ValueError(f"{len(sections)} sections for {axes} position axes")
-    _on(cos_sin, dev, "cos_sin", torch.float32)
-    if cos_sin.dim() != 2 or cos_sin.shape[1] != D_ROPE or not cos_sin.is_contiguous():
-        raise ValueError("cos_sin must be a contiguous [max_pos, 64] tensor")
+    _dense(slots, i, "slots", torch.int32, T)
+    sections = tuple(sections)
+    axes = len(sections)
+    if positions.dim() == 1:
+        _dense(positions, i, "positions", torch.int32, T)
+        if axes != 1:
+            raise ValueError(f"{axes} sections for one position axis")
+    else:
+        _dense(positions, i, "positions", torch.int32, axes, T)
+    sec = _SECTIONS.get(sections)
+    if sec is None:
+        sec = _SECTIONS[sections] = (ctypes.c_int32 * axes)(*sections)
+    max_pos = cos_sin.shape[0]
+    _dense(cos_sin, i, "cos_sin", torch.float32, max_pos, D_ROPE)
     if norm_weight is not None:
-        _on(norm_weight, dev, "norm_weight", dt)
-        if tuple(norm_weight.shape) != (D_LATENT,) or not norm_weight.is_contiguous():
-            raise ValueError("norm_weight must be a contiguous [512] tensor")
-    _err(err_flag, dev)
-    H, qs, qos = 0, (0, 0), (0, 0)
+        _dense(norm_weight, i, "norm_weight", dt, D_LATENT)
+    _err(err_flag, i)
+    H = qs = qh = os = oh = 0
     if q_pe is not None:
         H = q_pe.shape[1]
-        q_out = torch.empty((T, H, D_ROPE), dtype=dt, device=dev) if q_out is None else q_out
+        if q_out is None:
+            q_out = q_pe.new_empty((T, H, D_ROPE))
         for t, n in ((q_pe, "q_pe"), (q_out, "q_out")):
-            _on(t, dev, n, dt)
-            if t.dim() != 3 or tuple(t.shape) != (T, H, D_ROPE) or t.stride(2) != 1:
+            _on(t, i, n, dt)
+            if t.shape != (T, H, D_ROPE) or t.stride(2) != 1:
                 raise ValueError(f"{n} must be [T, H, 64] with unit stride along its heads")
-        qs, qos = (q_pe.stride(0), q_pe.stride(1)), (q_out.stride(0), q_out.stride(1))
+        (qs, qh, _), (os, oh, _) = q_pe.stride(), q_out.stride()
     elif q_out is not None:
         raise ValueError("q_out without q_pe")
     kv_dt = kv_cache.dtype if fmt == "e4m3" else dt
     if isinstance(kv_out, str):
         if kv_out != "new":
             raise ValueError("kv_out must be None, 'new' or a tensor")
-        kv_out = torch.empty((T, D_QK), dtype=kv_dt, device=dev)
-    if kv_out is not None:
-        _on(kv_out, dev, "kv_out", kv_dt)
+        kv_out = c_kv.new_empty((T, D_QK), dtype=kv_dt)
+    elif kv_out is not None:
+        _on(kv_out, i, "kv_out", kv_dt)
         if kv_out.numel() != T * D_QK or not kv_out.is_contiguous():
             raise ValueError("kv_out must be a contiguous [T, 576] tensor")
-    if T == 0:
-        return q_out, kv_out
-    with torch.cuda.device(dev):
-        st = _ffi.lib().mla_kv_append(
-            _p(c_kv), c_kv.stride(0), _p(k_pe), k_pe.stride(0), _p(norm_weight), float(eps),
-            _p(q_pe), qs[0], qs[1], _p(positions), axes, (ctypes.c_int32 * axes)(*sections),
-            _p(cos_sin), cos_sin.shape[0], 1 if interleaved else 0, _p(slots), T, H,
-            kv_cache.shape[0], kv_cache.shape[1], _code(dt), _ffi.KV_FORMAT[fmt],
-            float(1.0 if kv_scale is None else kv_scale), _p(kv_cache), _p(q_out), qos[0], qos[1],
-            _p(kv_out), _p(err_flag), _s(stream))
-    _ffi.check("mla_kv_append", st)
+    if T > 0:
+        _call("mla_kv_append", i, stream, c_kv.data_ptr(), c_kv.stride(0), k_pe.data_ptr(),
+              k_pe.stride(0), _ptr(norm_weight), eps, _ptr(q_pe), qs, qh, positions.data_ptr(), axes,
+              sec, cos_sin.data_ptr(), max_pos, 1 if interleaved else 0, slots.data_ptr(), T, H,
+              kv_cache.shape[0], kv_cache.shape[1], _code(dt), _ffi.KV_FORMAT[fmt],
+              1.0 if kv_scale is None else kv_scale, kv_cache.data_ptr(), _ptr(q_out), os, oh,
+              _ptr(kv_out), _ptr(err_flag))
     return q_out, kv_out
 
 
 def _pools(kv_cache: torch.Tensor, name: str):
     """(layers, layer stride in bytes, pages, bytes of a page, block size) of a pool
     [num_blocks, bs, W] or the layers' pools [layers, num_blocks, bs, W]."""
-    if not kv_cache.is_cuda or kv_cache.dim() not in (3, 4):
-        raise ValueError(f"{name} must be a CUDA tensor [(layers,) num_blocks, block_size, W]")
-    pool = kv_cache if kv_cache.dim() == 3 else kv_cache[0]
-    if not pool.is_contiguous():
-        raise ValueError(f"the pages of {name} must be contiguous")
+    shape = kv_cache.shape
+    if len(shape) not in (3, 4):
+        raise ValueError(f"{name} must be a tensor [(layers,) num_blocks, block_size, W]")
     size = kv_cache.element_size()
-    layers = 1 if kv_cache.dim() == 3 else kv_cache.shape[0]
-    stride = 0 if kv_cache.dim() == 3 else kv_cache.stride(0) * size
-    if layers > 1 and stride < pool.numel() * size:
+    n, bs, w = shape[-3:]
+    if kv_cache.stride()[-3:] != (bs * w, w, 1):
+        raise ValueError(f"the pages of {name} must be contiguous")
+    layers = 1 if len(shape) == 3 else shape[0]
+    stride = 0 if layers == 1 else kv_cache.stride(0) * size
+    if layers > 1 and stride < n * bs * w * size:
         raise ValueError(f"the layers of {name} overlap")
-    return layers, stride, pool.shape[0], pool.shape[1] * pool.shape[2] * size, pool.shape[1]
+    return layers, stride, n, bs * w * size, bs
 
 
 def mla_kv_copy_pages(src, dst, src_ids, dst_ids, *, err_flag=None, stream=None):
     """Pages src_ids [n] of the pool(s) `src` to pages dst_ids [n] of `dst`, in every layer.
     Pools are [num_blocks, bs, W] or [layers, num_blocks, bs, W] of one format.  dst_ids are
     distinct, and within one pool no page is both source and destination.  Returns dst."""
+    i = _device(src, "src")
     sl, ss, sn, sp, _ = _pools(src, "src")
     dl, ds, dn, dp, _ = _pools(dst, "dst")
     if sl != dl or sp != dp or src.dtype != dst.dtype:
         raise ValueError("src and dst must hold pages of one size and type in as many layers")
     n = src_ids.numel()
-    _on(dst, src.device, "dst")
-    _ids(src_ids, src.device, "src_ids", (n,))
-    _ids(dst_ids, src.device, "dst_ids", (n,))
-    _err(err_flag, src.device)
-    if n == 0:
-        return dst
-    with torch.cuda.device(src.device):
-        st = _ffi.lib().mla_kv_copy_pages(_p(src), ss, sn, _p(dst), ds, dn, sp, sl, _p(src_ids),
-                                          _p(dst_ids), n, _p(err_flag), _s(stream))
-    _ffi.check("mla_kv_copy_pages", st)
+    _on(dst, i, "dst")
+    _dense(src_ids, i, "src_ids", torch.int32, n)
+    _dense(dst_ids, i, "dst_ids", torch.int32, n)
+    _err(err_flag, i)
+    if n > 0:
+        _call("mla_kv_copy_pages", i, stream, src.data_ptr(), ss, sn, dst.data_ptr(), ds, dn, sp, sl,
+              src_ids.data_ptr(), dst_ids.data_ptr(), n, _ptr(err_flag))
     return dst
 
 
 def _page_state(block_table, seq_lens, ref_counts):
-    if not block_table.is_cuda or block_table.dim() != 2:
-        raise ValueError("block_table must be a CUDA tensor [rows, max_blocks]")
-    dev, rows = block_table.device, block_table.shape[0]
-    _ids(block_table, dev, "block_table", block_table.shape)
-    _ids(seq_lens, dev, "seq_lens", (rows,))
-    _ids(ref_counts, dev, "ref_counts", (ref_counts.numel(),))
-    return dev, rows
+    i = _device(block_table, "block_table")
+    R, max_blocks = block_table.shape
+    _dense(block_table, i, "block_table", torch.int32, R, max_blocks)
+    _dense(seq_lens, i, "seq_lens", torch.int32, R)
+    pages = ref_counts.numel()
+    _dense(ref_counts, i, "ref_counts", torch.int32, pages)
+    return i, R, max_blocks, pages
 
 
 def mla_kv_free(block_table, seq_lens, ref_counts, rows, *, block_size: int, err_flag=None,
                 stream=None):
     """Give the pages of the rows [n] (int32) of block_table [R, max_blocks] back: their
     ref_counts [num_blocks] go down, their entries become -1 and their seq_lens 0."""
-    dev, R = _page_state(block_table, seq_lens, ref_counts)
+    i, R, max_blocks, pages = _page_state(block_table, seq_lens, ref_counts)
     n = rows.numel()
-    _ids(rows, dev, "rows", (n,))
-    _err(err_flag, dev)
-    if n == 0:
-        return
-    with torch.cuda.device(dev):
-        st = _ffi.lib().mla_kv_free(_p(block_table), _p(seq_lens), _p(ref_counts), _p(rows), n, R,
-                                    ref_counts.numel(), int(block_size), block_table.shape[1],
-                                    _p(err_flag), _s(stream))
-    _ffi.check("mla_kv_free", st)
+    _dense(rows, i, "rows", torch.int32, n)
+    _err(err_flag, i)
+    if n > 0:
+        _call("mla_kv_free", i, stream, block_table.data_ptr(), seq_lens.data_ptr(),
+              ref_counts.data_ptr(), rows.data_ptr(), n, R, pages, block_size, max_blocks, _ptr(err_flag))
 
 
 def mla_kv_fork(kv_cache, block_table, seq_lens, ref_counts, parents, children, *,
@@ -472,31 +550,32 @@ def mla_kv_fork(kv_cache, block_table, seq_lens, ref_counts, parents, children, 
     kv_cache ([num_blocks, bs, W] or [layers, num_blocks, bs, W]) to the lowest free page.
     workspace: a tensor of mla_kv_fork_workspace_size(n) bytes for this call alone (default:
     a new one; give one to keep when capturing into a graph)."""
-    dev, R = _page_state(block_table, seq_lens, ref_counts)
+    i, R, max_blocks, num_blocks = _page_state(block_table, seq_lens, ref_counts)
     layers, stride, pages, page_bytes, bs = _pools(kv_cache, "kv_cache")
-    _on(kv_cache, dev, "kv_cache")
-    if pages != ref_counts.numel():
-        raise ValueError(f"ref_counts of {ref_counts.numel()} pages for a pool of {pages}")
+    _on(kv_cache, i, "kv_cache")
+    if pages != num_blocks:
+        raise ValueError(f"ref_counts of {num_blocks} pages for a pool of {pages}")
     n = parents.numel()
-    _ids(parents, dev, "parents", (n,))
-    _ids(children, dev, "children", (n,))
-    _err(err_flag, dev)
+    _dense(parents, i, "parents", torch.int32, n)
+    _dense(children, i, "children", torch.int32, n)
+    _err(err_flag, i)
     if n == 0:
         return
-    with torch.cuda.device(dev):
-        s = stream if stream is not None else torch.cuda.current_stream()
-        need = int(_ffi.lib().mla_kv_fork_workspace_size(n))
-        if workspace is None:
-            with torch.cuda.stream(s):     # freed in the order of the stream that uses it
-                workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+    if workspace is None:
+        need = max(16, int(_ffi.lib().mla_kv_fork_workspace_size(n)))
+        if stream is None:
+            workspace = block_table.new_empty(need, dtype=torch.uint8)
         else:
-            _on(workspace, dev, "workspace")
-            _need(workspace, "workspace")
-        st = _ffi.lib().mla_kv_fork(
-            _p(kv_cache), stride, page_bytes, layers, _p(block_table), _p(seq_lens),
-            _p(ref_counts), _p(parents), _p(children), n, R, pages, bs, block_table.shape[1],
-            _p(workspace), workspace.numel() * workspace.element_size(), _p(err_flag), _s(s))
-    _ffi.check("mla_kv_fork", st)
+            with torch.cuda.stream(stream):     # freed in the order of the stream that uses it
+                workspace = block_table.new_empty(need, dtype=torch.uint8)
+    else:
+        _on(workspace, i, "workspace")
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+    _call("mla_kv_fork", i, stream, kv_cache.data_ptr(), stride, page_bytes, layers,
+          block_table.data_ptr(), seq_lens.data_ptr(), ref_counts.data_ptr(), parents.data_ptr(),
+          children.data_ptr(), n, R, num_blocks, bs, max_blocks, workspace.data_ptr(),
+          workspace.numel() * workspace.element_size(), _ptr(err_flag))
 
 
 def torch_dtype(name: str) -> torch.dtype:
