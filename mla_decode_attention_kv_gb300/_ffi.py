@@ -69,6 +69,8 @@ class MlaError(RuntimeError):
 def lib(path: str | None = None):
     """Load libmla_dcp.so (built in-tree by ``build.build()``)."""
     global _LIB
+    if _LIB is not None:
+        return _LIB
     with _LOCK:
         if _LIB is None:
             path = path or _build.LIB_PATH

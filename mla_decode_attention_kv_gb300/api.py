@@ -350,11 +350,11 @@ def _partial_fp4(q_abs, q_pe, kv_cache, block_table, seq_lens, num_shards, kv_cu
     o_rows = ((B, q_len, P, H) if head_slices == 1
               else (head_slices, B * q_len, P, H // max(1, head_slices)))
     if o_part is None:
-        o_part = q_abs.new_empty(o_rows + (D_LATENT,), dtype=part_dtype or dt)
+        o_part = torch.empty(o_rows + (D_LATENT,), dtype=part_dtype or dt, device=q_abs.device)
     else:
         _dense(o_part, i, "o_part", part_dtype or o_part.dtype, *o_rows, D_LATENT)
     if lse_part is None:
-        lse_part = q_abs.new_empty(o_rows, dtype=torch.float32)
+        lse_part = torch.empty(o_rows, dtype=torch.float32, device=q_abs.device)
     else:
         _dense(lse_part, i, "lse_part", torch.float32, *o_rows)
     if isinstance(workspace, str):
@@ -426,9 +426,9 @@ def mla_kv_append(c_kv, k_pe, kv_cache, slots, positions, cos_sin, *, norm_weigh
     kv_cur (16-bit; E4M3 bytes for an E4M3 cache; over an E2M1 cache the values
     that were stored).  Returns (q_out, kv_out)."""
     i, dt = _device(c_kv, "c_kv"), c_kv.dtype
-    T = c_kv.shape[0]
-    if (c_kv.shape != (T, D_LATENT) or k_pe.shape != (T, D_ROPE) or c_kv.stride(1) != 1
-            or k_pe.stride(1) != 1):
+    T, w = c_kv.shape
+    (cs, c1), (ks, k1) = c_kv.stride(), k_pe.stride()
+    if w != D_LATENT or k_pe.shape != (T, D_ROPE) or c1 != 1 or k1 != 1:
         raise ValueError("c_kv must be [T, 512] and k_pe [T, 64] with unit stride along their rows")
     _on(k_pe, i, "k_pe", dt)
     _on(kv_cache, i, "kv_cache")
@@ -455,27 +455,32 @@ def mla_kv_append(c_kv, k_pe, kv_cache, slots, positions, cos_sin, *, norm_weigh
     H = qs = qh = os = oh = 0
     if q_pe is not None:
         H = q_pe.shape[1]
+        qs, qh, q1 = q_pe.stride()
+        _on(q_pe, i, "q_pe", dt)
+        if q_pe.shape != (T, H, D_ROPE) or q1 != 1:
+            raise ValueError("q_pe must be [T, H, 64] with unit stride along its heads")
         if q_out is None:
-            q_out = q_pe.new_empty((T, H, D_ROPE))
-        for t, n in ((q_pe, "q_pe"), (q_out, "q_out")):
-            _on(t, i, n, dt)
-            if t.shape != (T, H, D_ROPE) or t.stride(2) != 1:
-                raise ValueError(f"{n} must be [T, H, 64] with unit stride along its heads")
-        (qs, qh, _), (os, oh, _) = q_pe.stride(), q_out.stride()
+            q_out = torch.empty((T, H, D_ROPE), dtype=dt, device=c_kv.device)
+            os, oh = H * D_ROPE, D_ROPE
+        else:
+            os, oh, q1 = q_out.stride()
+            _on(q_out, i, "q_out", dt)
+            if q_out.shape != (T, H, D_ROPE) or q1 != 1:
+                raise ValueError("q_out must be [T, H, 64] with unit stride along its heads")
     elif q_out is not None:
         raise ValueError("q_out without q_pe")
     kv_dt = kv_cache.dtype if fmt == "e4m3" else dt
     if isinstance(kv_out, str):
         if kv_out != "new":
             raise ValueError("kv_out must be None, 'new' or a tensor")
-        kv_out = c_kv.new_empty((T, D_QK), dtype=kv_dt)
+        kv_out = torch.empty((T, D_QK), dtype=kv_dt, device=c_kv.device)
     elif kv_out is not None:
         _on(kv_out, i, "kv_out", kv_dt)
         if kv_out.numel() != T * D_QK or not kv_out.is_contiguous():
             raise ValueError("kv_out must be a contiguous [T, 576] tensor")
     if T > 0:
-        _call("mla_kv_append", i, stream, c_kv.data_ptr(), c_kv.stride(0), k_pe.data_ptr(),
-              k_pe.stride(0), _ptr(norm_weight), eps, _ptr(q_pe), qs, qh, positions.data_ptr(), axes,
+        _call("mla_kv_append", i, stream, c_kv.data_ptr(), cs, k_pe.data_ptr(), ks,
+              _ptr(norm_weight), eps, _ptr(q_pe), qs, qh, positions.data_ptr(), axes,
               sec, cos_sin.data_ptr(), max_pos, 1 if interleaved else 0, slots.data_ptr(), T, H,
               kv_cache.shape[0], kv_cache.shape[1], _code(dt), _ffi.KV_FORMAT[fmt],
               1.0 if kv_scale is None else kv_scale, kv_cache.data_ptr(), _ptr(q_out), os, oh,
@@ -564,10 +569,10 @@ def mla_kv_fork(kv_cache, block_table, seq_lens, ref_counts, parents, children, 
     if workspace is None:
         need = max(16, int(_ffi.lib().mla_kv_fork_workspace_size(n)))
         if stream is None:
-            workspace = block_table.new_empty(need, dtype=torch.uint8)
+            workspace = torch.empty(need, dtype=torch.uint8, device=block_table.device)
         else:
             with torch.cuda.stream(stream):     # freed in the order of the stream that uses it
-                workspace = block_table.new_empty(need, dtype=torch.uint8)
+                workspace = torch.empty(need, dtype=torch.uint8, device=block_table.device)
     else:
         _on(workspace, i, "workspace")
         if not workspace.is_contiguous():
