@@ -25,7 +25,7 @@
 // lane l owns latents 16 l .. 16 l + 15, which are one block of the E2M1 form,
 // so a block's maximum and its 8 bytes of codes stay in a lane; the key's pair
 // l belongs to lane l.  The queries go to blocks of their own, eight lanes a
-// head, 16 bytes a lane.
+// head, 16 bytes a lane, four heads of a token per lane.
 #include <cuda_fp4.h>
 #include <cuda_fp8.h>
 #include "cache_kernels.cuh"
@@ -113,23 +113,44 @@ __device__ __forceinline__ uint32_t block_scale(float amax, bool nan, float kv6)
   return nan ? 0x7Fu : to_e4m3(div_odd(amax, kv6));
 }
 
-// E2M1 codes of two values in a byte (the first in the low half); d = scale *
-// kv_scale of their block.  Values past 6 d saturate, the sign of a zero stays.
-__device__ __forceinline__ uint32_t e2m1_pair(float a, float b, float d) {
-  float x = 0.f, y = 0.f;
-  if (d > 0.f) {
-    x = div_odd(fabsf(a), d);
-    y = div_odd(fabsf(b), d);
-  }
-  const uint32_t m = __nv_cvt_float2_to_fp4x2(make_float2(x, y), __NV_E2M1, cudaRoundNearest);
+__device__ __forceinline__ uint32_t to_e2m1x2(float x, float y) {   // x in the low half
+  return __nv_cvt_float2_to_fp4x2(make_float2(x, y), __NV_E2M1, cudaRoundNearest);
+}
+
+// Block scale of E2M1 codes: d = s * kv_scale and its reciprocal (0 for d = 0,
+// so that every code is 0).
+struct Scale {
+  float d, r;
+};
+
+__device__ __forceinline__ Scale make_scale(uint32_t sb, float kv_scale) {
+  const float d = from_e4m3(sb) * kv_scale;
+  return {d, d > 0.f ? __frcp_rn(d) : 0.f};
+}
+
+// The exact form: the magnitudes' quotients rounded to odd.
+__device__ __noinline__ uint32_t e2m1_exact(float a, float b, float da, float db) {
+  return to_e2m1x2(div_odd(fabsf(a), da), div_odd(fabsf(b), db));
+}
+
+// E2M1 codes of two values in a byte (the first in the low half).  Values past
+// 6 d saturate, the sign of a zero stays.  The products with the reciprocals
+// are off by less than 2^-22 of themselves, so where a little less and a little
+// more than they are round to the same codes, those are the codes; else (a
+// quotient within 2^-21 of a border) the exact form decides.
+__device__ __forceinline__ uint32_t e2m1_pair(float a, float b, Scale sa, Scale sb) {
+  constexpr float kLess = 1.f - 0x1p-21f, kMore = 1.f + 0x1p-21f;
+  const float x = fabsf(a) * sa.r, y = fabsf(b) * sb.r;
+  uint32_t m = to_e2m1x2(x * kLess, y * kLess);
+  if (m != to_e2m1x2(x * kMore, y * kMore)) m = e2m1_exact(a, b, sa.d, sb.d);
   return (m & 0x77u) | ((__float_as_uint(a) >> 28) & 8u) | ((__float_as_uint(b) >> 24) & 0x80u);
 }
 
-// Value of one E2M1 code (the format's eight magnitudes).
-__device__ __forceinline__ float e2m1_value(uint32_t c) {
-  const uint32_t e = (c >> 1) & 3u, m = c & 1u;
-  const float mag = e == 0 ? 0.5f * m : __uint_as_float((126u + e) << 23) * (1.f + 0.5f * m);
-  return (c & 8u) ? -mag : mag;
+// The values of a byte's two codes.
+__device__ __forceinline__ float2 e2m1_values(uint32_t c) {
+  uint32_t h;
+  asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %1;\n cvt.rn.f16x2.e2m1x2 %0, a;\n}\n" : "=r"(h) : "r"(c));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
 // Position of RoPE pair i of token t: that of the axis its section belongs to.
@@ -248,14 +269,14 @@ __device__ void append_row(const AppendParams& ap, int t, int lane) {
         nan |= y[k] != y[k];
       }
       const uint32_t sb = block_scale(am, nan, ap.kv6);
-      const float d = from_e4m3(sb) * ap.kv_scale;
+      const Scale sc = make_scale(sb, ap.kv_scale);
       uint32_t code[2] = {0, 0};
 #pragma unroll
-      for (int k = 0; k < 8; ++k) code[k >> 2] |= e2m1_pair(y[2 * k], y[2 * k + 1], d) << (8 * (k & 3));
-#pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const uint32_t c = code[k >> 2] >> (8 * (k & 3));
-        w[k] = pack2<BF16>(e2m1_value(c & 15u) * d, e2m1_value((c >> 4) & 15u) * d);
+        const uint32_t c = e2m1_pair(y[2 * k], y[2 * k + 1], sc, sc);
+        code[k >> 2] |= c << (8 * (k & 3));
+        const float2 v = e2m1_values(c);
+        w[k] = pack2<BF16>(v.x * sc.d, v.y * sc.d);
       }
       // key: a block is 8 lanes' pairs (interleaved) or 16 lanes' first or
       // second values (halves)
@@ -278,11 +299,12 @@ __device__ void append_row(const AppendParams& ap, int t, int lane) {
         }
       }
       const uint32_t sb0 = block_scale(a0, n0, ap.kv6), sb1 = block_scale(a1, n1, ap.kv6);
-      const float d0 = from_e4m3(sb0) * ap.kv_scale, d1 = from_e4m3(sb1) * ap.kv_scale;
-      uint32_t kc = ap.interleaved ? e2m1_pair(r0, r1, d0)
-                                   : ((e2m1_pair(r0, 0.f, d0) & 15u) | (e2m1_pair(r1, 0.f, d1) << 4));
-      q0 = e2m1_value(kc & 15u) * d0;
-      q1 = e2m1_value(kc >> 4) * (ap.interleaved ? d0 : d1);
+      // (interleaved: both values' blocks are one)
+      const Scale s0 = make_scale(sb0, ap.kv_scale), s1 = make_scale(sb1, ap.kv_scale);
+      const uint32_t kc = e2m1_pair(r0, r1, s0, s1);
+      const float2 kv = e2m1_values(kc);
+      q0 = kv.x * s0.d;
+      q1 = kv.y * s1.d;
       // scales of four lanes in a word: lane 4 j writes blocks 4 j .. 4 j + 3
       uint32_t sw = sb;
       sw |= __shfl_down_sync(0xffffffffu, sw, 1) << 8;
@@ -353,29 +375,31 @@ __device__ void append_row(const AppendParams& ap, int t, int lane) {
   }
 }
 
-// Four RoPE pairs of one head's query: pairs 4 j .. 4 j + 3 for lane j of the
-// head's eight.
+// Up to kQueryHeads heads of one token's queries, by one warp: lane j of a
+// head's eight has pairs 4 j .. 4 j + 3, and the same pairs of every fourth
+// head, so the cosines are read once and all heads' loads are in flight with
+// them.
 template <bool BF16>
-__device__ void rotate_query(const AppendParams& ap, int64_t item, int j) {
-  const int t = static_cast<int>(item / ap.H), h = static_cast<int>(item - static_cast<int64_t>(t) * ap.H);
-  const uint16_t* src = static_cast<const uint16_t*>(ap.q_pe) + t * ap.q_stride + h * ap.q_head_stride;
-  uint16_t* dst = static_cast<uint16_t*>(ap.q_out) + t * ap.qo_stride + h * ap.qo_head_stride;
-  float a[4], b[4];
-  if (ap.interleaved) {
-    const uint4 x = *reinterpret_cast<const uint4*>(src + 8 * j);
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+__device__ void rotate_queries(const AppendParams& ap, int64_t item, int lane) {
+  const int t = static_cast<int>(item / ap.q_groups);
+  const int h0 = static_cast<int>(item - static_cast<int64_t>(t) * ap.q_groups) * kQueryHeads + (lane >> 3);
+  const int j = lane & 7;
+  const uint16_t* src = static_cast<const uint16_t*>(ap.q_pe) + t * ap.q_stride;
+  uint16_t* dst = static_cast<uint16_t*>(ap.q_out) + t * ap.qo_stride;
+  constexpr int kN = kQueryHeads / 4;
+  uint2 x[kN] = {}, z[kN] = {};
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float2 f = unpack<BF16>(w[k]);
-      a[k] = f.x;
-      b[k] = f.y;
+  for (int n = 0; n < kN; ++n) {
+    const int h = h0 + 4 * n;
+    if (h >= ap.H) continue;
+    if (ap.interleaved) {
+      const uint4 v = *reinterpret_cast<const uint4*>(src + h * ap.q_head_stride + 8 * j);
+      x[n] = make_uint2(v.x, v.y);
+      z[n] = make_uint2(v.z, v.w);
+    } else {
+      x[n] = *reinterpret_cast<const uint2*>(src + h * ap.q_head_stride + 4 * j);
+      z[n] = *reinterpret_cast<const uint2*>(src + h * ap.q_head_stride + 32 + 4 * j);
     }
-  } else {
-    const uint2 x = *reinterpret_cast<const uint2*>(src + 4 * j);
-    const uint2 z = *reinterpret_cast<const uint2*>(src + 32 + 4 * j);
-    const float2 x0 = unpack<BF16>(x.x), x1 = unpack<BF16>(x.y), z0 = unpack<BF16>(z.x), z1 = unpack<BF16>(z.y);
-    a[0] = x0.x; a[1] = x0.y; a[2] = x1.x; a[3] = x1.y;
-    b[0] = z0.x; b[1] = z0.y; b[2] = z1.x; b[3] = z1.y;
   }
   float4 co, si;
   const int i0 = 4 * j;
@@ -397,32 +421,41 @@ __device__ void rotate_query(const AppendParams& ap, int64_t item, int j) {
     si = make_float4(s[0], s[1], s[2], s[3]);
   }
   const float c[4] = {co.x, co.y, co.z, co.w}, s[4] = {si.x, si.y, si.z, si.w};
-  float u[4], v[4];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    u[k] = fmaf(a[k], c[k], -(b[k] * s[k]));
-    v[k] = fmaf(a[k], s[k], b[k] * c[k]);
-  }
-  if (ap.interleaved) {
-    *reinterpret_cast<uint4*>(dst + 8 * j) =
-        make_uint4(pack2<BF16>(u[0], v[0]), pack2<BF16>(u[1], v[1]), pack2<BF16>(u[2], v[2]), pack2<BF16>(u[3], v[3]));
-  } else {
-    *reinterpret_cast<uint2*>(dst + 4 * j) = make_uint2(pack2<BF16>(u[0], u[1]), pack2<BF16>(u[2], u[3]));
-    *reinterpret_cast<uint2*>(dst + 32 + 4 * j) = make_uint2(pack2<BF16>(v[0], v[1]), pack2<BF16>(v[2], v[3]));
+  for (int n = 0; n < kN; ++n) {
+    const int h = h0 + 4 * n;
+    if (h >= ap.H) continue;
+    const float2 f0 = unpack<BF16>(x[n].x), f1 = unpack<BF16>(x[n].y), f2 = unpack<BF16>(z[n].x), f3 = unpack<BF16>(z[n].y);
+    const float e[8] = {f0.x, f0.y, f1.x, f1.y, f2.x, f2.y, f3.x, f3.y};
+    float u[4], v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float a = ap.interleaved ? e[2 * k] : e[k], b = ap.interleaved ? e[2 * k + 1] : e[4 + k];
+      u[k] = fmaf(a, c[k], -(b * s[k]));
+      v[k] = fmaf(a, s[k], b * c[k]);
+    }
+    uint16_t* row = dst + h * ap.qo_head_stride;
+    if (ap.interleaved) {
+      *reinterpret_cast<uint4*>(row + 8 * j) =
+          make_uint4(pack2<BF16>(u[0], v[0]), pack2<BF16>(u[1], v[1]), pack2<BF16>(u[2], v[2]), pack2<BF16>(u[3], v[3]));
+    } else {
+      *reinterpret_cast<uint2*>(row + 4 * j) = make_uint2(pack2<BF16>(u[0], u[1]), pack2<BF16>(u[2], u[3]));
+      *reinterpret_cast<uint2*>(row + 32 + 4 * j) = make_uint2(pack2<BF16>(v[0], v[1]), pack2<BF16>(v[2], v[3]));
+    }
   }
 }
 
 }  // namespace
 
 template <bool BF16, int KIND>
-__global__ void __launch_bounds__(kAppendThreads) mla_kv_append_kernel(const AppendParams ap) {
+__global__ void __launch_bounds__(kAppendThreads, 4) mla_kv_append_kernel(const AppendParams ap) {
   const int blk = static_cast<int>(blockIdx.x);
   if (blk < ap.row_blocks) {
     const int t = blk * (kAppendThreads / 32) + (threadIdx.x >> 5);
     if (t < ap.T) append_row<BF16, KIND>(ap, t, threadIdx.x & 31);
   } else {
-    const int64_t item = static_cast<int64_t>(blk - ap.row_blocks) * (kAppendThreads / 8) + (threadIdx.x >> 3);
-    if (item < static_cast<int64_t>(ap.T) * ap.H) rotate_query<BF16>(ap, item, threadIdx.x & 7);
+    const int64_t item = static_cast<int64_t>(blk - ap.row_blocks) * (kAppendThreads / 32) + (threadIdx.x >> 5);
+    if (item < static_cast<int64_t>(ap.T) * ap.q_groups) rotate_queries<BF16>(ap, item, threadIdx.x & 31);
   }
 }
 
@@ -437,8 +470,8 @@ static int launch_append_t(const AppendParams& ap, int kind, unsigned blocks, cu
 
 int launch_append(AppendParams ap, int kind, bool bf16, cudaStream_t stream) {
   ap.row_blocks = ceil_div(ap.T, kAppendThreads / 32);
-  const int64_t heads = ap.q_pe ? static_cast<int64_t>(ap.T) * ap.H : 0;
-  const int64_t blocks = ap.row_blocks + (heads + kAppendThreads / 8 - 1) / (kAppendThreads / 8);
+  ap.q_groups = ap.q_pe ? ceil_div(ap.H, kQueryHeads) : 0;
+  const int64_t blocks = ap.row_blocks + (static_cast<int64_t>(ap.T) * ap.q_groups + kAppendThreads / 32 - 1) / (kAppendThreads / 32);
   return bf16 ? launch_append_t<true>(ap, kind, static_cast<unsigned>(blocks), stream)
               : launch_append_t<false>(ap, kind, static_cast<unsigned>(blocks), stream);
 }

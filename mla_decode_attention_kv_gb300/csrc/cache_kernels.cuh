@@ -16,6 +16,7 @@ constexpr int kE2m1Scales = 36;
 constexpr int kE2m1Row = kE2m1Codes + kE2m1Scales;
 
 constexpr int kAppendThreads = 256;
+constexpr int kQueryHeads = 16;         // heads of one token that a warp rotates
 constexpr int kMaxForkRows = 65536;   // rows of a block table that mla_kv_fork takes
 
 struct AppendParams {
@@ -35,7 +36,7 @@ struct AppendParams {
   int sec1, sec2;          // first pair of the second and of the third axis (32: none)
   int interleaved;
   float eps, kv_scale, kv6;   // kv6 = 6 kv_scale
-  int row_blocks;
+  int row_blocks, q_groups;   // blocks that make rows; warps per token that rotate queries
 };
 int launch_append(AppendParams ap, int kind, bool bf16, cudaStream_t stream);
 
