@@ -666,6 +666,8 @@ int mla_kv_append(const void* c_kv, int64_t c_stride, const void* k_pe, int64_t 
   ap.eps = eps;
   ap.kv_scale = kv_scale;
   ap.kv6 = 6.f * kv_scale;
+  ap.inv_kv = 1.f / kv_scale;
+  ap.inv_kv6 = 1.f / ap.kv6;
   ap.row_blocks = 0;
   return launched(mla::launch_append(ap, kv_format, dtype == MLA_BF16, reinterpret_cast<cudaStream_t>(stream)));
 }

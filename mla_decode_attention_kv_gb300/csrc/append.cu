@@ -11,14 +11,17 @@
 // axes (time, height, width) a pair reads the row of its section's position.
 //
 // What is stored in 8 or 4 bits is the nearest code of the value itself.  A
-// value computed in one fp32 step is off by 2^-24 or so and lands, once in a
-// few million values, on the wrong side of a border between two 4-bit codes
-// that lie a third of their size apart; the cache would then depend on the
-// order of a sum.  So row values are carried as unevaluated sums hi + lo of
-// two fp32 numbers (sums and products with their exact errors, Dekker and
-// Knuth), about 2^-46 off, and each rounding to fewer bits sees hi with lo
-// folded into its last bit (round to odd), which rounds the same way as hi +
-// lo itself.  It is 15-odd fp32 operations a value, below the memory's time.
+// value computed in plain fp32 is off by up to 2^-19 (the sum of squares) and
+// lands, once in a few million values, on the wrong side of a border between
+// two 4-bit codes that lie a third of their size apart; the cache would then
+// depend on the order of a sum.  So a row is made twice over: in fp32, where
+// each code is taken at a little less and a little more (2^-18) than the value,
+// and, where some code of the row differs (a row in some 200 for E2M1, in 15
+// for E4M3), again exactly: values as unevaluated sums hi + lo of two fp32
+// numbers (sums and products with their exact errors, Dekker and Knuth), about
+// 2^-46 off, rounded with lo folded into the last bit of hi (round to odd),
+// which rounds on to fewer bits the same way as hi + lo itself.  16-bit rows
+// are always made the exact way.
 //
 // What bounds it: bytes (the queries' 256 bytes per head and token, read and
 // written once), and the launch for few tokens.  One warp makes a token's row:
@@ -26,7 +29,6 @@
 // so a block's maximum and its 8 bytes of codes stay in a lane; the key's pair
 // l belongs to lane l.  The queries go to blocks of their own, eight lanes a
 // head, 16 bytes a lane, four heads of a token per lane.
-#include <cuda_fp4.h>
 #include <cuda_fp8.h>
 #include "cache_kernels.cuh"
 #include "common.cuh"
@@ -108,49 +110,75 @@ __device__ __forceinline__ float from_e4m3(uint32_t b) {
   return __half2float(*reinterpret_cast<const __half*>(&h));
 }
 
-// E4M3 byte of a block's scale, max / (6 kv_scale); NaN where a value is NaN
-__device__ __forceinline__ uint32_t block_scale(float amax, bool nan, float kv6) {
-  return nan ? 0x7Fu : to_e4m3(div_odd(amax, kv6));
+// Four E4M3 bytes of four values, and eight E2M1 codes of eight (the first in
+// the low bits; rounded to nearest even, saturating, zeros with their signs).
+// One block of PTX each: through the headers' byte types the packing takes
+// several times the conversions' instructions.
+__device__ __forceinline__ uint32_t to_e4m3x4(const float* v, float m) {
+  uint32_t o;
+  asm("{\n .reg .b16 a, b;\n cvt.rn.satfinite.e4m3x2.f32 a, %2, %1;\n cvt.rn.satfinite.e4m3x2.f32 b, %4, %3;\n"
+      " mov.b32 %0, {a, b};\n}\n"
+      : "=r"(o)
+      : "f"(v[0] * m), "f"(v[1] * m), "f"(v[2] * m), "f"(v[3] * m));
+  return o;
+}
+
+__device__ __forceinline__ uint32_t to_e2m1x8(const float* v, float m) {
+  uint32_t o;
+  asm("{\n .reg .b8 a, b, c, d;\n cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n mov.b32 %0, {a, b, c, d};\n}\n"
+      : "=r"(o)
+      : "f"(v[0] * m), "f"(v[1] * m), "f"(v[2] * m), "f"(v[3] * m), "f"(v[4] * m), "f"(v[5] * m), "f"(v[6] * m),
+        "f"(v[7] * m));
+  return o;
 }
 
 __device__ __forceinline__ uint32_t to_e2m1x2(float x, float y) {   // x in the low half
-  return __nv_cvt_float2_to_fp4x2(make_float2(x, y), __NV_E2M1, cudaRoundNearest);
+  uint32_t o;
+  asm("{\n .reg .b8 a, z;\n mov.b16 {a, z}, 0;\n cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n mov.b32 %0, {a, z, z, z};\n}\n"
+      : "=r"(o)
+      : "f"(x), "f"(y));
+  return o;
 }
 
-// Block scale of E2M1 codes: d = s * kv_scale and its reciprocal (0 for d = 0,
-// so that every code is 0).
-struct Scale {
-  float d, r;
-};
+// A little less and a little more than a value: the bounds of its fp32 error.
+constexpr float kLess = 1.f - 0x1p-18f, kMore = 1.f + 0x1p-18f;
 
-__device__ __forceinline__ Scale make_scale(uint32_t sb, float kv_scale) {
-  const float d = from_e4m3(sb) * kv_scale;
-  return {d, d > 0.f ? __frcp_rn(d) : 0.f};
+// E4M3 byte of a block's scale, max / (6 kv_scale); NaN where a value is NaN.
+// EXACT: amax is rounded to odd.  Otherwise `same` turns false where amax's
+// error could change the byte.
+template <bool EXACT>
+__device__ __forceinline__ uint32_t block_scale(float amax, bool nan, const AppendParams& ap, bool& same) {
+  uint32_t b;
+  if constexpr (EXACT) {
+    b = to_e4m3(div_odd(amax, ap.kv6));
+  } else {
+    const float q = amax * ap.inv_kv6;
+    b = to_e4m3(q * kLess);
+    same &= b == to_e4m3(q * kMore);
+  }
+  return nan ? 0x7Fu : b;
 }
 
-// The exact form: the magnitudes' quotients rounded to odd.
-__device__ __noinline__ uint32_t e2m1_exact(float a, float b, float da, float db) {
-  return to_e2m1x2(div_odd(fabsf(a), da), div_odd(fabsf(b), db));
+// The signed quotient v / d rounded to odd, 0 (with v's sign) for d = 0.
+__device__ __forceinline__ float div_signed(float v, float d) {
+  return copysignf(d > 0.f ? div_odd(fabsf(v), d) : 0.f, v);
 }
 
-// E2M1 codes of two values in a byte (the first in the low half).  Values past
-// 6 d saturate, the sign of a zero stays.  The products with the reciprocals
-// are off by less than 2^-22 of themselves, so where a little less and a little
-// more than they are round to the same codes, those are the codes; else (a
-// quotient within 2^-21 of a border) the exact form decides.
-__device__ __forceinline__ uint32_t e2m1_pair(float a, float b, Scale sa, Scale sb) {
-  constexpr float kLess = 1.f - 0x1p-21f, kMore = 1.f + 0x1p-21f;
-  const float x = fabsf(a) * sa.r, y = fabsf(b) * sb.r;
-  uint32_t m = to_e2m1x2(x * kLess, y * kLess);
-  if (m != to_e2m1x2(x * kMore, y * kMore)) m = e2m1_exact(a, b, sa.d, sb.d);
-  return (m & 0x77u) | ((__float_as_uint(a) >> 28) & 8u) | ((__float_as_uint(b) >> 24) & 0x80u);
-}
-
-// The values of a byte's two codes.
-__device__ __forceinline__ float2 e2m1_values(uint32_t c) {
-  uint32_t h;
-  asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %1;\n cvt.rn.f16x2.e2m1x2 %0, a;\n}\n" : "=r"(h) : "r"(c));
-  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+// The values of four bytes of codes, times d, as 16-bit pairs.
+template <bool BF16>
+__device__ __forceinline__ void e2m1_values(uint32_t c, float d, uint32_t* w) {
+  uint32_t h[4];
+  asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %4;\n"
+      " cvt.rn.f16x2.e2m1x2 %0, a;\n cvt.rn.f16x2.e2m1x2 %1, b;\n"
+      " cvt.rn.f16x2.e2m1x2 %2, c;\n cvt.rn.f16x2.e2m1x2 %3, d;\n}\n"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(c));
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[k]));
+    w[k] = pack2<BF16>(f.x * d, f.y * d);
+  }
 }
 
 // Position of RoPE pair i of token t: that of the axis its section belongs to.
@@ -165,9 +193,10 @@ __device__ __forceinline__ int pair_position(const AppendParams& ap, int t, int 
   return pos;
 }
 
-// One token's row, by one warp.
-template <bool BF16, int KIND>
-__device__ void append_row(const AppendParams& ap, int t, int lane) {
+// One token's row, by one warp.  EXACT false: false, with nothing stored, if
+// some code of the row needs the exact form.
+template <bool BF16, int KIND, bool EXACT>
+__device__ __forceinline__ bool append_row(const AppendParams& ap, int t, int lane) {
   // ---- latent: 16 values a lane
   uint32_t cw[8];
   {
@@ -192,48 +221,69 @@ __device__ void append_row(const AppendParams& ap, int t, int lane) {
   const float co = __ldg(cs + lane), si = __ldg(cs + 32 + lane);
   const int slot = __ldg(ap.slots + t);
 
-  float y[16];   // the row's values, rounded to odd
+  float y[16];   // the row's values (EXACT: rounded to odd)
+  bool same = true;
   if (ap.weight) {
     uint32_t ww[8];
     const uint4* wsrc = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(ap.weight) + 16 * lane);
     const uint4 a = __ldg(wsrc), b = __ldg(wsrc + 1);
     ww[0] = a.x; ww[1] = a.y; ww[2] = a.z; ww[3] = a.w;
     ww[4] = b.x; ww[5] = b.y; ww[6] = b.z; ww[7] = b.w;
-    // sum of squares: the squares of 16-bit values are exact in fp32, each
-    // addition's error is kept
-    float s = 0.f, e = 0.f;
+    if constexpr (EXACT) {
+      // sum of squares: the squares of 16-bit values are exact in fp32, each
+      // addition's error is kept
+      float s = 0.f, e = 0.f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float2 f = unpack<BF16>(cw[k]);
-      F2 u = two_sum(s, f.x * f.x);
-      e += u.lo;
-      u = two_sum(u.hi, f.y * f.y);
-      s = u.hi;
-      e += u.lo;
-    }
+      for (int k = 0; k < 8; ++k) {
+        const float2 f = unpack<BF16>(cw[k]);
+        F2 u = two_sum(s, f.x * f.x);
+        e += u.lo;
+        u = two_sum(u.hi, f.y * f.y);
+        s = u.hi;
+        e += u.lo;
+      }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const float s2 = __shfl_xor_sync(0xffffffffu, s, o), e2 = __shfl_xor_sync(0xffffffffu, e, o);
-      const F2 u = two_sum(s, s2);
-      s = u.hi;
-      e = (e + e2) + u.lo;
-    }
-    F2 m = two_sum(s * (1.f / 512), ap.eps);
-    m = renorm(m.hi, m.lo + e * (1.f / 512));
-    // 1 / sqrt(m): the fp32 estimate and one Newton step on its exact residual
-    const float r0 = rsqrtf(m.hi);
-    const float r2 = r0 * r0, r2e = fmaf(r0, r0, -r2);
-    const float res = fmaf(-m.hi, r2, 1.f) - (m.hi * r2e + m.lo * r2);
-    const float rl = 0.5f * r0 * res;
+      for (int o = 16; o > 0; o >>= 1) {
+        const float s2 = __shfl_xor_sync(0xffffffffu, s, o), e2 = __shfl_xor_sync(0xffffffffu, e, o);
+        const F2 u = two_sum(s, s2);
+        s = u.hi;
+        e = (e + e2) + u.lo;
+      }
+      F2 m = two_sum(s * (1.f / 512), ap.eps);
+      m = renorm(m.hi, m.lo + e * (1.f / 512));
+      // 1 / sqrt(m): the fp32 estimate and one Newton step on its exact residual
+      const float r0 = rsqrtf(m.hi);
+      const float r2 = r0 * r0, r2e = fmaf(r0, r0, -r2);
+      const float res = fmaf(-m.hi, r2, 1.f) - (m.hi * r2e + m.lo * r2);
+      const float rl = 0.5f * r0 * res;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float2 f = unpack<BF16>(cw[k]), w = unpack<BF16>(ww[k]);
+      for (int k = 0; k < 8; ++k) {
+        const float2 f = unpack<BF16>(cw[k]), w = unpack<BF16>(ww[k]);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float xw = h ? f.y * w.y : f.x * w.x;   // exact
-        const float p = xw * r0;
-        const F2 v = renorm(p, fmaf(xw, r0, -p) + xw * rl);
-        y[2 * k + h] = xw == 0.f ? xw : to_odd(v.hi, v.lo);
+        for (int h = 0; h < 2; ++h) {
+          const float xw = h ? f.y * w.y : f.x * w.x;   // exact
+          const float p = xw * r0;
+          const F2 v = renorm(p, fmaf(xw, r0, -p) + xw * rl);
+          y[2 * k + h] = xw == 0.f ? xw : to_odd(v.hi, v.lo);
+        }
+      }
+    } else {
+      float s = 0.f, e = 0.f;   // (two chains: half the latency and half the error)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float2 f = unpack<BF16>(cw[k]);
+        s = fmaf(f.x, f.x, s);
+        e = fmaf(f.y, f.y, e);
+      }
+      s += e;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      const float rs = rsqrtf(fmaf(s, 1.f / 512, ap.eps));
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float2 f = unpack<BF16>(cw[k]), w = unpack<BF16>(ww[k]);
+        y[2 * k] = f.x * w.x * rs;
+        y[2 * k + 1] = f.y * w.y * rs;
       }
     }
   } else {
@@ -268,15 +318,26 @@ __device__ void append_row(const AppendParams& ap, int t, int lane) {
         am = fmaxf(am, fabsf(y[k]));
         nan |= y[k] != y[k];
       }
-      const uint32_t sb = block_scale(am, nan, ap.kv6);
-      const Scale sc = make_scale(sb, ap.kv_scale);
-      uint32_t code[2] = {0, 0};
+      const uint32_t sb = block_scale<EXACT>(am, nan, ap, same);
+      const float d = from_e4m3(sb) * ap.kv_scale;
+      uint32_t code[2];
+      if constexpr (EXACT) {
+        float q[16];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const uint32_t c = e2m1_pair(y[2 * k], y[2 * k + 1], sc, sc);
-        code[k >> 2] |= c << (8 * (k & 3));
-        const float2 v = e2m1_values(c);
-        w[k] = pack2<BF16>(v.x * sc.d, v.y * sc.d);
+        for (int k = 0; k < 16; ++k) q[k] = div_signed(y[k], d);
+        code[0] = to_e2m1x8(q, 1.f);
+        code[1] = to_e2m1x8(q + 8, 1.f);
+      } else {
+        const float rd = d > 0.f ? __frcp_rn(d) : 0.f;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          code[k] = to_e2m1x8(y + 8 * k, rd * kLess);
+          same &= code[k] == to_e2m1x8(y + 8 * k, rd * kMore) || nan;
+        }
+      }
+      if (ap.kv_out) {
+        e2m1_values<BF16>(code[0], d, w);
+        e2m1_values<BF16>(code[1], d, w + 4);
       }
       // key: a block is 8 lanes' pairs (interleaved) or 16 lanes' first or
       // second values (halves)
@@ -298,13 +359,20 @@ __device__ void append_row(const AppendParams& ap, int t, int lane) {
           n1 |= m1 != 0;
         }
       }
-      const uint32_t sb0 = block_scale(a0, n0, ap.kv6), sb1 = block_scale(a1, n1, ap.kv6);
-      // (interleaved: both values' blocks are one)
-      const Scale s0 = make_scale(sb0, ap.kv_scale), s1 = make_scale(sb1, ap.kv_scale);
-      const uint32_t kc = e2m1_pair(r0, r1, s0, s1);
-      const float2 kv = e2m1_values(kc);
-      q0 = kv.x * s0.d;
-      q1 = kv.y * s1.d;
+      // (the key's values are exact in either form, so its codes are taken once)
+      bool unused = true;
+      const uint32_t sb0 = block_scale<true>(a0, n0, ap, unused), sb1 = block_scale<true>(a1, n1, ap, unused);
+      const float d0 = from_e4m3(sb0) * ap.kv_scale, d1 = from_e4m3(sb1) * ap.kv_scale;
+      const uint32_t kc = to_e2m1x2(div_signed(r0, d0), div_signed(r1, d1));
+      {
+        uint32_t v[4];
+        e2m1_values<BF16>(kc, 1.f, v);
+        const float2 f = unpack<BF16>(v[0]);
+        q0 = f.x * d0;
+        q1 = f.y * d1;
+      }
+      if constexpr (!EXACT)
+        if (!__all_sync(0xffffffffu, same)) return false;
       // scales of four lanes in a word: lane 4 j writes blocks 4 j .. 4 j + 3
       uint32_t sw = sb;
       sw |= __shfl_down_sync(0xffffffffu, sw, 1) << 8;
@@ -354,13 +422,21 @@ __device__ void append_row(const AppendParams& ap, int t, int lane) {
     if (KIND == kKvModel && store) put(static_cast<uint16_t*>(ap.cache) + static_cast<int64_t>(slot) * 576);
   } else {
     uint32_t w[4];
+    if constexpr (EXACT) {
+      float q[16];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      w[k] = 0;
+      for (int k = 0; k < 16; ++k) q[k] = div_signed(y[k], ap.kv_scale);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) w[k] |= to_e4m3(__fdiv_rn(y[4 * k + j], ap.kv_scale)) << (8 * j);
+      for (int k = 0; k < 4; ++k) w[k] = to_e4m3x4(q + 4 * k, 1.f);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        w[k] = to_e4m3x4(y + 4 * k, ap.inv_kv * kLess);
+        same &= w[k] == to_e4m3x4(y + 4 * k, ap.inv_kv * kMore);
+      }
+      if (!__all_sync(0xffffffffu, same)) return false;
     }
-    const uint32_t b0 = to_e4m3(__fdiv_rn(r0, ap.kv_scale)), b1 = to_e4m3(__fdiv_rn(r1, ap.kv_scale));
+    const uint32_t b0 = to_e4m3(div_signed(r0, ap.kv_scale)), b1 = to_e4m3(div_signed(r1, ap.kv_scale));
     auto put = [&](uint8_t* row) {
       *reinterpret_cast<uint4*>(row + 16 * lane) = make_uint4(w[0], w[1], w[2], w[3]);
       if (ap.interleaved) {
@@ -373,6 +449,12 @@ __device__ void append_row(const AppendParams& ap, int t, int lane) {
     if (ap.kv_out) put(static_cast<uint8_t*>(ap.kv_out) + static_cast<int64_t>(t) * 576);
     if (store) put(static_cast<uint8_t*>(ap.cache) + static_cast<int64_t>(slot) * 576);
   }
+  return true;
+}
+
+template <bool BF16, int KIND>
+__device__ __noinline__ void append_row_exact(const AppendParams& ap, int t, int lane) {
+  append_row<BF16, KIND, true>(ap, t, lane);
 }
 
 // Up to kQueryHeads heads of one token's queries, by one warp: lane j of a
@@ -448,11 +530,15 @@ __device__ void rotate_queries(const AppendParams& ap, int64_t item, int lane) {
 }  // namespace
 
 template <bool BF16, int KIND>
-__global__ void __launch_bounds__(kAppendThreads, 4) mla_kv_append_kernel(const AppendParams ap) {
+__global__ void __launch_bounds__(kAppendThreads, 4) mla_kv_append_kernel(const __grid_constant__ AppendParams ap) {
   const int blk = static_cast<int>(blockIdx.x);
   if (blk < ap.row_blocks) {
     const int t = blk * (kAppendThreads / 32) + (threadIdx.x >> 5);
-    if (t < ap.T) append_row<BF16, KIND>(ap, t, threadIdx.x & 31);
+    if (t >= ap.T) return;
+    if constexpr (KIND == kKvModel)
+      append_row<BF16, KIND, true>(ap, t, threadIdx.x & 31);
+    else if (!append_row<BF16, KIND, false>(ap, t, threadIdx.x & 31))
+      append_row_exact<BF16, KIND>(ap, t, threadIdx.x & 31);
   } else {
     const int64_t item = static_cast<int64_t>(blk - ap.row_blocks) * (kAppendThreads / 32) + (threadIdx.x >> 5);
     if (item < static_cast<int64_t>(ap.T) * ap.q_groups) rotate_queries<BF16>(ap, item, threadIdx.x & 31);

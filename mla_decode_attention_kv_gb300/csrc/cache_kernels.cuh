@@ -36,6 +36,7 @@ struct AppendParams {
   int sec1, sec2;          // first pair of the second and of the third axis (32: none)
   int interleaved;
   float eps, kv_scale, kv6;   // kv6 = 6 kv_scale
+  float inv_kv, inv_kv6;      // their reciprocals, rounded
   int row_blocks, q_groups;   // blocks that make rows; warps per token that rotate queries
 };
 int launch_append(AppendParams ap, int kind, bool bf16, cudaStream_t stream);
