@@ -21,15 +21,14 @@
 // x rows columns of tensor memory, at most half of it, so one CTA holds all of
 // a unit, and several query tokens' rows share one pass over the history.
 //
-// One persistent CTA per SM, 896 threads (640 for 64 rows, whose softmax takes
-// more registers a thread):
+// One persistent CTA per SM, 768 or 896 threads:
 //   w0      producer: raw pages (codes, scales) by bulk copies, queries by TMA
 //   w1      QK issuer            w2  PV issuer           w3  empty parts
-//   w4-11   softmax: two groups of four warps with half of the rows each; a
-//           token (16 TMEM lanes a warp in an M = 64 accumulator) has two
-//           threads of a group, one for each half of its rows.  O rescale and
-//           epilogue (thread = latent)
-//   w12-    unpacking: codes and scales to 128-byte-swizzled 16-bit chunks
+//   w4-     softmax: groups of four warps with 16 rows each; a token (16 TMEM
+//           lanes a warp in an M = 64 accumulator) has two threads of a group,
+//           one for each half of its rows.  O rescale and epilogue (thread =
+//           latent)
+//   rest    unpacking: codes and scales to 128-byte-swizzled 16-bit chunks
 // A tile's 512 latents are unpacked as two halves through a ring of half slots
 // (two tiles; one and a half for 64 rows, whose queries take 72 KB), its RoPE
 // columns with the second: the QK MMAs of a half start while the other is
@@ -52,7 +51,8 @@ namespace mla {
 namespace {
 
 constexpr int kTile4 = 64;                       // tokens
-constexpr int kSoftWarp = 4, kUnpackWarp = 12;   // first warp of the softmax and of the unpacking
+constexpr int kSoftWarp = 4;                     // first warp of the softmax
+constexpr int kGroup4 = 16;                      // rows (columns of S^T) of a softmax group
 constexpr int kRawCodes = kTile4 * kE2m1Codes;   // 18432
 constexpr int kRawStage = kTile4 * kE2m1Row;     // 20736
 constexpr int kChunk = kTile4 * 128;             // 8 KB: 64 columns of a tile
@@ -67,7 +67,9 @@ template <int N>
 struct Smem4 {
   static constexpr int kNH = N == 64 ? 3 : 4;    // half slots (a tile takes two)
   static constexpr int kNR = N == 64 ? 1 : 2;    // RoPE slots
+  static constexpr int kGroups = N / kGroup4;    // softmax groups of four warps
   static constexpr int kUW = N == 64 ? 8 : 16;   // unpacking warps
+  static constexpr int kUnpackWarp = kSoftWarp + 4 * kGroups;
   static constexpr int kThreads = (kUnpackWarp + kUW) * 32;
   static constexpr int kQ = N * 128 * 9;
   static constexpr int kHalfOff = 0;
@@ -75,10 +77,9 @@ struct Smem4 {
   static constexpr int kQOff = kRopeOff + kNR * kChunk;
   static constexpr int kPOff = kQOff + kQ;
   static constexpr int kP = kTile4 * N * 2;
-  static constexpr int kStageOff = kPOff + kP;               // 16 rows: the epilogue's staging
-  static constexpr int kRawOff = kStageOff + (N == 16 ? 4096 : 0);
+  static constexpr int kRawOff = kPOff + kP;
   static constexpr int kMOff = kRawOff + 2 * kRawStage;      // reference maxima [N]
-  static constexpr int kRedOff = kMOff + N * 4;              // reductions over the warps [2 groups][4][N / 2]
+  static constexpr int kRedOff = kMOff + N * 4;              // reductions over the warps [groups][4][16]
   static constexpr int kUnitOff = kRedOff + N * 16;
   static constexpr int kBarOff = kUnitOff + ((kUnits4 * 20 + 8 + 15) / 16) * 16;
   // barrier slots
@@ -361,12 +362,6 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 
 // Columns [c, c + NC) of an M = 64 accumulator for lanes 0-15 of the warp and
 // [c + NC, c + 2 NC) for lanes 16-31, both of the rows in TMEM lanes 0-15.
-__device__ __forceinline__ void tmem_half(uint32_t a, uint32_t (&r)[4]) {
-  asm volatile("tcgen05.ld.sync.aligned.16x32bx2.x4.b32 {%0,%1,%2,%3}, [%4], 4;\n tcgen05.wait::ld.sync.aligned;"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(a)
-               : "memory");
-}
 __device__ __forceinline__ void tmem_half(uint32_t a, uint32_t (&r)[8]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.16x32bx2.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8], 8;\n tcgen05.wait::ld.sync.aligned;"
@@ -374,17 +369,8 @@ __device__ __forceinline__ void tmem_half(uint32_t a, uint32_t (&r)[8]) {
       : "r"(a)
       : "memory");
 }
-__device__ __forceinline__ void tmem_half(uint32_t a, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x32bx2.x16.b32"
-      " {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16], 16;\n tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(a)
-      : "memory");
-}
 
-// 8, 16 or 32 columns of this warp's 32 lanes, loaded and waited for
+// Eight columns of this warp's 32 lanes, loaded and waited for
 __device__ __forceinline__ void tmem_get(uint32_t a, uint32_t (&r)[8]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n tcgen05.wait::ld.sync.aligned;"
@@ -392,47 +378,24 @@ __device__ __forceinline__ void tmem_get(uint32_t a, uint32_t (&r)[8]) {
       : "r"(a)
       : "memory");
 }
-__device__ __forceinline__ void tmem_get(uint32_t a, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32"
-      " {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(a)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_get(uint32_t a, uint32_t (&r)[32]) {
-  tmem_ld32(a, r);
-  tmem_wait_ld(r);
-}
 __device__ __forceinline__ void tmem_put(uint32_t a, const uint32_t (&r)[8]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(a), "r"(r[0]), "r"(r[1]),
                "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
 }
-__device__ __forceinline__ void tmem_put(uint32_t a, const uint32_t (&r)[16]) { tmem_st16(a, r); }
-__device__ __forceinline__ void tmem_put(uint32_t a, const uint32_t (&r)[32]) { tmem_st32(a, r); }
 
-// P^T, the MN-major B operand: a row of 16-bit columns per token (k).  For 32
-// and 64 rows the two softmax groups' columns are blocks of their own, [64
-// tokens][N / 2] with the swizzle as wide as a row (32 or 64 bytes), LBO from
-// block to block; for 16 rows one block holds both groups' eight columns.
-template <int N>
-struct PLayout {
-  static constexpr int kCols = N == 16 ? 16 : N / 2;        // columns of a block
-  static constexpr int kRow = kCols * 2;                    // bytes
-  static constexpr int kBlock = kTile4 * kRow;
-  static constexpr int kStep = 16 * kRow;                   // bytes from one k-step (16 tokens) to the next
-  static __device__ __forceinline__ uint64_t desc(uint32_t addr) {
-    constexpr uint64_t type = kCols == 32 ? 4 : 6;          // 64-, 32-byte swizzle
-    return static_cast<uint64_t>((addr >> 4) & 0x3FFF) | (static_cast<uint64_t>(kBlock >> 4) << 16) |
-           (static_cast<uint64_t>(8 * kRow >> 4) << 32) | (uint64_t{1} << 46) | (type << 61);
-  }
-  // byte offset of 16-byte unit k of token t in a block
-  static __device__ __forceinline__ uint32_t offset(int t, int k) {
-    return t * kRow + ((k ^ (kCols == 32 ? (t >> 1) & 3 : (t >> 2) & 1)) << 4);
-  }
-};
+// P^T, the MN-major B operand: each softmax group's 16 columns are a block of
+// their own, [64 tokens][16] 16-bit values with the 32-byte swizzle, LBO from
+// block to block.
+constexpr int kPRow = kGroup4 * 2;
+constexpr int kPBlock = kTile4 * kPRow;
+constexpr int kPStep = 16 * kPRow;       // bytes from one k-step (16 tokens) to the next
+__device__ __forceinline__ uint64_t p_desc(uint32_t addr) {
+  return static_cast<uint64_t>((addr >> 4) & 0x3FFF) | (static_cast<uint64_t>(kPBlock >> 4) << 16) |
+         (static_cast<uint64_t>(8 * kPRow >> 4) << 32) | (uint64_t{1} << 46) | (uint64_t{6} << 61);
+}
+// byte offset of 16-byte unit k (0, 1) of token t in a block
+__device__ __forceinline__ uint32_t p_offset(int t, int k) { return t * kPRow + ((k ^ ((t >> 2) & 1)) << 4); }
 
 // Reduction over the 16 lanes of a half warp of NC columns held one row per
 // lane: every step halves the columns a lane keeps, so 16 columns take 15
@@ -527,7 +490,7 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
       mbar_init(&bar[L::B_RAW_FULL + s], 1);
       mbar_init(&bar[L::B_RAW_EMPTY + s], L::kUW);
       mbar_init(&bar[L::B_S_FULL + s], 1);
-      mbar_init(&bar[L::B_S_EMPTY + s], 8);
+      mbar_init(&bar[L::B_S_EMPTY + s], 4 * L::kGroups);
     }
     for (int s = 0; s < L::kNH; ++s) {
       mbar_init(&bar[L::B_FULL + s], L::kUW);
@@ -535,7 +498,7 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
     }
     mbar_init(&bar[L::B_Q_FULL], 1);
     mbar_init(&bar[L::B_Q_EMPTY], 1);
-    mbar_init(&bar[L::B_P_FULL], 8);
+    mbar_init(&bar[L::B_P_FULL], 4 * L::kGroups);
     mbar_init(&bar[L::B_P_EMPTY], 1);
     mbar_init(&bar[L::B_DONE_QK], 1);
     mbar_init(&bar[L::B_DONE_PV], 1);
@@ -690,7 +653,7 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
     const bool leader = elect_one();
     constexpr uint32_t idesc = make_idesc_f16(128, N, BF16, true, true);
     const uint64_t v0 = make_desc_sw128(smem_u32(smem + L::kHalfOff), kChunk, 1024);
-    const uint64_t p0 = PLayout<N>::desc(smem_u32(smem + L::kPOff));
+    const uint64_t p0 = p_desc(smem_u32(smem + L::kPOff));
     auto wait = [&](uint64_t* b, uint32_t parity) { return __all_sync(0xffffffffu, waits.wait(b, parity)) != 0; };
     Iter4<N> it;
     it.start(fp, tab, rng);
@@ -714,7 +677,7 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
               if (leader)
-                umma_ss(tmem + L::kTmemO + (2 * h + p) * N, v + p * (2 * kChunk >> 4) + kk * 128, p0 + kk * (PLayout<N>::kStep >> 4), idesc,
+                umma_ss(tmem + L::kTmemO + (2 * h + p) * N, v + p * (2 * kChunk >> 4) + kk * 128, p0 + kk * (kPStep >> 4), idesc,
                         kk ? 1u : more);
           }
           if (leader) umma_commit(&bar[L::B_EMPTY + sl]);
@@ -739,24 +702,22 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
         for (int c = lane; c < (fp.part_dtype == kFP32 ? 128 : 64); c += 32) o[c] = make_uint4(0, 0, 0, 0);
       }
     }
-  } else if (warp < kUnpackWarp) {
+  } else if (warp < L::kUnpackWarp) {
     // ------------------------------------------------ softmax, O rescale, epilogue
-    // Two groups of four warps, each with half of the rows (columns of S^T)
-    // and nothing shared between them.
-    constexpr int NG = N / 2, NC = N / 4;      // columns of a group, of a thread
-    constexpr int NO = N == 64 ? 16 : 8;       // columns of O at a time
-    using PL = PLayout<N>;
+    // Groups of four warps with 16 of the rows (columns of S^T) each and nothing
+    // shared between them: a token's columns are its two threads', eight each.
+    constexpr int NG = kGroup4, NC = NG / 2;   // columns of a group, of a thread
+    constexpr int NO = 8;                      // columns of O at a time
     const int grp = (warp - kSoftWarp) >> 2, wq = warp & 3;
-    const int gtid = threadIdx.x - kSoftWarp * 32 - grp * 128;
     const int barid = 1 + grp;
     const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
     const int tok = wq * 16 + (lane & 15);     // token of the tile
-    const int c0 = grp * NG + (lane >> 4) * NC;   // first column of this thread
-    const int cr = (lane >> 4) * NC + (lane & 15) / (16 / NC);   // column (of the group) that col_reduce leaves here
-    uint8_t* sP = smem + L::kPOff + (N == 16 ? 0 : grp * PL::kBlock);   // this group's block
-    // a warp's staging of the epilogue: its share of the group's block of P, which no
-    // MMA reads then (16 rows: a region of its own)
-    uint8_t* stage = N == 16 ? smem + L::kStageOff + (warp - kSoftWarp) * 512 : sP + wq * (PL::kBlock / 4);
+    const int cg = (lane >> 4) * NC;           // first column of this thread in the group
+    const int cr = cg + ((lane & 15) >> 1);    // column of the group that col_reduce leaves here
+    uint8_t* sP = smem + L::kPOff + grp * kPBlock;   // this group's block
+    // a warp's staging of the epilogue: its quarter of the group's block of P,
+    // which no MMA reads then
+    uint8_t* stage = sP + wq * (kPBlock / 4);
     float* s_m = reinterpret_cast<float*>(smem + L::kMOff) + grp * NG;
     float* red = reinterpret_cast<float*>(smem + L::kRedOff) + grp * (4 * NG);   // [4][NG]
     float l[NC], m[NC];
@@ -775,7 +736,7 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
       // past the end; in the CURRENT part the rows of earlier query tokens
       int nmin = N;
       if (it.tok0() + tok < ui.hi) nmin = cur ? min(N, max(0, tok * fp.H - ui.g * N)) : 0;
-      nmin -= c0;
+      nmin -= grp * NG + cg;
       ok = ok && waits.lazy(&bar[L::B_S_FULL + sb], (g >> 1) & 1);
       __syncwarp();
       tc_fence_after();
@@ -805,7 +766,7 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
         float a[NC];
 #pragma unroll
         for (int k = 0; k < NC; ++k) {
-          const float* r = red + (c0 - grp * NG) + k;
+          const float* r = red + cg + k;
           const float t = fmaxf(fmaxf(r[0], r[NG]), fmaxf(r[2 * NG], r[3 * NG]));
           a[k] = 1.f;
           if (first) {
@@ -821,8 +782,8 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
         if (wq == 0 && (lane & 15) == 0) {
 #pragma unroll
           for (int k = 0; k < NC; ++k) {
-            s_m[c0 - grp * NG + k] = m[k];
-            red[c0 - grp * NG + k] = a[k];
+            s_m[cg + k] = m[k];
+            red[cg + k] = a[k];
           }
         }
         if (!first) {
@@ -856,15 +817,7 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
       if (g >= 1) ok = ok && waits.lazy(&bar[L::B_P_EMPTY], (g - 1) & 1);
       ok = __all_sync(0xffffffffu, ok);
       if (ok) {
-        const int hw = lane >> 4;
-        if constexpr (NC == 4) {
-          *reinterpret_cast<uint2*>(sP + PL::offset(tok, grp) + hw * 8) = make_uint2(pk[0], pk[1]);
-        } else {
-#pragma unroll
-          for (int k = 0; k < NC / 8; ++k)
-            *reinterpret_cast<uint4*>(sP + PL::offset(tok, hw * (NC / 8) + k)) =
-                make_uint4(pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]);
-        }
+        *reinterpret_cast<uint4*>(sP + p_offset(tok, lane >> 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar[L::B_P_FULL]);
@@ -916,12 +869,9 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
               reinterpret_cast<uint16_t*>(stage)[k * 32 + lane] =
                   static_cast<uint16_t>(pack2_dt(__uint_as_float(o[k]), 0.f, fp.part_dtype));
             __syncwarp();
-#pragma unroll
-            for (int k = 0; k < NO; k += 8) {
-              const uint4 x = *reinterpret_cast<const uint4*>(stage + k * 64 + lane * 16);
-              const int64_t d = dst[n0 + k + (lane >> 2)];
-              if (d >= 0) *reinterpret_cast<uint4*>(out + d + lat0 * 2 + (lane & 3) * 16) = x;
-            }
+            const uint4 x = *reinterpret_cast<const uint4*>(stage + lane * 16);
+            const int64_t d = dst[n0 + (lane >> 2)];
+            if (d >= 0) *reinterpret_cast<uint4*>(out + d + lat0 * 2 + (lane & 3) * 16) = x;
             __syncwarp();
           } else {
 #pragma unroll
@@ -929,12 +879,9 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
 #pragma unroll
               for (int k = 0; k < NO / 2; ++k) reinterpret_cast<uint32_t*>(stage)[k * 32 + lane] = o[h + k];
               __syncwarp();
-#pragma unroll
-              for (int k = 0; k < NO / 2; k += 4) {
-                const uint4 x = *reinterpret_cast<const uint4*>(stage + k * 128 + lane * 16);
-                const int64_t d = dst[n0 + h + k + (lane >> 3)];
-                if (d >= 0) *reinterpret_cast<uint4*>(out + d + lat0 * 4 + (lane & 7) * 16) = x;
-              }
+              const uint4 x = *reinterpret_cast<const uint4*>(stage + lane * 16);
+              const int64_t d = dst[n0 + h + (lane >> 3)];
+              if (d >= 0) *reinterpret_cast<uint4*>(out + d + lat0 * 4 + (lane & 7) * 16) = x;
               __syncwarp();
             }
           }
@@ -951,7 +898,7 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
     // half's eight 32-column units spread over the warps, the RoPE columns
     // with the second.  One fence and one arrival a half.
     constexpr int GP = L::kUW / 2, NU = 8 / GP;     // column groups; units of a half per lane
-    const int w = warp - kUnpackWarp;
+    const int w = warp - L::kUnpackWarp;
     const int t = (w & 1) * 32 + lane, grp = w >> 1;
     uint8_t* half0 = smem + L::kHalfOff;
     Iter4<N> it;
