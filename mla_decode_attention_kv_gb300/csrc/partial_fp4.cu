@@ -31,14 +31,13 @@
 //   rest    unpacking: codes and scales to 128-byte-swizzled 16-bit chunks
 // A tile's 512 latents are unpacked as two halves through a ring of half slots
 // (two tiles; one and a half for 64 rows, whose queries take 72 KB), its RoPE
-// columns with the second: the QK MMAs of a half start while the other is
+// columns with the first: the QK MMAs of a half start while the other is
 // unpacked, and a slot is free when its PV MMAs are done.
 //
-// The softmax keeps its reference maximum per row in shared memory and tests
-// each tile against it; only a tile that exceeds it by 2^8 (and the first of a
-// piece) reduces the maximum over the tokens (the lanes) and rescales O.  Row
-// sums stay in registers, one partial sum per token lane and row, and are
-// reduced once per piece.
+// The softmax keeps each row's reference maximum in registers; only a tile with
+// a weight past 2^8 (and the first of a piece) reduces the maximum over the
+// tokens (the lanes) and rescales O.  Row sums stay in registers too, one
+// partial sum per token lane and row, and are reduced once per piece.
 //
 // Every wait is bounded, as in the 16-bit kernel.
 #include <mutex>
@@ -80,7 +79,8 @@ struct Smem4 {
   static constexpr int kRawOff = kPOff + kP;
   static constexpr int kMOff = kRawOff + 2 * kRawStage;      // reference maxima [N]
   static constexpr int kRedOff = kMOff + N * 4;              // reductions over the warps [groups][4][16]
-  static constexpr int kUnitOff = kRedOff + N * 16;
+  static constexpr int kFlagOff = kRedOff + N * 16;          // [3 tiles][4 groups]: weights past the limit
+  static constexpr int kUnitOff = kFlagOff + 48;
   static constexpr int kBarOff = kUnitOff + ((kUnits4 * 20 + 8 + 15) / 16) * 16;
   // barrier slots
   enum : int {
@@ -94,6 +94,8 @@ struct Smem4 {
     B_S_EMPTY = B_S_FULL + 2,
     B_P_FULL = B_S_EMPTY + 2,
     B_P_EMPTY,
+    B_P_FIXED,
+    B_ROPE_EMPTY,
     B_DONE_QK,
     B_DONE_PV,
     B_COUNT
@@ -500,6 +502,9 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
     mbar_init(&bar[L::B_Q_EMPTY], 1);
     mbar_init(&bar[L::B_P_FULL], 4 * L::kGroups);
     mbar_init(&bar[L::B_P_EMPTY], 1);
+    mbar_init(&bar[L::B_P_FIXED], 4 * L::kGroups);
+    mbar_init(&bar[L::B_ROPE_EMPTY], 1);
+    for (int k = 0; k < 12; ++k) reinterpret_cast<int*>(smem + L::kFlagOff)[k] = 0;
     mbar_init(&bar[L::B_DONE_QK], 1);
     mbar_init(&bar[L::B_DONE_PV], 1);
     *abort_flag = 0;
@@ -627,18 +632,21 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
             break;
           }
           tc_fence_after();
+          if (h == 0) {   // the RoPE columns come with the first half
+            const uint64_t r = r0 + (g % L::kNR) * (kChunk >> 4);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              if (leader) umma_ss(d, r + kk * 2, q0 + 8 * (N * 8) + kk * 2, idesc, kk ? 1u : 0u);
+            if (L::kNR == 1 && leader) umma_commit(&bar[L::B_ROPE_EMPTY]);
+          }
           const uint64_t a = a0 + sl * (kHalf >> 4);
 #pragma unroll
           for (int kk = 0; kk < 16; ++kk)
             if (leader)
               umma_ss(d, a + (kk >> 2) * (kChunk >> 4) + (kk & 3) * 2, q0 + (4 * h + (kk >> 2)) * (N * 8) + (kk & 3) * 2,
-                      idesc, (h | kk) ? 1u : 0u);
+                      idesc, 1u);
         }
         if (!ok) break;
-        const uint64_t r = r0 + (g % L::kNR) * (kChunk >> 4);   // (full with the second half)
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          if (leader) umma_ss(d, r + kk * 2, q0 + 8 * (N * 8) + kk * 2, idesc, 1u);
         if (leader) {
           umma_commit(&bar[L::B_S_FULL + sb]);
           if (lastq && k == n - 1) umma_commit(&bar[L::B_Q_EMPTY]);
@@ -657,7 +665,7 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
     auto wait = [&](uint64_t* b, uint32_t parity) { return __all_sync(0xffffffffu, waits.wait(b, parity)) != 0; };
     Iter4<N> it;
     it.start(fp, tab, rng);
-    int g = 0;
+    int g = 0, nfix = 0;
     bool ok = true;
     while (ok && it.valid) {
       const int n = it.jend - it.j;
@@ -665,6 +673,15 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
         if (!wait(&bar[L::B_P_FULL], g & 1)) {
           ok = false;
           break;
+        }
+        // weights past the limit are made again first (the softmax, below)
+        const volatile int* fl = reinterpret_cast<const volatile int*>(smem + L::kFlagOff) + (g % 3) * 4;
+        if (fl[0] | fl[1] | fl[2] | fl[3]) {
+          if (!wait(&bar[L::B_P_FIXED], nfix & 1)) {
+            ok = false;
+            break;
+          }
+          ++nfix;
         }
         tc_fence_after();
         const uint32_t more = k > 0 ? 1u : 0u;
@@ -727,6 +744,70 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
     it.start(fp, tab, rng);
     int g = 0;
     bool ok = true;
+    // New reference maxima of the group's rows from the tile's scores x, O and l
+    // brought to them (not for a piece's first tile).  False: time to leave.
+    auto new_maxima = [&](const float (&x)[NC], bool first, bool ok) {
+      if (!named_bar_and(barid, 128, ok)) return false;
+      float y[NC];
+#pragma unroll
+      for (int k = 0; k < NC; ++k) y[k] = x[k];
+      const float mx = col_reduce<NC, true>(y, lane);
+      red[wq * NG + cr] = mx;
+      named_bar_sync(barid, 128);
+      float a[NC];
+#pragma unroll
+      for (int k = 0; k < NC; ++k) {
+        const float* r = red + cg + k;
+        const float t = fmaxf(fmaxf(r[0], r[NG]), fmaxf(r[2 * NG], r[3 * NG]));
+        a[k] = 1.f;
+        if (first) {
+          m[k] = t == -INFINITY ? 0.f : t;
+          l[k] = 0.f;
+        } else if (t > m[k] + kThresh) {
+          a[k] = fast_exp2(m[k] - t);
+          m[k] = t;
+          l[k] *= a[k];
+        }
+      }
+      named_bar_sync(barid, 128);   // red has been read
+      if (wq == 0 && (lane & 15) == 0) {
+#pragma unroll
+        for (int k = 0; k < NC; ++k) {
+          s_m[cg + k] = m[k];
+          red[cg + k] = a[k];
+        }
+      }
+      named_bar_sync(barid, 128);
+      if (!first) {
+        // O *= alpha (the PV product of the tile before is done)
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < 4 * NG; c += NO) {
+          uint32_t o[NO];
+          const uint32_t oa = tmem + lanes + L::kTmemO + (c / NG) * N + grp * NG + c % NG;
+          tmem_get(oa, o);
+#pragma unroll
+          for (int k = 0; k < NO; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * red[c % NG + k]);
+          tmem_put(oa, o);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        named_bar_sync(barid, 128);   // alpha has been read
+      }
+      return true;
+    };
+    // weights of the tile's scores, and P^T written
+    auto weights = [&](const float (&x)[NC], float (&p)[NC]) {
+      uint32_t pk[NC / 2];
+#pragma unroll
+      for (int k = 0; k < NC; k += 2) {
+        p[k] = fast_exp2(x[k] - m[k]);   // masked: exp2(-inf) = 0
+        p[k + 1] = fast_exp2(x[k + 1] - m[k + 1]);
+        pk[k / 2] = pack2<BF16>(p[k], p[k + 1]);
+      }
+      return make_uint4(pk[0], pk[1], pk[2], pk[3]);
+    };
+    volatile int* flags = reinterpret_cast<volatile int*>(smem + L::kFlagOff);
     while (it.valid) {
       const Unit4 ui = it.ui;
       const int sb = g & 1;
@@ -737,91 +818,61 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
       int nmin = N;
       if (it.tok0() + tok < ui.hi) nmin = cur ? min(N, max(0, tok * fp.H - ui.g * N)) : 0;
       nmin -= grp * NG + cg;
-      ok = ok && waits.lazy(&bar[L::B_S_FULL + sb], (g >> 1) & 1);
-      __syncwarp();
+      ok = __all_sync(0xffffffffu, ok && waits.lazy(&bar[L::B_S_FULL + sb], (g >> 1) & 1)) != 0;
       tc_fence_after();
       uint32_t v[NC];
       tmem_half(tmem + lanes + L::kTmemS + sb * N + grp * NG, v);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar[L::B_S_EMPTY + sb]);
-      // scores in the log2 domain, relative to the reference maximum
-      float x[NC];
+      // scores in the log2 domain
+      float x[NC], p[NC];
+#pragma unroll
+      for (int k = 0; k < NC; ++k) x[k] = k >= nmin ? __uint_as_float(v[k]) * sl : -INFINITY;
+      if (first && !new_maxima(x, true, ok)) break;
+      // The weights are made and handed over against the reference maximum as
+      // it stands; a warp that finds one past 2^8 raises its group's flag of
+      // this tile, and the group makes them again before the PV product, which
+      // looks at the flags, reads them.  (A barrier to agree first cost 500
+      // cycles of every tile.)
       float top = -INFINITY;
 #pragma unroll
-      for (int k = 0; k < NC; ++k) {
-        x[k] = k >= nmin ? __uint_as_float(v[k]) * sl : -INFINITY;
-        top = fmaxf(top, x[k] - m[k]);
-      }
-      // does every score stay below the reference maximum + 8?
-      if (!named_bar_and(barid, 128, ok && !first && top <= kThresh)) {
-        if (!named_bar_and(barid, 128, ok)) break;
-        // ---- new reference maxima: each row's maximum over the tile's tokens
-        float y[NC];
-#pragma unroll
-        for (int k = 0; k < NC; ++k) y[k] = x[k];
-        const float mx = col_reduce<NC, true>(y, lane);
-        red[wq * NG + cr] = mx;
-        named_bar_sync(barid, 128);
-        float a[NC];
-#pragma unroll
-        for (int k = 0; k < NC; ++k) {
-          const float* r = red + cg + k;
-          const float t = fmaxf(fmaxf(r[0], r[NG]), fmaxf(r[2 * NG], r[3 * NG]));
-          a[k] = 1.f;
-          if (first) {
-            m[k] = t == -INFINITY ? 0.f : t;
-            l[k] = 0.f;
-          } else if (t > m[k] + kThresh) {
-            a[k] = fast_exp2(m[k] - t);
-            m[k] = t;
-            l[k] *= a[k];
-          }
-        }
-        named_bar_sync(barid, 128);   // red has been read
-        if (wq == 0 && (lane & 15) == 0) {
-#pragma unroll
-          for (int k = 0; k < NC; ++k) {
-            s_m[cg + k] = m[k];
-            red[cg + k] = a[k];
-          }
-        }
-        if (!first) {
-          // O *= alpha, once the PV product of the tile before is done
-          if (g >= 1) ok = waits.lazy(&bar[L::B_P_EMPTY], (g - 1) & 1);
-          if (!named_bar_and(barid, 128, ok)) break;
-          tc_fence_after();
-#pragma unroll 1
-          for (int c = 0; c < 4 * NG; c += NO) {
-            uint32_t o[NO];
-            const uint32_t oa = tmem + lanes + L::kTmemO + (c / NG) * N + grp * NG + c % NG;
-            tmem_get(oa, o);
-#pragma unroll
-            for (int k = 0; k < NO; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * red[c % NG + k]);
-            tmem_put(oa, o);
-          }
-          tmem_wait_st();
-          tc_fence_before();
-        }
-        named_bar_sync(barid, 128);   // alpha has been read
-      }
-      // ---- weights, row sums, P^T
-      uint32_t pk[NC / 2];
-#pragma unroll
-      for (int k = 0; k < NC; k += 2) {
-        const float p = fast_exp2(x[k] - m[k]), q = fast_exp2(x[k + 1] - m[k + 1]);   // masked: exp2(-inf) = 0
-        l[k] += p;
-        l[k + 1] += q;
-        pk[k / 2] = pack2<BF16>(p, q);
-      }
-      if (g >= 1) ok = ok && waits.lazy(&bar[L::B_P_EMPTY], (g - 1) & 1);
-      ok = __all_sync(0xffffffffu, ok);
+      for (int k = 0; k < NC; ++k) top = fmaxf(top, x[k] - m[k]);
+      uint4 pk = weights(x, p);
+      if (g >= 1) ok = __all_sync(0xffffffffu, ok && waits.lazy(&bar[L::B_P_EMPTY], (g - 1) & 1)) != 0;
       if (ok) {
-        *reinterpret_cast<uint4*>(sP + p_offset(tok, lane >> 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+        *reinterpret_cast<uint4*>(sP + p_offset(tok, lane >> 4)) = pk;
+        const bool over = __any_sync(0xffffffffu, top > kThresh) != 0;
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar[L::B_P_FULL]);
+        if (lane == 0) {
+          // (three tiles' flags in turn: every reader of the ones cleared here
+          // is behind P_FULL of the tile before, every writer behind this one)
+          if (wq == 0) flags[((g + 1) % 3) * 4 + grp] = 0;
+          if (over) flags[(g % 3) * 4 + grp] = 1;
+          mbar_arrive(&bar[L::B_P_FULL]);
+        }
+        __syncwarp();
+        ok = __all_sync(0xffffffffu, waits.lazy(&bar[L::B_P_FULL], g & 1)) != 0;
       }
+      if (ok) {
+        const volatile int* fl = flags + (g % 3) * 4;
+        int any = fl[grp];
+#pragma unroll
+        for (int k = 0; k < L::kGroups; ++k) any |= fl[k] << 1;
+        if (any) {
+          if (any & 1) {
+            if (!new_maxima(x, false, ok)) break;
+            pk = weights(x, p);
+            *reinterpret_cast<uint4*>(sP + p_offset(tok, lane >> 4)) = pk;
+            fence_proxy_async_smem();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar[L::B_P_FIXED]);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < NC; ++k) l[k] += p[k];
       if (it.last()) {
         // ---- epilogue of the piece: row sums over the tokens, O / l, LSE
         ok = ok && waits.lazy(&bar[L::B_P_EMPTY], g & 1);
@@ -896,7 +947,7 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
     // ------------------------------------------------ unpacking
     // A lane is a token; the two halves of the latents one after the other, a
     // half's eight 32-column units spread over the warps, the RoPE columns
-    // with the second.  One fence and one arrival a half.
+    // with the first.  One fence and one arrival a half.
     constexpr int GP = L::kUW / 2, NU = 8 / GP;     // column groups; units of a half per lane
     const int w = warp - L::kUnpackWarp;
     const int t = (w & 1) * 32 + lane, grp = w >> 1;
@@ -938,51 +989,65 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
+        // decoded into registers first, so that a slot that gets free waits for
+        // the stores alone
+        uint4 x[NU][4], xr[8 / GP];
+#pragma unroll
+        for (int k = 0; k < NU; ++k) {
+          if (cur) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              x[k][j] = valid ? row[h * 32 + (k * GP + grp) * 4 + j] : make_uint4(0, 0, 0, 0);
+          } else {
+            const uint4 cw = c[h * NU + k];
+            uint32_t m0, m1, a[4];
+            multipliers(sc[h * NU + k], valid, m0, m1);
+            unpack8<BF16>(cw.x, m0, a);
+            x[k][0] = make_uint4(a[0], a[1], a[2], a[3]);
+            unpack8<BF16>(cw.y, m0, a);
+            x[k][1] = make_uint4(a[0], a[1], a[2], a[3]);
+            unpack8<BF16>(cw.z, m1, a);
+            x[k][2] = make_uint4(a[0], a[1], a[2], a[3]);
+            unpack8<BF16>(cw.w, m1, a);
+            x[k][3] = make_uint4(a[0], a[1], a[2], a[3]);
+          }
+        }
+        if (h == 0) {
+#pragma unroll
+          for (int j = 0; j < 8 / GP; ++j) {
+            if (cur) {
+              xr[j] = valid ? row[64 + grp * (8 / GP) + j] : make_uint4(0, 0, 0, 0);
+            } else {
+              uint32_t m0, m1, a[4];
+              multipliers(rsc, valid, m0, m1);
+              unpack8<BF16>(rc[j], m0, a);
+              xr[j] = make_uint4(a[0], a[1], a[2], a[3]);
+            }
+          }
+        }
         const int hc = 2 * g + h, sl = hc % L::kNH;
         if (hc >= L::kNH && !__all_sync(0xffffffffu, waits.wait(&bar[L::B_EMPTY + sl], ((hc / L::kNH) - 1) & 1))) {
           ok = false;
           break;
         }
 #pragma unroll
-        for (int k = h * NU; k < (h + 1) * NU; ++k) {
-          const int u = (k % NU) * GP + grp;                  // unit of the half
-          uint4 x[4];
-          if (cur) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) x[j] = valid ? row[h * 32 + u * 4 + j] : make_uint4(0, 0, 0, 0);
-          } else {
-            uint32_t m0, m1, a[4];
-            multipliers(sc[k], valid, m0, m1);
-            unpack8<BF16>(c[k].x, m0, a);
-            x[0] = make_uint4(a[0], a[1], a[2], a[3]);
-            unpack8<BF16>(c[k].y, m0, a);
-            x[1] = make_uint4(a[0], a[1], a[2], a[3]);
-            unpack8<BF16>(c[k].z, m1, a);
-            x[2] = make_uint4(a[0], a[1], a[2], a[3]);
-            unpack8<BF16>(c[k].w, m1, a);
-            x[3] = make_uint4(a[0], a[1], a[2], a[3]);
-          }
+        for (int k = 0; k < NU; ++k) {
+          const int u = k * GP + grp;                         // 32-column unit of the half
           uint8_t* d = half0 + sl * kHalf + (u >> 1) * kChunk;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(d + sw128_offset(t, (u & 1) * 4 + j)) = x[j];
+          for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(d + sw128_offset(t, (u & 1) * 4 + j)) = x[k][j];
         }
-        if (h == 1) {
-          // (the RoPE slot's last readers were done before this half slot's)
-          uint8_t* d = smem + L::kRopeOff + (g % L::kNR) * kChunk;
-          uint32_t m0, m1, a[4];
-          multipliers(rsc, valid, m0, m1);
-#pragma unroll
-          for (int j = 0; j < 8 / GP; ++j) {
-            const int u = grp * (8 / GP) + j;                 // 16-byte unit of the chunk
-            uint4 x;
-            if (cur) {
-              x = valid ? row[64 + u] : make_uint4(0, 0, 0, 0);
-            } else {
-              unpack8<BF16>(rc[j], m0, a);
-              x = make_uint4(a[0], a[1], a[2], a[3]);
-            }
-            *reinterpret_cast<uint4*>(d + sw128_offset(t, u)) = x;
+        if (h == 0) {
+          // (with two RoPE slots the last reader of this one was done before the
+          // half slot's)
+          if (L::kNR == 1 && g >= 1 && !__all_sync(0xffffffffu, waits.wait(&bar[L::B_ROPE_EMPTY], (g - 1) & 1))) {
+            ok = false;
+            break;
           }
+          uint8_t* d = smem + L::kRopeOff + (g % L::kNR) * kChunk;
+#pragma unroll
+          for (int j = 0; j < 8 / GP; ++j)
+            *reinterpret_cast<uint4*>(d + sw128_offset(t, grp * (8 / GP) + j)) = xr[j];
         }
         fence_proxy_async_smem();
         __syncwarp();
