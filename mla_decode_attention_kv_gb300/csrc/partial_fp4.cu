@@ -24,10 +24,10 @@
 // One persistent CTA per SM, 768 or 896 threads:
 //   w0      producer: raw pages (codes, scales) by bulk copies, queries by TMA
 //   w1      QK issuer            w2  PV issuer           w3  empty parts
-//   w4-     softmax: groups of four warps with 16 rows each; a token (16 TMEM
-//           lanes a warp in an M = 64 accumulator) has two threads of a group,
-//           one for each half of its rows.  O rescale and epilogue (thread =
-//           latent)
+//   w4-     softmax: one group of four warps for 16 rows, two for more; a token
+//           (16 TMEM lanes a warp in an M = 64 accumulator) has two threads of a
+//           group, one for each half of the 16 rows at hand.  O rescale and
+//           epilogue (thread = latent)
 //   rest    unpacking: codes and scales to 128-byte-swizzled 16-bit chunks
 // A tile's 512 latents are unpacked as two halves through a ring of half slots
 // (two tiles; one and a half for 64 rows, whose queries take 72 KB), its RoPE
@@ -51,7 +51,8 @@ namespace {
 
 constexpr int kTile4 = 64;                       // tokens
 constexpr int kSoftWarp = 4;                     // first warp of the softmax
-constexpr int kGroup4 = 16;                      // rows (columns of S^T) of a softmax group
+constexpr int kPass4 = 16;                       // rows (columns of S^T) that a softmax group takes at a time
+constexpr int kUnpackWarps = 16;                 // eight for each half of a tile
 constexpr int kRawCodes = kTile4 * kE2m1Codes;   // 18432
 constexpr int kRawStage = kTile4 * kE2m1Row;     // 20736
 constexpr int kChunk = kTile4 * 128;             // 8 KB: 64 columns of a tile
@@ -66,10 +67,10 @@ template <int N>
 struct Smem4 {
   static constexpr int kNH = N == 64 ? 3 : 4;    // half slots (a tile takes two)
   static constexpr int kNR = N == 64 ? 1 : 2;    // RoPE slots
-  static constexpr int kGroups = N / kGroup4;    // softmax groups of four warps
-  static constexpr int kUW = N == 64 ? 8 : 16;   // unpacking warps
+  static constexpr int kGroups = N == 16 ? 1 : 2;              // softmax groups of four warps
+  static constexpr int kPasses = N / (kPass4 * kGroups);       // sixteen rows each
   static constexpr int kUnpackWarp = kSoftWarp + 4 * kGroups;
-  static constexpr int kThreads = (kUnpackWarp + kUW) * 32;
+  static constexpr int kThreads = (kUnpackWarp + kUnpackWarps) * 32;
   static constexpr int kQ = N * 128 * 9;
   static constexpr int kHalfOff = 0;
   static constexpr int kRopeOff = kHalfOff + kNH * kHalf;
@@ -79,8 +80,8 @@ struct Smem4 {
   static constexpr int kRawOff = kPOff + kP;
   static constexpr int kMOff = kRawOff + 2 * kRawStage;      // reference maxima [N]
   static constexpr int kRedOff = kMOff + N * 4;              // reductions over the warps [groups][4][16]
-  static constexpr int kFlagOff = kRedOff + N * 16;          // [3 tiles][4 groups]: weights past the limit
-  static constexpr int kUnitOff = kFlagOff + 48;
+  static constexpr int kFlagOff = kRedOff + kGroups * 256;          // [3 tiles][2 groups]: weights past the limit
+  static constexpr int kUnitOff = kFlagOff + 32;
   static constexpr int kBarOff = kUnitOff + ((kUnits4 * 20 + 8 + 15) / 16) * 16;
   // barrier slots
   enum : int {
@@ -386,10 +387,9 @@ __device__ __forceinline__ void tmem_put(uint32_t a, const uint32_t (&r)[8]) {
                : "memory");
 }
 
-// P^T, the MN-major B operand: each softmax group's 16 columns are a block of
-// their own, [64 tokens][16] 16-bit values with the 32-byte swizzle, LBO from
+// P^T, the MN-major B operand: each 16 columns are a block of their own, [64 tokens][16] 16-bit values with the 32-byte swizzle, LBO from
 // block to block.
-constexpr int kPRow = kGroup4 * 2;
+constexpr int kPRow = kPass4 * 2;
 constexpr int kPBlock = kTile4 * kPRow;
 constexpr int kPStep = 16 * kPRow;       // bytes from one k-step (16 tokens) to the next
 __device__ __forceinline__ uint64_t p_desc(uint32_t addr) {
@@ -490,12 +490,12 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bar[L::B_RAW_FULL + s], 1);
-      mbar_init(&bar[L::B_RAW_EMPTY + s], L::kUW);
+      mbar_init(&bar[L::B_RAW_EMPTY + s], kUnpackWarps);
       mbar_init(&bar[L::B_S_FULL + s], 1);
       mbar_init(&bar[L::B_S_EMPTY + s], 4 * L::kGroups);
     }
     for (int s = 0; s < L::kNH; ++s) {
-      mbar_init(&bar[L::B_FULL + s], L::kUW);
+      mbar_init(&bar[L::B_FULL + s], kUnpackWarps / 2);
       mbar_init(&bar[L::B_EMPTY + s], 1);
     }
     mbar_init(&bar[L::B_Q_FULL], 1);
@@ -504,7 +504,7 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
     mbar_init(&bar[L::B_P_EMPTY], 1);
     mbar_init(&bar[L::B_P_FIXED], 4 * L::kGroups);
     mbar_init(&bar[L::B_ROPE_EMPTY], 1);
-    for (int k = 0; k < 12; ++k) reinterpret_cast<int*>(smem + L::kFlagOff)[k] = 0;
+    for (int k = 0; k < 6; ++k) reinterpret_cast<int*>(smem + L::kFlagOff)[k] = 0;
     mbar_init(&bar[L::B_DONE_QK], 1);
     mbar_init(&bar[L::B_DONE_PV], 1);
     *abort_flag = 0;
@@ -675,8 +675,8 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
           break;
         }
         // weights past the limit are made again first (the softmax, below)
-        const volatile int* fl = reinterpret_cast<const volatile int*>(smem + L::kFlagOff) + (g % 3) * 4;
-        if (fl[0] | fl[1] | fl[2] | fl[3]) {
+        const volatile int* fl = reinterpret_cast<const volatile int*>(smem + L::kFlagOff) + (g % 3) * 2;
+        if (fl[0] | fl[1]) {
           if (!wait(&bar[L::B_P_FIXED], nfix & 1)) {
             ok = false;
             break;
@@ -721,33 +721,37 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
     }
   } else if (warp < L::kUnpackWarp) {
     // ------------------------------------------------ softmax, O rescale, epilogue
-    // Groups of four warps with 16 of the rows (columns of S^T) each and nothing
-    // shared between them: a token's columns are its two threads', eight each.
-    constexpr int NG = kGroup4, NC = NG / 2;   // columns of a group, of a thread
+    // Groups of four warps with an equal share of the rows (columns of S^T) each
+    // and nothing shared between them; a group takes its rows 16 at a time, and
+    // a token's 16 columns are its two threads', eight each.
+    constexpr int NG = kPass4, NC = NG / 2, PASSES = L::kPasses;
     constexpr int NO = 8;                      // columns of O at a time
     const int grp = (warp - kSoftWarp) >> 2, wq = warp & 3;
     const int barid = 1 + grp;
     const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
     const int tok = wq * 16 + (lane & 15);     // token of the tile
-    const int cg = (lane >> 4) * NC;           // first column of this thread in the group
-    const int cr = cg + ((lane & 15) >> 1);    // column of the group that col_reduce leaves here
-    uint8_t* sP = smem + L::kPOff + grp * kPBlock;   // this group's block
-    // a warp's staging of the epilogue: its quarter of the group's block of P,
-    // which no MMA reads then
-    uint8_t* stage = sP + wq * (kPBlock / 4);
-    float* s_m = reinterpret_cast<float*>(smem + L::kMOff) + grp * NG;
+    const int cg = (lane >> 4) * NC;           // first column of this thread among the 16
+    const int cr = cg + ((lane & 15) >> 1);    // column that col_reduce leaves here
     float* red = reinterpret_cast<float*>(smem + L::kRedOff) + grp * (4 * NG);   // [4][NG]
-    float l[NC], m[NC];
-#pragma unroll
-    for (int k = 0; k < NC; ++k) l[k] = m[k] = 0.f;
+    volatile int* flags = reinterpret_cast<volatile int*>(smem + L::kFlagOff);
+    float l[PASSES][NC], m[PASSES][NC];
     Iter4<N> it;
     it.start(fp, tab, rng);
     int g = 0;
     bool ok = true;
-    // New reference maxima of the group's rows from the tile's scores x, O and l
-    // brought to them (not for a piece's first tile).  False: time to leave.
-    auto new_maxima = [&](const float (&x)[NC], bool first, bool ok) {
-      if (!named_bar_and(barid, 128, ok)) return false;
+    // first column and P block of pass q
+    auto col0 = [&](int q) { return (grp * PASSES + q) * NG; };
+    auto block = [&](int q) { return smem + L::kPOff + (grp * PASSES + q) * kPBlock; };
+    // the tile's scores of pass q in the log2 domain, columns below nmin masked
+    auto scores = [&](int q, float sl, int nmin, float (&x)[NC]) {
+      uint32_t v[NC];
+      tmem_half(tmem + lanes + L::kTmemS + (g & 1) * N + col0(q), v);
+#pragma unroll
+      for (int k = 0; k < NC; ++k) x[k] = col0(q) + cg + k >= nmin ? __uint_as_float(v[k]) * sl : -INFINITY;
+    };
+    // New reference maxima of 16 rows from the tile's scores x, with O and l
+    // brought to them (not for a piece's first tile).
+    auto new_maxima = [&](int q, const float (&x)[NC], float (&lq)[NC], float (&mq)[NC], bool first) {
       float y[NC];
 #pragma unroll
       for (int k = 0; k < NC; ++k) y[k] = x[k];
@@ -761,19 +765,20 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
         const float t = fmaxf(fmaxf(r[0], r[NG]), fmaxf(r[2 * NG], r[3 * NG]));
         a[k] = 1.f;
         if (first) {
-          m[k] = t == -INFINITY ? 0.f : t;
-          l[k] = 0.f;
-        } else if (t > m[k] + kThresh) {
-          a[k] = fast_exp2(m[k] - t);
-          m[k] = t;
-          l[k] *= a[k];
+          mq[k] = t == -INFINITY ? 0.f : t;
+          lq[k] = 0.f;
+        } else if (t > mq[k] + kThresh) {
+          a[k] = fast_exp2(mq[k] - t);
+          mq[k] = t;
+          lq[k] *= a[k];
         }
       }
       named_bar_sync(barid, 128);   // red has been read
       if (wq == 0 && (lane & 15) == 0) {
+        float* s_m = reinterpret_cast<float*>(smem + L::kMOff) + col0(q) + cg;
 #pragma unroll
         for (int k = 0; k < NC; ++k) {
-          s_m[cg + k] = m[k];
+          s_m[k] = mq[k];
           red[cg + k] = a[k];
         }
       }
@@ -784,7 +789,7 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
 #pragma unroll 1
         for (int c = 0; c < 4 * NG; c += NO) {
           uint32_t o[NO];
-          const uint32_t oa = tmem + lanes + L::kTmemO + (c / NG) * N + grp * NG + c % NG;
+          const uint32_t oa = tmem + lanes + L::kTmemO + (c / NG) * N + col0(q) + c % NG;
           tmem_get(oa, o);
 #pragma unroll
           for (int k = 0; k < NO; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * red[c % NG + k]);
@@ -794,265 +799,268 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
         tc_fence_before();
         named_bar_sync(barid, 128);   // alpha has been read
       }
-      return true;
     };
-    // weights of the tile's scores, and P^T written
-    auto weights = [&](const float (&x)[NC], float (&p)[NC]) {
+    // weights p of the scores against the maxima (masked: exp2(-inf) = 0), in 16 bits
+    auto weights = [&](const float (&x)[NC], const float (&mq)[NC], float (&p)[NC]) {
       uint32_t pk[NC / 2];
 #pragma unroll
       for (int k = 0; k < NC; k += 2) {
-        p[k] = fast_exp2(x[k] - m[k]);   // masked: exp2(-inf) = 0
-        p[k + 1] = fast_exp2(x[k + 1] - m[k + 1]);
+        p[k] = fast_exp2(x[k] - mq[k]);
+        p[k + 1] = fast_exp2(x[k + 1] - mq[k + 1]);
         pk[k / 2] = pack2<BF16>(p[k], p[k + 1]);
       }
       return make_uint4(pk[0], pk[1], pk[2], pk[3]);
     };
-    volatile int* flags = reinterpret_cast<volatile int*>(smem + L::kFlagOff);
     while (it.valid) {
       const Unit4 ui = it.ui;
       const int sb = g & 1;
       const bool cur = ui.p == fp.S, first = it.first();
       const float sl = cur ? fp.scale_log2 : fp.scale_log2 * fp.kv_scale;
-      // columns below nmin are masked for this thread's token: all of a token
-      // past the end; in the CURRENT part the rows of earlier query tokens
+      // rows below nmin are masked for this thread's token: all of a token past
+      // the end; in the CURRENT part the rows of earlier query tokens
       int nmin = N;
       if (it.tok0() + tok < ui.hi) nmin = cur ? min(N, max(0, tok * fp.H - ui.g * N)) : 0;
-      nmin -= grp * NG + cg;
       ok = __all_sync(0xffffffffu, ok && waits.lazy(&bar[L::B_S_FULL + sb], (g >> 1) & 1)) != 0;
       tc_fence_after();
-      uint32_t v[NC];
-      tmem_half(tmem + lanes + L::kTmemS + sb * N + grp * NG, v);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar[L::B_S_EMPTY + sb]);
-      // scores in the log2 domain
-      float x[NC], p[NC];
+      if (first) {
+        if (!named_bar_and(barid, 128, ok)) break;
 #pragma unroll
-      for (int k = 0; k < NC; ++k) x[k] = k >= nmin ? __uint_as_float(v[k]) * sl : -INFINITY;
-      if (first && !new_maxima(x, true, ok)) break;
-      // The weights are made and handed over against the reference maximum as
-      // it stands; a warp that finds one past 2^8 raises its group's flag of
+        for (int q = 0; q < PASSES; ++q) {
+          float x[NC];
+          scores(q, sl, nmin, x);
+          new_maxima(q, x, l[q], m[q], true);
+        }
+      }
+      // The weights are made and handed over against the reference maxima as
+      // they stand; a warp that finds one past 2^8 raises its group's flag of
       // this tile, and the group makes them again before the PV product, which
       // looks at the flags, reads them.  (A barrier to agree first cost 500
       // cycles of every tile.)
-      float top = -INFINITY;
+      uint4 pk[PASSES];
+      uint32_t over = 0;   // passes of this warp with such a weight: not in l yet
 #pragma unroll
-      for (int k = 0; k < NC; ++k) top = fmaxf(top, x[k] - m[k]);
-      uint4 pk = weights(x, p);
+      for (int q = 0; q < PASSES; ++q) {
+        float x[NC], p[NC];
+        scores(q, sl, nmin, x);
+        float top = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < NC; ++k) top = fmaxf(top, x[k] - m[q][k]);
+        pk[q] = weights(x, m[q], p);
+        if (__any_sync(0xffffffffu, top > kThresh)) {
+          over |= 1u << q;
+        } else {
+#pragma unroll
+          for (int k = 0; k < NC; ++k) l[q][k] += p[k];
+        }
+      }
       if (g >= 1) ok = __all_sync(0xffffffffu, ok && waits.lazy(&bar[L::B_P_EMPTY], (g - 1) & 1)) != 0;
       if (ok) {
-        *reinterpret_cast<uint4*>(sP + p_offset(tok, lane >> 4)) = pk;
-        const bool over = __any_sync(0xffffffffu, top > kThresh) != 0;
+#pragma unroll
+        for (int q = 0; q < PASSES; ++q) *reinterpret_cast<uint4*>(block(q) + p_offset(tok, lane >> 4)) = pk[q];
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          // (three tiles' flags in turn: every reader of the ones cleared here
+          // (three tiles' flags in turn: every reader of the one cleared here
           // is behind P_FULL of the tile before, every writer behind this one)
-          if (wq == 0) flags[((g + 1) % 3) * 4 + grp] = 0;
-          if (over) flags[(g % 3) * 4 + grp] = 1;
+          if (wq == 0) flags[((g + 1) % 3) * 2 + grp] = 0;
+          if (over) flags[(g % 3) * 2 + grp] = 1;
           mbar_arrive(&bar[L::B_P_FULL]);
         }
         __syncwarp();
         ok = __all_sync(0xffffffffu, waits.lazy(&bar[L::B_P_FULL], g & 1)) != 0;
       }
       if (ok) {
-        const volatile int* fl = flags + (g % 3) * 4;
-        int any = fl[grp];
+        const int mine = flags[(g % 3) * 2 + grp], other = flags[(g % 3) * 2 + (grp ^ 1)];
+        if (mine | other) {
+          if (mine) {
+            if (!named_bar_and(barid, 128, ok)) break;
 #pragma unroll
-        for (int k = 0; k < L::kGroups; ++k) any |= fl[k] << 1;
-        if (any) {
-          if (any & 1) {
-            if (!new_maxima(x, false, ok)) break;
-            pk = weights(x, p);
-            *reinterpret_cast<uint4*>(sP + p_offset(tok, lane >> 4)) = pk;
+            for (int q = 0; q < PASSES; ++q) {
+              float x[NC], p[NC];
+              scores(q, sl, nmin, x);
+              if (!(over >> q & 1)) {
+#pragma unroll
+                for (int k = 0; k < NC; ++k) l[q][k] -= fast_exp2(x[k] - m[q][k]);
+              }
+              new_maxima(q, x, l[q], m[q], false);
+              const uint4 w = weights(x, m[q], p);
+#pragma unroll
+              for (int k = 0; k < NC; ++k) l[q][k] += p[k];
+              *reinterpret_cast<uint4*>(block(q) + p_offset(tok, lane >> 4)) = w;
+            }
             fence_proxy_async_smem();
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar[L::B_P_FIXED]);
         }
       }
-#pragma unroll
-      for (int k = 0; k < NC; ++k) l[k] += p[k];
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar[L::B_S_EMPTY + sb]);
       if (it.last()) {
         // ---- epilogue of the piece: row sums over the tokens, O / l, LSE
-        ok = ok && waits.lazy(&bar[L::B_P_EMPTY], g & 1);
+        ok = __all_sync(0xffffffffu, ok && waits.lazy(&bar[L::B_P_EMPTY], g & 1)) != 0;
         if (!named_bar_and(barid, 128, ok)) break;
         tc_fence_after();
-        const float part = col_reduce<NC, false>(l, lane);
-        red[wq * NG + cr] = part;
-        named_bar_sync(barid, 128);
         const bool whole = it.whole();
         const int slot = 2 * cid + (it.u == rng.u_begin ? 0 : 1);
-        // row k of the group in lane k
         const int esz = fp.part_dtype == kFP32 ? 4 : 2;
-        float sum = 1.f;
-        if (lane < NG) sum = (red[lane] + red[NG + lane]) + (red[2 * NG + lane] + red[3 * NG + lane]);
-        named_bar_sync(barid, 128);
-        float* inv = red;                                        // [NG]
-        int64_t* dst = reinterpret_cast<int64_t*>(red + NG);     // [NG] byte offset of the row, -1: none
-        if (wq == 0 && lane < NG) {
-          const float lse2 = s_m[lane] + log2f(sum);
-          const int n = grp * NG + lane, r = ui.g * N + n;
-          int64_t row = -1;
-          if (r < fp.R) {
-            row = whole ? out_row4(fp, ui.b, r, ui.p) : static_cast<int64_t>(slot) * N + n;
-            if (whole) fp.lse_part[row] = lse2 * kLn2;
-            else fp.ws_lse[row] = lse2;
-          }
-          inv[lane] = (cur ? 1.f : fp.kv_scale) / sum;
-          dst[lane] = row < 0 ? -1 : row * 512 * esz;
-        }
-        named_bar_sync(barid, 128);
-        // NO rows of 32 latents at a time through the warp's staging: written a
-        // latent per lane, read back and stored 16 bytes per lane along the rows
         char* out = static_cast<char*>(whole ? fp.o_part : fp.ws_o);
+#pragma unroll
+        for (int q = 0; q < PASSES; ++q) {
+          const float part = col_reduce<NC, false>(l[q], lane);
+          red[wq * NG + cr] = part;
+          named_bar_sync(barid, 128);
+          // row k of the 16 in lane k
+          float sum = 1.f;
+          if (lane < NG) sum = (red[lane] + red[NG + lane]) + (red[2 * NG + lane] + red[3 * NG + lane]);
+          named_bar_sync(barid, 128);
+          float* inv = red;                                        // [NG]
+          int64_t* dst = reinterpret_cast<int64_t*>(red + NG);     // [NG] byte offset of the row, -1: none
+          if (wq == 0 && lane < NG) {
+            const int n = col0(q) + lane, r = ui.g * N + n;
+            const float lse2 = reinterpret_cast<const float*>(smem + L::kMOff)[n] + log2f(sum);
+            int64_t row = -1;
+            if (r < fp.R) {
+              row = whole ? out_row4(fp, ui.b, r, ui.p) : static_cast<int64_t>(slot) * N + n;
+              if (whole) fp.lse_part[row] = lse2 * kLn2;
+              else fp.ws_lse[row] = lse2;
+            }
+            inv[lane] = (cur ? 1.f : fp.kv_scale) / sum;
+            dst[lane] = row < 0 ? -1 : row * 512 * esz;
+          }
+          named_bar_sync(barid, 128);
+          // NO rows of 32 latents at a time through the warp's staging (its
+          // quarter of the rows' block of P, which no MMA reads now): written a
+          // latent per lane, read back and stored 16 bytes per lane along the rows
+          uint8_t* stage = block(q) + wq * (kPBlock / 4);
 #pragma unroll 1
-        for (int c = 0; c < 4 * NG; c += NO) {
-          uint32_t o[NO];
-          const int n0 = c % NG;
-          tmem_get(tmem + lanes + L::kTmemO + (c / NG) * N + grp * NG + n0, o);
-          const int lat0 = (c / NG) * 128 + wq * 32;
+          for (int c = 0; c < 4 * NG; c += NO) {
+            uint32_t o[NO];
+            const int n0 = c % NG;
+            tmem_get(tmem + lanes + L::kTmemO + (c / NG) * N + col0(q) + n0, o);
+            const int lat0 = (c / NG) * 128 + wq * 32;
 #pragma unroll
-          for (int k = 0; k < NO; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * inv[n0 + k]);
-          if (esz == 2) {
+            for (int k = 0; k < NO; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * inv[n0 + k]);
+            if (esz == 2) {
 #pragma unroll
-            for (int k = 0; k < NO; ++k)
-              reinterpret_cast<uint16_t*>(stage)[k * 32 + lane] =
-                  static_cast<uint16_t>(pack2_dt(__uint_as_float(o[k]), 0.f, fp.part_dtype));
-            __syncwarp();
-            const uint4 x = *reinterpret_cast<const uint4*>(stage + lane * 16);
-            const int64_t d = dst[n0 + (lane >> 2)];
-            if (d >= 0) *reinterpret_cast<uint4*>(out + d + lat0 * 2 + (lane & 3) * 16) = x;
-            __syncwarp();
-          } else {
-#pragma unroll
-            for (int h = 0; h < NO; h += NO / 2) {
-#pragma unroll
-              for (int k = 0; k < NO / 2; ++k) reinterpret_cast<uint32_t*>(stage)[k * 32 + lane] = o[h + k];
+              for (int k = 0; k < NO; ++k)
+                reinterpret_cast<uint16_t*>(stage)[k * 32 + lane] =
+                    static_cast<uint16_t>(pack2_dt(__uint_as_float(o[k]), 0.f, fp.part_dtype));
               __syncwarp();
               const uint4 x = *reinterpret_cast<const uint4*>(stage + lane * 16);
-              const int64_t d = dst[n0 + h + (lane >> 3)];
-              if (d >= 0) *reinterpret_cast<uint4*>(out + d + lat0 * 4 + (lane & 7) * 16) = x;
+              const int64_t d = dst[n0 + (lane >> 2)];
+              if (d >= 0) *reinterpret_cast<uint4*>(out + d + lat0 * 2 + (lane & 3) * 16) = x;
               __syncwarp();
+            } else {
+#pragma unroll
+              for (int h = 0; h < NO; h += NO / 2) {
+#pragma unroll
+                for (int k = 0; k < NO / 2; ++k) reinterpret_cast<uint32_t*>(stage)[k * 32 + lane] = o[h + k];
+                __syncwarp();
+                const uint4 x = *reinterpret_cast<const uint4*>(stage + lane * 16);
+                const int64_t d = dst[n0 + h + (lane >> 3)];
+                if (d >= 0) *reinterpret_cast<uint4*>(out + d + lat0 * 4 + (lane & 7) * 16) = x;
+                __syncwarp();
+              }
             }
           }
+          tc_fence_before();
+          named_bar_sync(barid, 128);   // red has been read
         }
-        tc_fence_before();
-        named_bar_sync(barid, 128);   // red and s_m have been read
       }
       it.advance(fp);
       ++g;
     }
   } else {
     // ------------------------------------------------ unpacking
-    // A lane is a token; the two halves of the latents one after the other, a
-    // half's eight 32-column units spread over the warps, the RoPE columns
-    // with the first.  One fence and one arrival a half.
-    constexpr int GP = L::kUW / 2, NU = 8 / GP;     // column groups; units of a half per lane
+    // Eight warps for each half of the latents; a lane is a token, and its two
+    // 32-column units of the half (the RoPE columns too, in the first) are decoded into
+    // registers ahead of the slot, so that a slot that gets free waits for the
+    // stores alone.  One fence and one arrival a tile and warp.
     const int w = warp - L::kUnpackWarp;
-    const int t = (w & 1) * 32 + lane, grp = w >> 1;
+    const int h = w >> 3, t = (w & 1) * 32 + lane, grp = (w >> 1) & 3;
     uint8_t* half0 = smem + L::kHalfOff;
     Iter4<N> it;
     it.start(fp, tab, rng);
     int g = 0, rs = 0;
-    bool ok = true;
-    while (ok && it.valid) {
+    while (it.valid) {
       const bool cur = it.ui.p == fp.S;
       const bool valid = it.tok0() + t < it.ui.hi;
-      uint4 c[2 * NU] = {};
-      uint32_t sc[2 * NU] = {}, rc[2] = {0, 0}, rsc = 0;
-      const uint4* row = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(fp.kv_cur) +
-                                                        (static_cast<int64_t>(it.ui.b) * fp.q_len + t) * 576);
+      uint4 x[2][4], xr[2];
       if (!cur) {
         const int st = rs & 1;
         if (!__all_sync(0xffffffffu, waits.wait(&bar[L::B_RAW_FULL + st], (rs >> 1) & 1))) break;
         const uint8_t* codes = smem + L::kRawOff + st * kRawStage + t * kE2m1Codes;
         const uint8_t* scales = smem + L::kRawOff + st * kRawStage + kRawCodes + t * kE2m1Scales;
+        uint4 c[2];
+        uint32_t sc[2], rsc = 0;
+        uint2 rc = make_uint2(0, 0);
 #pragma unroll
-        for (int k = 0; k < 2 * NU; ++k) {
-          const int u = (k / NU) * 8 + (k % NU) * GP + grp;   // 32-column unit of the 16
+        for (int k = 0; k < 2; ++k) {
+          const int u = h * 8 + k * 4 + grp;                  // 32-column unit of the 16
           c[k] = *reinterpret_cast<const uint4*>(codes + u * 16);
           sc[k] = *reinterpret_cast<const uint16_t*>(scales + u * 2);
         }
-        if constexpr (GP == 8) {
-          rc[0] = *reinterpret_cast<const uint32_t*>(codes + 256 + grp * 4);
-          rsc = scales[32 + grp / 2];
-        } else {
-          const uint2 x = *reinterpret_cast<const uint2*>(codes + 256 + grp * 8);
-          rc[0] = x.x;
-          rc[1] = x.y;
+        if (h == 0) {
+          rc = *reinterpret_cast<const uint2*>(codes + 256 + grp * 8);
           rsc = scales[32 + grp];
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar[L::B_RAW_EMPTY + st]);
         ++rs;
-      }
+        uint32_t m0, m1, a[4];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        // decoded into registers first, so that a slot that gets free waits for
-        // the stores alone
-        uint4 x[NU][4], xr[8 / GP];
-#pragma unroll
-        for (int k = 0; k < NU; ++k) {
-          if (cur) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              x[k][j] = valid ? row[h * 32 + (k * GP + grp) * 4 + j] : make_uint4(0, 0, 0, 0);
-          } else {
-            const uint4 cw = c[h * NU + k];
-            uint32_t m0, m1, a[4];
-            multipliers(sc[h * NU + k], valid, m0, m1);
-            unpack8<BF16>(cw.x, m0, a);
-            x[k][0] = make_uint4(a[0], a[1], a[2], a[3]);
-            unpack8<BF16>(cw.y, m0, a);
-            x[k][1] = make_uint4(a[0], a[1], a[2], a[3]);
-            unpack8<BF16>(cw.z, m1, a);
-            x[k][2] = make_uint4(a[0], a[1], a[2], a[3]);
-            unpack8<BF16>(cw.w, m1, a);
-            x[k][3] = make_uint4(a[0], a[1], a[2], a[3]);
-          }
+        for (int k = 0; k < 2; ++k) {
+          multipliers(sc[k], valid, m0, m1);
+          unpack8<BF16>(c[k].x, m0, a);
+          x[k][0] = make_uint4(a[0], a[1], a[2], a[3]);
+          unpack8<BF16>(c[k].y, m0, a);
+          x[k][1] = make_uint4(a[0], a[1], a[2], a[3]);
+          unpack8<BF16>(c[k].z, m1, a);
+          x[k][2] = make_uint4(a[0], a[1], a[2], a[3]);
+          unpack8<BF16>(c[k].w, m1, a);
+          x[k][3] = make_uint4(a[0], a[1], a[2], a[3]);
         }
         if (h == 0) {
-#pragma unroll
-          for (int j = 0; j < 8 / GP; ++j) {
-            if (cur) {
-              xr[j] = valid ? row[64 + grp * (8 / GP) + j] : make_uint4(0, 0, 0, 0);
-            } else {
-              uint32_t m0, m1, a[4];
-              multipliers(rsc, valid, m0, m1);
-              unpack8<BF16>(rc[j], m0, a);
-              xr[j] = make_uint4(a[0], a[1], a[2], a[3]);
-            }
-          }
+          multipliers(rsc, valid, m0, m1);
+          unpack8<BF16>(rc.x, m0, a);
+          xr[0] = make_uint4(a[0], a[1], a[2], a[3]);
+          unpack8<BF16>(rc.y, m0, a);
+          xr[1] = make_uint4(a[0], a[1], a[2], a[3]);
         }
-        const int hc = 2 * g + h, sl = hc % L::kNH;
-        if (hc >= L::kNH && !__all_sync(0xffffffffu, waits.wait(&bar[L::B_EMPTY + sl], ((hc / L::kNH) - 1) & 1))) {
-          ok = false;
-          break;
-        }
+      } else {
+        const uint4* row = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(fp.kv_cur) +
+                                                          (static_cast<int64_t>(it.ui.b) * fp.q_len + t) * 576);
+        const uint4 none = make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int k = 0; k < NU; ++k) {
-          const int u = k * GP + grp;                         // 32-column unit of the half
-          uint8_t* d = half0 + sl * kHalf + (u >> 1) * kChunk;
+        for (int k = 0; k < 2; ++k)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(d + sw128_offset(t, (u & 1) * 4 + j)) = x[k][j];
-        }
-        if (h == 0) {
-          // (with two RoPE slots the last reader of this one was done before the
-          // half slot's)
-          if (L::kNR == 1 && g >= 1 && !__all_sync(0xffffffffu, waits.wait(&bar[L::B_ROPE_EMPTY], (g - 1) & 1))) {
-            ok = false;
-            break;
-          }
-          uint8_t* d = smem + L::kRopeOff + (g % L::kNR) * kChunk;
+          for (int j = 0; j < 4; ++j) x[k][j] = valid ? row[h * 32 + (k * 4 + grp) * 4 + j] : none;
 #pragma unroll
-          for (int j = 0; j < 8 / GP; ++j)
-            *reinterpret_cast<uint4*>(d + sw128_offset(t, grp * (8 / GP) + j)) = xr[j];
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar[L::B_FULL + sl]);
+        for (int j = 0; j < 2; ++j) xr[j] = valid && h == 0 ? row[64 + grp * 2 + j] : none;
       }
+      const int hc = 2 * g + h, sl = hc % L::kNH;
+      if (hc >= L::kNH && !__all_sync(0xffffffffu, waits.wait(&bar[L::B_EMPTY + sl], ((hc / L::kNH) - 1) & 1))) break;
+      // (with two RoPE slots the last reader of this one was done before the half slot's)
+      if (L::kNR == 1 && h == 0 && g >= 1 &&
+          !__all_sync(0xffffffffu, waits.wait(&bar[L::B_ROPE_EMPTY], (g - 1) & 1)))
+        break;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int u = k * 4 + grp;                            // 32-column unit of the half
+        uint8_t* d = half0 + sl * kHalf + (u >> 1) * kChunk;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(d + sw128_offset(t, (u & 1) * 4 + j)) = x[k][j];
+      }
+      if (h == 0) {
+        uint8_t* d = smem + L::kRopeOff + (g % L::kNR) * kChunk;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) *reinterpret_cast<uint4*>(d + sw128_offset(t, grp * 2 + j)) = xr[j];
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar[L::B_FULL + sl]);
       it.advance(fp);
       ++g;
     }
