@@ -21,14 +21,14 @@
 // x rows columns of tensor memory, at most half of it, so one CTA holds all of
 // a unit, and several query tokens' rows share one pass over the history.
 //
-// One persistent CTA per SM, 768 or 896 threads:
+// One persistent CTA per SM, 896 threads:
 //   w0      producer: raw pages (codes, scales) by bulk copies, queries by TMA
 //   w1      QK issuer            w2  PV issuer           w3  empty parts
-//   w4-     softmax: one group of four warps for 16 rows, two for more; a token
-//           (16 TMEM lanes a warp in an M = 64 accumulator) has two threads of a
-//           group, one for each half of the 16 rows at hand.  O rescale and
-//           epilogue (thread = latent)
-//   rest    unpacking: codes and scales to 128-byte-swizzled 16-bit chunks
+//   w4-11   softmax: two groups of four warps with half of the rows each, 8 or
+//           16 at a time; a token (16 TMEM lanes a warp in an M = 64 accumulator)
+//           has two threads of a group, one for each half of the rows at hand.
+//           O rescale and epilogue (thread = latent)
+//   w12-27  unpacking: codes and scales to 128-byte-swizzled 16-bit chunks
 // A tile's 512 latents are unpacked as two halves through a ring of half slots
 // (two tiles; one and a half for 64 rows, whose queries take 72 KB), its RoPE
 // columns with the first: the QK MMAs of a half start while the other is
@@ -51,7 +51,7 @@ namespace {
 
 constexpr int kTile4 = 64;                       // tokens
 constexpr int kSoftWarp = 4;                     // first warp of the softmax
-constexpr int kPass4 = 16;                       // rows (columns of S^T) that a softmax group takes at a time
+constexpr int kGroups4 = 2;                      // softmax groups of four warps
 constexpr int kUnpackWarps = 16;                 // eight for each half of a tile
 constexpr int kRawCodes = kTile4 * kE2m1Codes;   // 18432
 constexpr int kRawStage = kTile4 * kE2m1Row;     // 20736
@@ -67,9 +67,9 @@ template <int N>
 struct Smem4 {
   static constexpr int kNH = N == 64 ? 3 : 4;    // half slots (a tile takes two)
   static constexpr int kNR = N == 64 ? 1 : 2;    // RoPE slots
-  static constexpr int kGroups = N == 16 ? 1 : 2;              // softmax groups of four warps
-  static constexpr int kPasses = N / (kPass4 * kGroups);       // sixteen rows each
-  static constexpr int kUnpackWarp = kSoftWarp + 4 * kGroups;
+  static constexpr int kRows = N == 16 ? 8 : 16;               // rows (columns of S^T) that a group takes at a time
+  static constexpr int kPasses = N / (kGroups4 * kRows);
+  static constexpr int kUnpackWarp = kSoftWarp + 4 * kGroups4;
   static constexpr int kThreads = (kUnpackWarp + kUnpackWarps) * 32;
   static constexpr int kQ = N * 128 * 9;
   static constexpr int kHalfOff = 0;
@@ -77,10 +77,11 @@ struct Smem4 {
   static constexpr int kQOff = kRopeOff + kNR * kChunk;
   static constexpr int kPOff = kQOff + kQ;
   static constexpr int kP = kTile4 * N * 2;
-  static constexpr int kRawOff = kPOff + kP;
+  static constexpr int kStageOff = kPOff + kP;               // 16 rows: the epilogue's staging
+  static constexpr int kRawOff = kStageOff + (N == 16 ? 4096 : 0);
   static constexpr int kMOff = kRawOff + 2 * kRawStage;      // reference maxima [N]
-  static constexpr int kRedOff = kMOff + N * 4;              // reductions over the warps [groups][4][16]
-  static constexpr int kFlagOff = kRedOff + kGroups * 256;          // [3 tiles][2 groups]: weights past the limit
+  static constexpr int kRedOff = kMOff + N * 4;              // reductions over the warps, [4][rows] for each pass
+  static constexpr int kFlagOff = kRedOff + N * 16;          // [3 tiles][2 groups]: weights past the limit
   static constexpr int kUnitOff = kFlagOff + 32;
   static constexpr int kBarOff = kUnitOff + ((kUnits4 * 20 + 8 + 15) / 16) * 16;
   // barrier slots
@@ -365,6 +366,12 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 
 // Columns [c, c + NC) of an M = 64 accumulator for lanes 0-15 of the warp and
 // [c + NC, c + 2 NC) for lanes 16-31, both of the rows in TMEM lanes 0-15.
+__device__ __forceinline__ void tmem_half(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x32bx2.x4.b32 {%0,%1,%2,%3}, [%4], 4;\n tcgen05.wait::ld.sync.aligned;"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
 __device__ __forceinline__ void tmem_half(uint32_t a, uint32_t (&r)[8]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.16x32bx2.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8], 8;\n tcgen05.wait::ld.sync.aligned;"
@@ -387,9 +394,9 @@ __device__ __forceinline__ void tmem_put(uint32_t a, const uint32_t (&r)[8]) {
                : "memory");
 }
 
-// P^T, the MN-major B operand: each 16 columns are a block of their own, [64 tokens][16] 16-bit values with the 32-byte swizzle, LBO from
-// block to block.
-constexpr int kPRow = kPass4 * 2;
+// P^T, the MN-major B operand: each 16 columns are a block of their own, [64
+// tokens][16] 16-bit values with the 32-byte swizzle, LBO from block to block.
+constexpr int kPRow = 16 * 2;
 constexpr int kPBlock = kTile4 * kPRow;
 constexpr int kPStep = 16 * kPRow;       // bytes from one k-step (16 tokens) to the next
 __device__ __forceinline__ uint64_t p_desc(uint32_t addr) {
@@ -492,7 +499,7 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
       mbar_init(&bar[L::B_RAW_FULL + s], 1);
       mbar_init(&bar[L::B_RAW_EMPTY + s], kUnpackWarps);
       mbar_init(&bar[L::B_S_FULL + s], 1);
-      mbar_init(&bar[L::B_S_EMPTY + s], 4 * L::kGroups);
+      mbar_init(&bar[L::B_S_EMPTY + s], 4 * kGroups4);
     }
     for (int s = 0; s < L::kNH; ++s) {
       mbar_init(&bar[L::B_FULL + s], kUnpackWarps / 2);
@@ -500,9 +507,9 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
     }
     mbar_init(&bar[L::B_Q_FULL], 1);
     mbar_init(&bar[L::B_Q_EMPTY], 1);
-    mbar_init(&bar[L::B_P_FULL], 4 * L::kGroups);
+    mbar_init(&bar[L::B_P_FULL], 4 * kGroups4);
     mbar_init(&bar[L::B_P_EMPTY], 1);
-    mbar_init(&bar[L::B_P_FIXED], 4 * L::kGroups);
+    mbar_init(&bar[L::B_P_FIXED], 4 * kGroups4);
     mbar_init(&bar[L::B_ROPE_EMPTY], 1);
     for (int k = 0; k < 6; ++k) reinterpret_cast<int*>(smem + L::kFlagOff)[k] = 0;
     mbar_init(&bar[L::B_DONE_QK], 1);
@@ -721,37 +728,55 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
     }
   } else if (warp < L::kUnpackWarp) {
     // ------------------------------------------------ softmax, O rescale, epilogue
-    // Groups of four warps with an equal share of the rows (columns of S^T) each
-    // and nothing shared between them; a group takes its rows 16 at a time, and
-    // a token's 16 columns are its two threads', eight each.
-    constexpr int NG = kPass4, NC = NG / 2, PASSES = L::kPasses;
+    // Two groups of four warps with half of the rows (columns of S^T) each and
+    // nothing shared between them; a group takes its rows 8 or 16 at a time, and
+    // a token has two threads of a group, one for each half of those.
+    constexpr int NG = L::kRows, NC = NG / 2, PASSES = L::kPasses;
     constexpr int NO = 8;                      // columns of O at a time
     const int grp = (warp - kSoftWarp) >> 2, wq = warp & 3;
     const int barid = 1 + grp;
     const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
     const int tok = wq * 16 + (lane & 15);     // token of the tile
-    const int cg = (lane >> 4) * NC;           // first column of this thread among the 16
-    const int cr = cg + ((lane & 15) >> 1);    // column that col_reduce leaves here
-    float* red = reinterpret_cast<float*>(smem + L::kRedOff) + grp * (4 * NG);   // [4][NG]
+    const int cg = (lane >> 4) * NC;           // first column of this thread in a pass
+    const int cr = cg + (lane & 15) / (16 / NC);   // column that col_reduce leaves here
+    auto red_of = [&](int q) { return reinterpret_cast<float*>(smem + L::kRedOff) + (grp * PASSES + q) * (4 * NG); };   // [4][NG]
     volatile int* flags = reinterpret_cast<volatile int*>(smem + L::kFlagOff);
     float l[PASSES][NC], m[PASSES][NC];
     Iter4<N> it;
     it.start(fp, tab, rng);
     int g = 0;
     bool ok = true;
-    // first column and P block of pass q
+    // first column of pass q, where this token's weights go in P^T, and a warp's
+    // staging of the epilogue: its quarter of the pass's block of P, which no MMA
+    // reads then (16 rows: both groups are in one block, so a region of its own)
     auto col0 = [&](int q) { return (grp * PASSES + q) * NG; };
-    auto block = [&](int q) { return smem + L::kPOff + (grp * PASSES + q) * kPBlock; };
-    // the tile's scores of pass q in the log2 domain, columns below nmin masked
-    auto scores = [&](int q, float sl, int nmin, float (&x)[NC]) {
+    auto put = [&](int q, const uint32_t (&w)[NC / 2]) {
+      uint8_t* block = smem + L::kPOff + (N == 16 ? 0 : (grp * PASSES + q) * kPBlock);
+      if constexpr (NC == 4)
+        *reinterpret_cast<uint2*>(block + p_offset(tok, grp) + (lane >> 4) * 8) = make_uint2(w[0], w[1]);
+      else
+        *reinterpret_cast<uint4*>(block + p_offset(tok, lane >> 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+    };
+    auto stage_of = [&](int q) {
+      return N == 16 ? smem + L::kStageOff + (warp - kSoftWarp) * 512
+                     : smem + L::kPOff + (grp * PASSES + q) * kPBlock + wq * (kPBlock / 4);
+    };
+    // the tile's scores of pass q in the log2 domain, relative to mq, columns
+    // below nmin masked (`all`: there are none)
+    auto scores = [&](int q, float sl, bool all, int nmin, const float (&mq)[NC], float (&x)[NC]) {
       uint32_t v[NC];
       tmem_half(tmem + lanes + L::kTmemS + (g & 1) * N + col0(q), v);
 #pragma unroll
-      for (int k = 0; k < NC; ++k) x[k] = col0(q) + cg + k >= nmin ? __uint_as_float(v[k]) * sl : -INFINITY;
+      for (int k = 0; k < NC; ++k) x[k] = fmaf(__uint_as_float(v[k]), sl, -mq[k]);
+      if (!all) {
+#pragma unroll
+        for (int k = 0; k < NC; ++k) x[k] = col0(q) + cg + k >= nmin ? x[k] : -INFINITY;
+      }
     };
     // New reference maxima of 16 rows from the tile's scores x, with O and l
     // brought to them (not for a piece's first tile).
     auto new_maxima = [&](int q, const float (&x)[NC], float (&lq)[NC], float (&mq)[NC], bool first) {
+      float* red = red_of(q);
       float y[NC];
 #pragma unroll
       for (int k = 0; k < NC; ++k) y[k] = x[k];
@@ -767,9 +792,10 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
         if (first) {
           mq[k] = t == -INFINITY ? 0.f : t;
           lq[k] = 0.f;
-        } else if (t > mq[k] + kThresh) {
-          a[k] = fast_exp2(mq[k] - t);
-          mq[k] = t;
+        } else if (t > kThresh) {   // (t is relative to mq)
+          const float mn = mq[k] + t;
+          a[k] = fast_exp2(mq[k] - mn);
+          mq[k] = mn;
           lq[k] *= a[k];
         }
       }
@@ -800,16 +826,14 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
         named_bar_sync(barid, 128);   // alpha has been read
       }
     };
-    // weights p of the scores against the maxima (masked: exp2(-inf) = 0), in 16 bits
-    auto weights = [&](const float (&x)[NC], const float (&mq)[NC], float (&p)[NC]) {
-      uint32_t pk[NC / 2];
+    // weights of the scores, in place (masked: exp2(-inf) = 0), and in 16 bits
+    auto weights = [&](float (&x)[NC], uint32_t (&pk)[NC / 2]) {
 #pragma unroll
       for (int k = 0; k < NC; k += 2) {
-        p[k] = fast_exp2(x[k] - mq[k]);
-        p[k + 1] = fast_exp2(x[k + 1] - mq[k + 1]);
-        pk[k / 2] = pack2<BF16>(p[k], p[k + 1]);
+        x[k] = fast_exp2(x[k]);
+        x[k + 1] = fast_exp2(x[k + 1]);
+        pk[k / 2] = pack2<BF16>(x[k], x[k + 1]);
       }
-      return make_uint4(pk[0], pk[1], pk[2], pk[3]);
     };
     while (it.valid) {
       const Unit4 ui = it.ui;
@@ -820,6 +844,7 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
       // the end; in the CURRENT part the rows of earlier query tokens
       int nmin = N;
       if (it.tok0() + tok < ui.hi) nmin = cur ? min(N, max(0, tok * fp.H - ui.g * N)) : 0;
+      const bool all = !cur && it.tok0() + kTile4 <= ui.hi;
       ok = __all_sync(0xffffffffu, ok && waits.lazy(&bar[L::B_S_FULL + sb], (g >> 1) & 1)) != 0;
       tc_fence_after();
       if (first) {
@@ -827,7 +852,9 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
 #pragma unroll
         for (int q = 0; q < PASSES; ++q) {
           float x[NC];
-          scores(q, sl, nmin, x);
+#pragma unroll
+          for (int k = 0; k < NC; ++k) m[q][k] = 0.f;
+          scores(q, sl, all, nmin, m[q], x);
           new_maxima(q, x, l[q], m[q], true);
         }
       }
@@ -836,27 +863,27 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
       // this tile, and the group makes them again before the PV product, which
       // looks at the flags, reads them.  (A barrier to agree first cost 500
       // cycles of every tile.)
-      uint4 pk[PASSES];
+      uint32_t pk[PASSES][NC / 2];
       uint32_t over = 0;   // passes of this warp with such a weight: not in l yet
 #pragma unroll
       for (int q = 0; q < PASSES; ++q) {
-        float x[NC], p[NC];
-        scores(q, sl, nmin, x);
-        float top = -INFINITY;
+        float x[NC];
+        scores(q, sl, all, nmin, m[q], x);
+        float top = fmaxf(x[0], x[1]);
 #pragma unroll
-        for (int k = 0; k < NC; ++k) top = fmaxf(top, x[k] - m[q][k]);
-        pk[q] = weights(x, m[q], p);
+        for (int k = 2; k < NC; ++k) top = fmaxf(top, x[k]);
+        weights(x, pk[q]);
         if (__any_sync(0xffffffffu, top > kThresh)) {
           over |= 1u << q;
         } else {
 #pragma unroll
-          for (int k = 0; k < NC; ++k) l[q][k] += p[k];
+          for (int k = 0; k < NC; ++k) l[q][k] += x[k];
         }
       }
       if (g >= 1) ok = __all_sync(0xffffffffu, ok && waits.lazy(&bar[L::B_P_EMPTY], (g - 1) & 1)) != 0;
       if (ok) {
 #pragma unroll
-        for (int q = 0; q < PASSES; ++q) *reinterpret_cast<uint4*>(block(q) + p_offset(tok, lane >> 4)) = pk[q];
+        for (int q = 0; q < PASSES; ++q) put(q, pk[q]);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -876,17 +903,16 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
             if (!named_bar_and(barid, 128, ok)) break;
 #pragma unroll
             for (int q = 0; q < PASSES; ++q) {
-              float x[NC], p[NC];
-              scores(q, sl, nmin, x);
-              if (!(over >> q & 1)) {
+              float x[NC];
+              scores(q, sl, all, nmin, m[q], x);
+              new_maxima(q, x, l[q], m[q], false);   // (scales what l has of this tile, too)
+              scores(q, sl, all, nmin, m[q], x);
+              weights(x, pk[q]);
+              put(q, pk[q]);
+              if (over >> q & 1) {
 #pragma unroll
-                for (int k = 0; k < NC; ++k) l[q][k] -= fast_exp2(x[k] - m[q][k]);
+                for (int k = 0; k < NC; ++k) l[q][k] += x[k];
               }
-              new_maxima(q, x, l[q], m[q], false);
-              const uint4 w = weights(x, m[q], p);
-#pragma unroll
-              for (int k = 0; k < NC; ++k) l[q][k] += p[k];
-              *reinterpret_cast<uint4*>(block(q) + p_offset(tok, lane >> 4)) = w;
             }
             fence_proxy_async_smem();
           }
@@ -909,65 +935,79 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
 #pragma unroll
         for (int q = 0; q < PASSES; ++q) {
           const float part = col_reduce<NC, false>(l[q], lane);
-          red[wq * NG + cr] = part;
-          named_bar_sync(barid, 128);
-          // row k of the 16 in lane k
-          float sum = 1.f;
-          if (lane < NG) sum = (red[lane] + red[NG + lane]) + (red[2 * NG + lane] + red[3 * NG + lane]);
-          named_bar_sync(barid, 128);
-          float* inv = red;                                        // [NG]
-          int64_t* dst = reinterpret_cast<int64_t*>(red + NG);     // [NG] byte offset of the row, -1: none
-          if (wq == 0 && lane < NG) {
-            const int n = col0(q) + lane, r = ui.g * N + n;
-            const float lse2 = reinterpret_cast<const float*>(smem + L::kMOff)[n] + log2f(sum);
-            int64_t row = -1;
-            if (r < fp.R) {
-              row = whole ? out_row4(fp, ui.b, r, ui.p) : static_cast<int64_t>(slot) * N + n;
-              if (whole) fp.lse_part[row] = lse2 * kLn2;
-              else fp.ws_lse[row] = lse2;
-            }
-            inv[lane] = (cur ? 1.f : fp.kv_scale) / sum;
-            dst[lane] = row < 0 ? -1 : row * 512 * esz;
+          red_of(q)[wq * NG + cr] = part;
+        }
+        named_bar_sync(barid, 128);
+        // row `lane` of the group's: its sum, then its factor and where it goes
+        constexpr int NR = NG * PASSES;
+        const float* rl = red_of(0) + (lane / NG) * (4 * NG) + lane % NG;
+        float sum = 1.f;
+        if (lane < NR) sum = (rl[0] + rl[NG]) + (rl[2 * NG] + rl[3 * NG]);
+        named_bar_sync(barid, 128);
+        float* inv = red_of(0);                                  // [NR]
+        int64_t* dst = reinterpret_cast<int64_t*>(inv + NR);     // [NR] byte offset of the row, -1: none
+        if (wq == 0 && lane < NR) {
+          const int n = col0(0) + lane, r = ui.g * N + n;
+          const float lse2 = reinterpret_cast<const float*>(smem + L::kMOff)[n] + log2f(sum);
+          int64_t row = -1;
+          if (r < fp.R) {
+            row = whole ? out_row4(fp, ui.b, r, ui.p) : static_cast<int64_t>(slot) * N + n;
+            if (whole) fp.lse_part[row] = lse2 * kLn2;
+            else fp.ws_lse[row] = lse2;
           }
-          named_bar_sync(barid, 128);
-          // NO rows of 32 latents at a time through the warp's staging (its
-          // quarter of the rows' block of P, which no MMA reads now): written a
-          // latent per lane, read back and stored 16 bytes per lane along the rows
-          uint8_t* stage = block(q) + wq * (kPBlock / 4);
+          inv[lane] = (cur ? 1.f : fp.kv_scale) / sum;
+          dst[lane] = row < 0 ? -1 : row * 512 * esz;
+        }
+        named_bar_sync(barid, 128);
+        // NO rows of 32 latents at a time through the warp's staging: written a
+        // latent per lane, read back and stored 16 bytes per lane along the rows
 #pragma unroll 1
-          for (int c = 0; c < 4 * NG; c += NO) {
-            uint32_t o[NO];
-            const int n0 = c % NG;
-            tmem_get(tmem + lanes + L::kTmemO + (c / NG) * N + col0(q) + n0, o);
-            const int lat0 = (c / NG) * 128 + wq * 32;
+        for (int c = 0; c < 4 * NG; c += NO) {
+          const int n0 = c % NG;
+          const int lat0 = (c / NG) * 128 + wq * 32;
+          uint32_t o[PASSES][NO];
 #pragma unroll
-            for (int k = 0; k < NO; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * inv[n0 + k]);
-            if (esz == 2) {
+          for (int q = 0; q < PASSES; ++q) {
+            tmem_get(tmem + lanes + L::kTmemO + (c / NG) * N + col0(q) + n0, o[q]);
+#pragma unroll
+            for (int k = 0; k < NO; ++k)
+              o[q][k] = __float_as_uint(__uint_as_float(o[q][k]) * inv[q * NG + n0 + k]);
+          }
+          if (esz == 2) {
+#pragma unroll
+            for (int q = 0; q < PASSES; ++q) {
+              uint16_t* stage = reinterpret_cast<uint16_t*>(stage_of(q));
 #pragma unroll
               for (int k = 0; k < NO; ++k)
-                reinterpret_cast<uint16_t*>(stage)[k * 32 + lane] =
-                    static_cast<uint16_t>(pack2_dt(__uint_as_float(o[k]), 0.f, fp.part_dtype));
-              __syncwarp();
-              const uint4 x = *reinterpret_cast<const uint4*>(stage + lane * 16);
-              const int64_t d = dst[n0 + (lane >> 2)];
+                stage[k * 32 + lane] = static_cast<uint16_t>(pack2_dt(__uint_as_float(o[q][k]), 0.f, fp.part_dtype));
+            }
+            __syncwarp();
+#pragma unroll
+            for (int q = 0; q < PASSES; ++q) {
+              const uint4 x = *reinterpret_cast<const uint4*>(stage_of(q) + lane * 16);
+              const int64_t d = dst[q * NG + n0 + (lane >> 2)];
               if (d >= 0) *reinterpret_cast<uint4*>(out + d + lat0 * 2 + (lane & 3) * 16) = x;
-              __syncwarp();
-            } else {
+            }
+            __syncwarp();
+          } else {
+#pragma unroll
+            for (int q = 0; q < PASSES; ++q) {
+              uint8_t* stage = stage_of(q);
 #pragma unroll
               for (int h = 0; h < NO; h += NO / 2) {
 #pragma unroll
-                for (int k = 0; k < NO / 2; ++k) reinterpret_cast<uint32_t*>(stage)[k * 32 + lane] = o[h + k];
+                for (int k = 0; k < NO / 2; ++k) reinterpret_cast<uint32_t*>(stage)[k * 32 + lane] = o[q][h + k];
                 __syncwarp();
                 const uint4 x = *reinterpret_cast<const uint4*>(stage + lane * 16);
-                const int64_t d = dst[n0 + h + (lane >> 3)];
+                const int64_t d = dst[q * NG + n0 + h + (lane >> 3)];
                 if (d >= 0) *reinterpret_cast<uint4*>(out + d + lat0 * 4 + (lane & 7) * 16) = x;
                 __syncwarp();
               }
             }
           }
-          tc_fence_before();
-          named_bar_sync(barid, 128);   // red has been read
         }
+        tc_fence_before();
+        named_bar_sync(barid, 128);   // red has been read
       }
       it.advance(fp);
       ++g;
