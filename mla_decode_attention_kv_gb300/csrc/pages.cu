@@ -60,6 +60,7 @@ int launch_copy_pages(CopyParams cp, cudaStream_t stream) {
 // first thread, so a row named twice is given back once.
 __global__ void __launch_bounds__(256) mla_kv_free_kernel(const FreeParams fp) {
   __shared__ int s_pages;
+  griddep_launch_dependents();   // (a fork behind it starts meanwhile, and waits)
   const int r = __ldg(fp.rows + blockIdx.x);
   if (r < 0 || r >= fp.num_rows) {
     if (threadIdx.x == 0) set_error(fp.err, kDevBadRow);
@@ -131,8 +132,10 @@ __global__ void __launch_bounds__(kPlanThreads) mla_kv_fork_plan_kernel(const Fo
   __shared__ int s_bad;
   int32_t* fresh = fp.ws + 4;
   int32_t* list = fresh + fp.n;
+  griddep_launch_dependents();
   for (int i = threadIdx.x; i < (fp.rows + 31) / 32; i += kPlanThreads) s_child[i] = s_parent[i] = 0;
   if (threadIdx.x == 0) s_bad = 0;
+  griddep_wait();   // the grid before, a mla_kv_free for one, is done
   __syncthreads();
   const int per = (fp.n + kPlanThreads - 1) / kPlanThreads;
   const int a = min(fp.n, static_cast<int>(threadIdx.x) * per), e = min(fp.n, a + per);
@@ -212,6 +215,7 @@ __global__ void __launch_bounds__(kPlanThreads) mla_kv_fork_plan_kernel(const Fo
 }
 
 __global__ void __launch_bounds__(kCopyThreads) mla_kv_fork_apply_kernel(const ForkParams fp) {
+  griddep_wait();   // the plan is complete
   if (fp.ws[0] == 0) return;
   const int per = fp.layers * fp.chunks + 1;
   const int k = blockIdx.x / per, j = blockIdx.x - k * per;
@@ -250,11 +254,21 @@ __global__ void __launch_bounds__(kCopyThreads) mla_kv_fork_apply_kernel(const F
 
 int launch_fork(ForkParams fp, cudaStream_t stream) {
   fp.chunks = static_cast<int>((fp.page_bytes + kCopyChunk - 1) / kCopyChunk);
-  mla_kv_fork_plan_kernel<<<1, kPlanThreads, 0, stream>>>(fp);
-  if (cudaPeekAtLastError() != cudaSuccess) return -1;
   const unsigned blocks = static_cast<unsigned>(fp.n) * (fp.layers * fp.chunks + 1);
-  mla_kv_fork_apply_kernel<<<blocks, kCopyThreads, 0, stream>>>(fp);
-  return 0;
+  // programmatic launches: a grid's start overlaps the one before, for which it waits
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  cfg.stream = stream;
+  cfg.gridDim = dim3(1);
+  cfg.blockDim = dim3(kPlanThreads);
+  if (cudaLaunchKernelEx(&cfg, mla_kv_fork_plan_kernel, fp) != cudaSuccess) return -1;
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(kCopyThreads);
+  return cudaLaunchKernelEx(&cfg, mla_kv_fork_apply_kernel, fp) != cudaSuccess ? -1 : 0;
 }
 
 }  // namespace mla

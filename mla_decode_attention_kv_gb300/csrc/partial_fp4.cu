@@ -222,7 +222,7 @@ constexpr int kCostUnit = N == 64 ? 4 : 3;
 
 struct PartScratch {
   unsigned long long scan[32];
-  int2 pre[1024];                  // tiles and cost before each thread's units
+  int4 pre[1024];                  // of each thread's units: tiles and cost before, tiles of the first
   int bound[kFp4MaxCtas + 1];      // first tile of each CTA's share
   int whole[kFp4MaxCtas + 1];      // cost before the first unit that starts at or behind it
   int4 rng;
@@ -237,10 +237,11 @@ __device__ __forceinline__ Range4 partition4(const Fp4Params& fp, PartScratch* p
   const int per = (U + NT - 1) / NT;
   auto cost_of = [](int nt) { return nt > 0 ? kCostTile * nt + kCostUnit<N> : 0; };
   {
-    int cnt = 0, cost = 0;
+    int cnt = 0, cost = 0, first = 0;
     const int a = min(U, tid * per), e = min(U, a + per);
     for (int u = a; u < e; ++u) {
       const int nt = tiles4(unit4<N>(fp, u));
+      if (u == a) first = nt;
       cnt += nt;
       cost += cost_of(nt);
     }
@@ -257,7 +258,7 @@ __device__ __forceinline__ Range4 partition4(const Fp4Params& fp, PartScratch* p
     unsigned long long base = 0;
     for (int w = 0; w < warp; ++w) base += ps->scan[w];
     const unsigned long long before = base + incl - mine;
-    ps->pre[tid] = make_int2(static_cast<int>(before & 0xffffffffu), static_cast<int>(before >> 32));
+    ps->pre[tid] = make_int4(static_cast<int>(before & 0xffffffffu), static_cast<int>(before >> 32), first, 0);
   }
   unsigned long long all = 0;
 #pragma unroll
@@ -278,19 +279,20 @@ __device__ __forceinline__ Range4 partition4(const Fp4Params& fp, PartScratch* p
     int u, nt, t0, c0;   // unit, its tiles, tiles and cost before it
   };
   auto find = [&](int x, bool by_cost) {
-    int lo = 0, hi = NT - 1;   // the last thread with pre <= x
+    int lo = 0, hi = min(U, NT) - 1;   // the last thread with pre <= x
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
       if ((by_cost ? ps->pre[mid].y : ps->pre[mid].x) <= x) lo = mid;
       else hi = mid - 1;
     }
-    Found f{lo * per, 0, ps->pre[lo].x, ps->pre[lo].y};
-    for (;; ++f.u) {
-      f.nt = tiles4(unit4<N>(fp, f.u));
+    const int4 p = ps->pre[lo];
+    Found f{lo * per, p.z, p.x, p.y};
+    for (;;) {
       const int c = cost_of(f.nt);
       if (by_cost ? x < f.c0 + c : x < f.t0 + f.nt) return f;
       f.t0 += f.nt;
       f.c0 += c;
+      f.nt = tiles4(unit4<N>(fp, ++f.u));
     }
   };
   // boundary c: the tiles that start below the cost c * all_cost / ncta
@@ -529,7 +531,10 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
     prefetch_tmap(&tm_qlat);
     prefetch_tmap(&tm_qpe);
   }
-  griddep_launch_dependents();   // the merge grid may be scheduled as CTAs retire; it waits for this one
+  // (programmatic launches: this grid's start overlaps the one before, the
+  // merge grid's start this one; each waits for the other to be done)
+  griddep_launch_dependents();
+  griddep_wait();
   const Range4 rng = partition4<N, L::kThreads>(fp, reinterpret_cast<PartScratch*>(smem), cid, ncta);
   {
     const int n = rng.u_begin <= rng.u_last ? min(rng.u_last - rng.u_begin + 1, kUnits4) : 0;
@@ -1237,18 +1242,21 @@ static int launch4(const CUtensorMap& qlat, const CUtensorMap& qpe, const Fp4Par
   const int most = fp4_max_ctas();
   if (most < 1 || cudaGetDevice(&dev) != cudaSuccess || !prepare4<BF16, N>(dev)) return -1;
   const int ctas = fp.split ? fp.split : std::max(1, std::min(fp.num_units, most));
-  mla_partial_fp4_kernel<BF16, N><<<ctas, Smem4<N>::kThreads, Smem4<N>::kTotal, stream>>>(qlat, qpe, fp);
-  if (!fp.split) return 0;
-  if (cudaPeekAtLastError() != cudaSuccess) return -1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas, (N + 31) / 32, 1);
-  cfg.blockDim = dim3(256, 1, 1);
-  cfg.stream = stream;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
+  cfg.stream = stream;
+  cfg.gridDim = dim3(ctas, 1, 1);
+  cfg.blockDim = dim3(Smem4<N>::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = Smem4<N>::kTotal;
+  if (cudaLaunchKernelEx(&cfg, mla_partial_fp4_kernel<BF16, N>, qlat, qpe, fp) != cudaSuccess) return -1;
+  if (!fp.split) return 0;
+  cfg.gridDim = dim3(ctas, (N + 31) / 32, 1);
+  cfg.blockDim = dim3(256, 1, 1);
+  cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, mla_partial_fp4_merge_kernel, fp, N) != cudaSuccess ? -1 : 0;
 }
 
