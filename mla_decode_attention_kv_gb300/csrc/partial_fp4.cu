@@ -400,6 +400,33 @@ __device__ __forceinline__ void tmem_put(uint32_t a, const uint32_t (&r)[8]) {
                : "memory");
 }
 
+// 8 X columns of 16 lanes (issued; tmem_wait_frag waits): thread t has, of each
+// 8 columns, columns 2 (t % 4) and + 1 of lanes t / 4 (r[0], r[1]) and t / 4 + 8.
+__device__ __forceinline__ void tmem_ld_frag(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a));
+}
+__device__ __forceinline__ void tmem_ld_frag(uint32_t a, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(a));
+}
+template <int K>
+__device__ __forceinline__ void tmem_wait_frag(uint32_t (&r)[K], uint32_t (&q)[K]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int k = 0; k < K; ++k) asm volatile("" : "+r"(r[k]), "+r"(q[k])::"memory");   // (no use before the wait)
+}
+
+// Four 8 x 8 matrices of 16-bit values stored transposed: lane 8 i + k gives the
+// address of row k of matrix i.
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z),
+               "r"(w)
+               : "memory");
+}
+
 // P^T, the MN-major B operand: each 16 columns are a block of their own, [64
 // tokens][16] 16-bit values with the 32-byte swizzle, LBO from block to block.
 constexpr int kPRow = 16 * 2;
@@ -968,44 +995,70 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
           dst[lane] = row < 0 ? -1 : row * 512 * esz;
         }
         named_bar_sync(barid, 128);
-        // NO rows of 32 latents at a time through the warp's staging: written a
-        // latent per lane, read back and stored 16 bytes per lane along the rows
-#pragma unroll 1
-        for (int c = 0; c < 4 * NG; c += NO) {
-          const int n0 = c % NG;
-          const int lat0 = (c / NG) * 128 + wq * 32;
-          uint32_t o[PASSES][NO];
+        if (esz == 2) {
+          // 32 latents of 8 rows at a time: read as matrix fragments, scaled,
+          // stored transposed into the warp's staging (16-byte unit j of row k at
+          // unit j ^ (k / 2 & 3): no bank conflicts) and from there to the rows,
+          // 16 bytes a lane
+          constexpr int NF = NG / 2;             // registers of a fragment: 4 for 8 rows
+          float f[PASSES][NG / 4];
+          char* to[PASSES][NG / 8];
+          const int row = lane >> 2, unit = (lane & 3) ^ ((lane >> 3) & 3);
+          const int mrow = lane & 7, munit = (lane >> 3) ^ ((mrow >> 1) & 3);
 #pragma unroll
           for (int q = 0; q < PASSES; ++q) {
-            tmem_get(tmem + lanes + L::kTmemO + (c / NG) * N + col0(q) + n0, o[q]);
 #pragma unroll
-            for (int k = 0; k < NO; ++k)
-              o[q][k] = __float_as_uint(__uint_as_float(o[q][k]) * inv[q * NG + n0 + k]);
+            for (int k = 0; k < NG / 8; ++k) {
+              f[q][2 * k] = inv[q * NG + 8 * k + 2 * (lane & 3)];
+              f[q][2 * k + 1] = inv[q * NG + 8 * k + 2 * (lane & 3) + 1];
+              const int64_t d = dst[q * NG + 8 * k + row];
+              to[q][k] = d < 0 ? nullptr : out + d + wq * 64 + (lane & 3) * 16;
+            }
           }
-          if (esz == 2) {
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
 #pragma unroll
             for (int q = 0; q < PASSES; ++q) {
-              uint16_t* stage = reinterpret_cast<uint16_t*>(stage_of(q));
+              uint32_t lo[NF], hi[NF];           // latents 0-15 and 16-31 of the warp's 32
+              const uint32_t oa = tmem + lanes + L::kTmemO + c * N + col0(q);
+              tmem_ld_frag(oa, lo);
+              tmem_ld_frag(oa + (16u << 16), hi);
+              tmem_wait_frag(lo, hi);
+              const uint32_t stage = smem_u32(stage_of(q));
 #pragma unroll
-              for (int k = 0; k < NO; ++k)
-                stage[k * 32 + lane] = static_cast<uint16_t>(pack2_dt(__uint_as_float(o[q][k]), 0.f, fp.part_dtype));
+              for (int k = 0; k < NG / 8; ++k) {
+                uint32_t w[4];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                  w[j] = pack2_dt(__uint_as_float(lo[4 * k + 2 * j]) * f[q][2 * k],
+                                  __uint_as_float(lo[4 * k + 2 * j + 1]) * f[q][2 * k + 1], fp.part_dtype);
+                  w[2 + j] = pack2_dt(__uint_as_float(hi[4 * k + 2 * j]) * f[q][2 * k],
+                                      __uint_as_float(hi[4 * k + 2 * j + 1]) * f[q][2 * k + 1], fp.part_dtype);
+                }
+                __syncwarp();   // the staging has been read
+                stmatrix_x4_trans(stage + mrow * 64 + munit * 16, w[0], w[1], w[2], w[3]);
+                __syncwarp();
+                const uint4 x = ld_shared_v4(stage + row * 64 + unit * 16);
+                if (to[q][k]) *reinterpret_cast<uint4*>(to[q][k] + c * 256) = x;
+              }
             }
-            __syncwarp();
-#pragma unroll
+          }
+        } else {
+          // fp32 rows: 8 rows of 32 latents at a time, written a latent per lane
+#pragma unroll 1
+          for (int c = 0; c < 4 * NG; c += NO) {
+            const int n0 = c % NG;
+            const int lat0 = (c / NG) * 128 + wq * 32;
+#pragma unroll 1
             for (int q = 0; q < PASSES; ++q) {
-              const uint4 x = *reinterpret_cast<const uint4*>(stage_of(q) + lane * 16);
-              const int64_t d = dst[q * NG + n0 + (lane >> 2)];
-              if (d >= 0) *reinterpret_cast<uint4*>(out + d + lat0 * 2 + (lane & 3) * 16) = x;
-            }
-            __syncwarp();
-          } else {
-#pragma unroll
-            for (int q = 0; q < PASSES; ++q) {
+              uint32_t o[NO];
+              tmem_get(tmem + lanes + L::kTmemO + (c / NG) * N + col0(q) + n0, o);
               uint8_t* stage = stage_of(q);
 #pragma unroll
               for (int h = 0; h < NO; h += NO / 2) {
 #pragma unroll
-                for (int k = 0; k < NO / 2; ++k) reinterpret_cast<uint32_t*>(stage)[k * 32 + lane] = o[q][h + k];
+                for (int k = 0; k < NO / 2; ++k)
+                  reinterpret_cast<float*>(stage)[k * 32 + lane] = __uint_as_float(o[h + k]) * inv[q * NG + n0 + h + k];
                 __syncwarp();
                 const uint4 x = *reinterpret_cast<const uint4*>(stage + lane * 16);
                 const int64_t d = dst[q * NG + n0 + h + (lane >> 3)];
@@ -1133,78 +1186,95 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
 }
 
 // ---------------------------------------------------------------- merge of cut units
-// One block per (CTA, 32 rows): merges the pieces of the cut unit whose last
-// tile that CTA held by their LSEs, eight threads a row (64 columns each).
-__global__ void __launch_bounds__(256, 2) mla_partial_fp4_merge_kernel(const Fp4Params fp, int rows) {
+// A warp per row of the cut unit whose last tile the CTA blockIdx.x held: merges
+// the unit's pieces by their LSEs.  A lane looks up a piece (up to 32 at a
+// time), so their places and weights are there after three dependent reads;
+// then the pieces' rows are summed in their order, 16 columns a lane.
+__global__ void __launch_bounds__(256) mla_partial_fp4_merge_kernel(const Fp4Params fp, int rows) {
   griddep_wait();
   const int4 rec = fp.ws_units[blockIdx.x];
-  const int u = rec.x;
-  const int n = blockIdx.y * 32 + (threadIdx.x >> 3);
-  if (u < 0 || n >= rows) return;
+  const int u = rec.x, lane = threadIdx.x & 31;
+  const int n = blockIdx.y * 8 + (threadIdx.x >> 5);
+  if (u < 0) return;
   const int p = u % fp.P, gb = u / fp.P, b = gb % fp.B, r = (gb / fp.B) * rows + n;
   if (r >= fp.R) return;
-  const int sub = threadIdx.x & 7;
   const bool f32 = fp.part_dtype == kFP32;
-  float acc[64];
+  float acc[16];
 #pragma unroll
-  for (int t = 0; t < 64; ++t) acc[t] = 0.f;
+  for (int t = 0; t < 16; ++t) acc[t] = 0.f;
   float m = -INFINITY, wsum = 0.f;
-  for (int c = rec.z; c <= rec.w; ++c) {
-    const int s0 = fp.ws_bounds[c], s1 = fp.ws_bounds[c + 1];
-    if (s1 <= s0) continue;                             // CTA without tiles
-    const int64_t row = static_cast<int64_t>(2 * c + (s0 >= rec.y ? 0 : 1)) * rows + n;   // its first or last piece
-    const float l = fp.ws_lse[row];
-    if (l > m) {
-      const float sc = exp2f(m - l);
-#pragma unroll
-      for (int t = 0; t < 64; ++t) acc[t] *= sc;
-      wsum *= sc;
-      m = l;
+  for (int c0 = rec.z; c0 <= rec.w; c0 += 32) {
+    const int c = c0 + lane;
+    int64_t row = 0;
+    float l = -INFINITY;
+    if (c <= rec.w) {
+      const int s0 = fp.ws_bounds[c], s1 = fp.ws_bounds[c + 1];
+      if (s1 > s0) {   // (else a CTA without tiles)
+        row = static_cast<int64_t>(2 * c + (s0 >= rec.y ? 0 : 1)) * rows + n;   // its first or last piece
+        l = fp.ws_lse[row];
+      }
     }
-    const float w = l == m ? 1.f : exp2f(l - m);
-    wsum += w;
+    float mx = l;
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int64_t e0 = row * 512 + sub * 64 + 32 * half;
-      float x[32];
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    if (mx > m) {   // a new reference maximum (at first the scale is 0)
+      const float sc = exp2f(m - mx);
+#pragma unroll
+      for (int t = 0; t < 16; ++t) acc[t] *= sc;
+      wsum *= sc;
+      m = mx;
+    }
+    // (a NaN is no maximum; it goes through its weight)
+    const float w = row == 0 && l == -INFINITY ? 0.f : l == m ? 1.f : exp2f(l - m);
+    const int np = min(32, rec.w - c0 + 1);
+#pragma unroll 4
+    for (int k = 0; k < np; ++k) {
+      const float wk = __shfl_sync(0xffffffffu, w, k);
+      const int64_t e0 = __shfl_sync(0xffffffffu, row, k) * 512 + lane * 16;
+      if (wk == 0.f) continue;
+      wsum += wk;
       if (f32) {
         const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(fp.ws_o) + e0);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float4 f = src[k];
-          x[4 * k] = f.x;
-          x[4 * k + 1] = f.y;
-          x[4 * k + 2] = f.z;
-          x[4 * k + 3] = f.w;
+        for (int j = 0; j < 4; ++j) {
+          const float4 f = src[j];
+          acc[4 * j] = fmaf(wk, f.x, acc[4 * j]);
+          acc[4 * j + 1] = fmaf(wk, f.y, acc[4 * j + 1]);
+          acc[4 * j + 2] = fmaf(wk, f.z, acc[4 * j + 2]);
+          acc[4 * j + 3] = fmaf(wk, f.w, acc[4 * j + 3]);
         }
       } else {
         const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(fp.ws_o) + e0);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint4 h = src[k];
+        for (int j = 0; j < 2; ++j) {
+          const uint4 h = src[j];
           const uint32_t hw[4] = {h.x, h.y, h.z, h.w};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 f2 = unpack2(hw[j], fp.part_dtype);
-            x[8 * k + 2 * j] = f2.x;
-            x[8 * k + 2 * j + 1] = f2.y;
+          for (int i = 0; i < 4; ++i) {
+            const float2 f2 = unpack2(hw[i], fp.part_dtype);
+            acc[8 * j + 2 * i] = fmaf(wk, f2.x, acc[8 * j + 2 * i]);
+            acc[8 * j + 2 * i + 1] = fmaf(wk, f2.y, acc[8 * j + 2 * i + 1]);
           }
         }
       }
-#pragma unroll
-      for (int t = 0; t < 32; ++t) acc[32 * half + t] = fmaf(w, x[t], acc[32 * half + t]);
     }
   }
   const float inv = 1.f / wsum;
   const int64_t row = out_row4(fp, b, r, p);
+  if (f32) {
+    float4* d = reinterpret_cast<float4*>(static_cast<float*>(fp.o_part) + row * 512 + lane * 16);
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint32_t v[32];
+    for (int j = 0; j < 4; ++j)
+      d[j] = make_float4(acc[4 * j] * inv, acc[4 * j + 1] * inv, acc[4 * j + 2] * inv, acc[4 * j + 3] * inv);
+  } else {
+    uint32_t w[8];
 #pragma unroll
-    for (int t = 0; t < 32; ++t) v[t] = __float_as_uint(acc[32 * h + t]);
-    store_row32(fp.o_part, row * 512 + sub * 64 + 32 * h, v, inv, fp.part_dtype);
+    for (int j = 0; j < 8; ++j) w[j] = pack2_dt(acc[2 * j] * inv, acc[2 * j + 1] * inv, fp.part_dtype);
+    uint4* d = reinterpret_cast<uint4*>(static_cast<uint16_t*>(fp.o_part) + row * 512 + lane * 16);
+    d[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    d[1] = make_uint4(w[4], w[5], w[6], w[7]);
   }
-  if (sub == 0) fp.lse_part[row] = (m + log2f(wsum)) * kLn2;
+  if (lane == 0) fp.lse_part[row] = (m + log2f(wsum)) * kLn2;
 }
 
 // ---------------------------------------------------------------- launcher
@@ -1254,7 +1324,7 @@ static int launch4(const CUtensorMap& qlat, const CUtensorMap& qpe, const Fp4Par
   cfg.dynamicSmemBytes = Smem4<N>::kTotal;
   if (cudaLaunchKernelEx(&cfg, mla_partial_fp4_kernel<BF16, N>, qlat, qpe, fp) != cudaSuccess) return -1;
   if (!fp.split) return 0;
-  cfg.gridDim = dim3(ctas, (N + 31) / 32, 1);
+  cfg.gridDim = dim3(ctas, N / 8, 1);
   cfg.blockDim = dim3(256, 1, 1);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, mla_partial_fp4_merge_kernel, fp, N) != cudaSuccess ? -1 : 0;
