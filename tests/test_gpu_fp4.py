@@ -194,6 +194,41 @@ def test_fp4_device_errors():
     c.check(*c.run())
 
 
+def test_fp4_pages_past_4_gb():
+    """Page offsets past 2^32 bytes: a sequence on the last pages of a large pool."""
+    c = Fp4([700], 16, bs=256, seed=16)
+    blocks = (1 << 32) // (256 * 324) + 60
+    pool = torch.zeros(blocks, 256, 324, dtype=torch.uint8, device=DEV)
+    n = c.pages.shape[0]
+    pool[blocks - n:] = c.pages
+    c.pages = pool
+    c.gtable += torch.where(c.gtable >= 0, blocks - n, 0).to(torch.int32)
+    c.check(*c.run())
+
+
+def test_fp4_shared_and_repeated_pages():
+    """Sequences that share pages (a fork), and a page that stands twice in a row."""
+    c = Fp4([128, 128], 24, bs=32, seed=17)
+    c.table[1] = c.table[0][[0, 1, 1, 3]]
+    c.gtable = torch.from_numpy(c.table).to(DEV)
+    h = c.hist[0]
+    c.hist[1] = np.concatenate([h[:64], h[32:64], h[96:]])
+    c.check(*c.run())
+
+
+def test_fp4_two_streams_at_once():
+    """Calls on two streams with their default workspaces (one each)."""
+    cs = [Fp4([5000, 300], 16, shards=1, seed=18), Fp4([4000], 128, shards=2, seed=19)]
+    torch.cuda.synchronize()
+    streams, outs = [torch.cuda.Stream(), torch.cuda.Stream()], [None, None]
+    for _ in range(4):
+        for k in range(2):
+            outs[k] = cs[k].run(stream=streams[k])
+    torch.cuda.synchronize()
+    for c, o in zip(cs, outs):
+        c.check(*o)
+
+
 def test_fp4_graph_stream_and_two_workspaces():
     """Two captured calls that replay at once on two streams, each with a workspace
     of its own."""

@@ -207,6 +207,22 @@ def test_fork_in_a_graph():
     assert p.err.item() == 0
 
 
+def test_fork_into_strided_layers_and_back_to_back():
+    """Layers that are views of a larger tensor, and three forks in a row on one stream
+    (each starts while the one before ends)."""
+    p = Pool([40, 33, 100], 6, layers=3)
+    base = torch.zeros(6, *p.cache.shape[1:], dtype=torch.uint8, device=DEV)
+    base[::2] = p.cache
+    p.cache = base[::2]
+    for a, b in (([0, 1], [3, 4]), ([3, 2], [5, 6]), ([6, 4], [7, 8])):
+        api.mla_kv_fork(p.cache, p.table, p.lens, p.refs, p.ids(a), p.ids(b), err_flag=p.err)
+        p.host_fork(a, b)
+    torch.cuda.synchronize()
+    assert p.err.item() == 0 and not base[1::2].any()
+    p.cache = p.cache.contiguous()
+    p.same()
+
+
 def test_page_refusals():
     p = Pool([40], 2)
     with pytest.raises(MlaError):
