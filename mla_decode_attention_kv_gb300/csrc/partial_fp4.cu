@@ -506,6 +506,32 @@ __device__ __forceinline__ void multipliers(uint32_t s2, bool valid, uint32_t& m
   m1 = __byte_perm(x, 0, 0x3232);
 }
 
+// Not 0 where one of eight 16-bit values is a NaN or an infinity (exponent bits
+// all ones: adding the lowest of them carries into the sign's place).
+template <bool BF16>
+__device__ __forceinline__ uint32_t not_finite(const uint4& v) {
+  constexpr uint32_t kExp = BF16 ? 0x7F807F80u : 0x7C007C00u, kOne = BF16 ? 0x00800080u : 0x04000400u;
+  return (((v.x & kExp) + kOne) | ((v.y & kExp) + kOne) | ((v.z & kExp) + kOne) | ((v.w & kExp) + kOne)) & 0x80008000u;
+}
+
+// Whether latents of a CURRENT token are not finite: this thread's 64 of half h
+// and, with h = 0, the same of the other half; `row` is at the thread's place in
+// the first half.  h < 0: no token.  (Out of line: inlined, its registers cost
+// the history's tiles 4 to 7 % more time.)
+template <bool BF16>
+__device__ __noinline__ bool current_bad(const uint4* row, int h) {
+  uint32_t bad = 0;
+  if (h >= 0) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) bad |= not_finite<BF16>(row[32 + j]);
+    if (h == 0) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) bad |= not_finite<BF16>(row[j]);
+    }
+  }
+  return bad != 0;
+}
+
 }  // namespace
 
 // ---------------------------------------------------------------- the kernel
@@ -1142,12 +1168,14 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
         const uint4* row = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(fp.kv_cur) +
                                                           (static_cast<int64_t>(it.ui.b) * fp.q_len + t) * 576);
         const uint4 none = make_uint4(0, 0, 0, 0);
+        const bool clean = !current_bad<BF16>(row + grp * 8, valid ? h : -1);
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) x[k][j] = valid ? row[h * 32 + (grp * 2 + k) * 4 + j] : none;
+          for (int j = 0; j < 4; ++j) x[k][j] = valid && clean ? row[h * 32 + (grp * 2 + k) * 4 + j] : none;
 #pragma unroll
         for (int j = 0; j < 2; ++j) xr[j] = valid && h == 0 ? row[64 + grp * 2 + j] : none;
+        if (!clean) xr[0].x = 0x7FFF7FFFu;
       }
       const int hc = 2 * g + h, sl = hc % L::kNH;
       if (hc >= L::kNH && !__all_sync(0xffffffffu, waits.wait(&bar[L::B_EMPTY + sl], ((hc / L::kNH) - 1) & 1))) break;
