@@ -244,7 +244,9 @@ int mla_dcp_decode_partial_fp8(const void* q_abs, const void* q_pe, const void* 
  * Differences from mla_dcp_decode_partial_sliced:
  *   kv_cache   [num_blocks] E2M1 pages (MLA_KV_E2M1 above); the slots of a
  *              last block past L_b may hold any bytes
- *   kv_cur     [B, q_len, 576] values of in_dtype (not codes), or NULL
+ *   kv_cur     [B, q_len, 576] values of in_dtype (not codes), or NULL; a token
+ *              with a NaN or an infinity reaches the rows that see it alone (a
+ *              latent that is not finite makes them NaN)
  *   kv_scale   > 0 and finite (scale * kv_scale too); MLA_ERR_BAD_SHAPE otherwise
  *   workspace  of mla_dcp_decode_partial_fp4_workspace_size bytes, or NULL
  * Precision: every code * s is a value of either 16-bit type, so the tensor
@@ -430,7 +432,8 @@ int mla_gather_kv(const void* kv_cache, const int32_t* block_table, const int32_
  *         code = rn_E2M1(value / (s kv_scale)), 0 where s is 0; a zero keeps
  *         its sign; a block that holds a NaN gets s = NaN
  * (exactly so where kv_scale is a power of two; q_out is computed in fp32).
- * Row sums and values are fp32: inputs beyond 1e18 overflow the mean.
+ * mean(c^2) + eps counts as at least 2^-120 (a row of zeros stays zeros); beyond
+ * 1e16 inputs leave the range of its fp32 sum.
  *
  *   c_kv      [T, 512] dtype, rows c_stride elements apart
  *   k_pe      [T, 64] dtype, rows k_stride elements apart
@@ -508,7 +511,9 @@ int mla_kv_free(int32_t* block_table, int32_t* seq_lens, int32_t* ref_counts, co
  * A child's row holds nothing before (seq_lens[c] = 0; mla_kv_free), is forked
  * into once and is no parent of the call, or MLA_DEV_BAD_ROW; too few free
  * pages: MLA_DEV_NO_FREE_PAGE.  In both cases, and for a parent's length out of
- * range (MLA_DEV_BAD_SEQ_LEN), nothing at all is changed.
+ * range (MLA_DEV_BAD_SEQ_LEN), nothing at all is changed.  An entry of a parent's
+ * row outside [0, num_blocks) sets MLA_DEV_BAD_BLOCK_ID: it becomes -1 in the
+ * child's row, or, the last page, is not copied.
  *   kv_cache   pools of every layer, as in mla_kv_copy_pages
  *   parents, children [n] int32 (device), 1 <= n <= num_rows <= 65536
  *   workspace  of mla_kv_fork_workspace_size(n) bytes; calls that may overlap

@@ -144,6 +144,10 @@ __device__ __forceinline__ uint32_t to_e2m1x2(float x, float y) {   // x in the 
 // A little less and a little more than a value: the bounds of its fp32 error.
 constexpr float kLess = 1.f - 0x1p-18f, kMore = 1.f + 0x1p-18f;
 
+// The mean square plus eps counts as at least this, so that a row of zeros with
+// eps 0 stays zeros, and the estimate's square stays in range (a NaN passes).
+constexpr float kLeastMean = 0x1p-120f;
+
 // E4M3 byte of a block's scale, max / (6 kv_scale); NaN where a value is NaN.
 // EXACT: amax is rounded to odd.  Otherwise `same` turns false where amax's
 // error could change the byte.
@@ -251,6 +255,7 @@ __device__ __forceinline__ bool append_row(const AppendParams& ap, int t, int la
       }
       F2 m = two_sum(s * (1.f / 512), ap.eps);
       m = renorm(m.hi, m.lo + e * (1.f / 512));
+      if (m.hi < kLeastMean) m = {kLeastMean, 0.f};
       // 1 / sqrt(m): the fp32 estimate and one Newton step on its exact residual
       const float r0 = rsqrtf(m.hi);
       const float r2 = r0 * r0, r2e = fmaf(r0, r0, -r2);
@@ -278,7 +283,8 @@ __device__ __forceinline__ bool append_row(const AppendParams& ap, int t, int la
       s += e;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      const float rs = rsqrtf(fmaf(s, 1.f / 512, ap.eps));
+      const float mean = fmaf(s, 1.f / 512, ap.eps);
+      const float rs = rsqrtf(mean < kLeastMean ? kLeastMean : mean);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const float2 f = unpack<BF16>(cw[k]), w = unpack<BF16>(ww[k]);

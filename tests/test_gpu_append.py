@@ -166,6 +166,34 @@ def test_append_zero_rows_ties_and_saturation():
     assert (kv_out[3, :512] == 6 * 448).all() and (kv_out[4] == 0).all()
 
 
+@pytest.mark.parametrize("kind", ["model", "e4m3", "e2m1"])
+def test_append_zero_rows_without_eps(kind):
+    """0 / sqrt(0 + 0) counts as 0 (padding rows), and other rows are normalised as ever."""
+    c = Case(5, 2, kind, pad=False)
+    c.kv_a[1] = 0
+    c.kv_a[3] = -0.0
+    _, kv_out = c.run(eps=0.0)
+    v = kv_out.view(torch.uint8) & 0x7F if kind == "e4m3" else kv_out
+    assert (v[[1, 3]] == 0).all()
+    r = f64(c.c_kv)[[0, 2, 4]]
+    ref = r / np.sqrt((r * r).mean(-1, keepdims=True)) * f64(c.weight)
+    if kind == "e4m3":
+        assert np.array_equal(kv_out.view(torch.uint8).cpu().numpy()[[0, 2, 4], :512], cu.e4m3_bytes(ref / c.kv_scale))
+    elif kind == "model":
+        assert np.all(np.abs(f64(kv_out)[[0, 2, 4], :512] - ref) <= 2.0 ** -8 * np.abs(ref) * (1 + 2.0 ** -20))
+
+
+def test_append_one_token_of_any_stride():
+    """The stride of a dimension of one element means nothing."""
+    a, b = Case(1, 1, "model", seed=3), Case(1, 1, "model", seed=3)
+    b.c_kv = a.c_kv.clone().reshape(512, 1).t()
+    b.k_pe = a.k_pe.clone().reshape(64, 1).t()
+    b.q_pe = a.q_pe.clone().reshape(64, 1, 1).permute(1, 2, 0)
+    assert b.c_kv.stride(0) == 1 and b.q_pe.stride(1) == 1
+    (q1, kv1), (q2, kv2) = a.run(), b.run()
+    assert torch.equal(q1, q2) and torch.equal(kv1, kv2) and torch.equal(a.cache, b.cache)
+
+
 def test_append_far_slots():
     """Slots past 2^31 bytes into the pool (32-bit byte offsets would wrap)."""
     blocks = (1 << 31) // (256 * 324) + 40
