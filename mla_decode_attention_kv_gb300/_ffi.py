@@ -55,7 +55,6 @@ SIGNATURES = {
 STATUS = {0: "MLA_OK", 1: "MLA_ERR_NULL_POINTER", 2: "MLA_ERR_BAD_SHAPE",
           3: "MLA_ERR_BAD_DTYPE", 4: "MLA_ERR_MISALIGNED", 5: "MLA_ERR_BAD_SHARDS",
           6: "MLA_ERR_BAD_BLOCK", 7: "MLA_ERR_CUDA"}
-KV_FORMAT = {"model": 0, "e4m3": 1, "e2m1": 2}
 DTYPE = {"bf16": 0, "fp16": 1, "fp32": 2}
 
 

@@ -342,9 +342,11 @@ int mla_dcp_decode_partial_fp4(const void* q_abs, const void* q_pe, const void* 
   const int rows = mla::fp4_unit_rows(R);
   const int64_t G = (R + rows - 1) / rows;
   const int P = num_shards + (kv_cur ? 1 : 0);
-  // the kernel counts tokens, units and the cost of its tiles in 32 bits
+  // the kernel counts tokens (up to a round of the shards past the end), units
+  // (their fixed cost is a few tiles') and the cost of its tiles in 32 bits
   const int64_t tokens = static_cast<int64_t>(max_blocks) * block_size;
-  if (tokens > INT32_MAX || G * B * P > INT32_MAX / 4 || G * B * (tokens / 64 + 1) > INT32_MAX / 2)
+  if (tokens + static_cast<int64_t>(num_shards) * block_size + 64 > INT32_MAX || G * B * P > INT32_MAX / 16 ||
+      G * B * (tokens / 64 + 1) > INT32_MAX / 2)
     return MLA_ERR_BAD_SHAPE;
   CUtensorMap tm_qlat, tm_qpe;
   if (!make_map(&tm_qlat, q_abs, 512, B * R, 1024, 64, rows, bf16) ||

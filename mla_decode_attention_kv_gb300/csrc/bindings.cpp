@@ -99,6 +99,10 @@ int32_t* error_word(const at::Tensor* t, int dev) {
   return static_cast<int32_t*>(t->data_ptr());
 }
 
+// Elements from one index of dimension d to the next (a dimension of one may
+// have any stride: none is needed).
+int64_t step(const at::Tensor& t, int64_t d) { return t.size(d) > 1 ? t.stride(d) : 0; }
+
 void* ptr(const at::Tensor* t) { return t ? t->data_ptr() : nullptr; }
 
 int dtype_code(at::ScalarType dt) {
@@ -219,7 +223,7 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (q_out->sizes() != q_pe->sizes() || q_out->stride(2) != 1)
           bad_value("q_out must be [T, H, 64] with unit stride along its heads");
       }
-      qs = q_pe->stride(0), qh = q_pe->stride(1), os = q_out->stride(0), oh = q_out->stride(1);
+      qs = step(*q_pe, 0), qh = step(*q_pe, 1), os = step(*q_out, 0), oh = step(*q_out, 1);
     } else if (a[9] != Py_None) {
       bad_value("q_out without q_pe");
     }
@@ -232,12 +236,14 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
       on(*kv_out, dev, "kv_out", kt);
       if (kv_out->numel() != T * kQk || !kv_out->is_contiguous()) bad_value("kv_out must be a contiguous [T, 576] tensor");
     }
+    const int interleaved = PyObject_IsTrue(a[12]);
+    if (interleaved < 0) throw PythonError{};
     int st = MLA_OK;
     if (T > 0)
-      st = mla_kv_append(c_kv.data_ptr(), c_kv.stride(0), k_pe.data_ptr(), k_pe.stride(0), ptr(weight), number(a[7]),
+      st = mla_kv_append(c_kv.data_ptr(), step(c_kv, 0), k_pe.data_ptr(), step(k_pe, 0), ptr(weight), number(a[7]),
                          ptr(q_pe), qs, qh, static_cast<const int32_t*>(positions.data_ptr()), static_cast<int>(axes),
                          sections, static_cast<const float*>(cos_sin.data_ptr()), fits(cos_sin.size(0), "max_pos"),
-                         PyObject_IsTrue(a[12]), static_cast<const int32_t*>(slots.data_ptr()), fits(T, "T"),
+                         interleaved, static_cast<const int32_t*>(slots.data_ptr()), fits(T, "T"),
                          fits(H, "H"), fits(cache.size(0), "num_blocks"), fits(cache.size(1), "block_size"), code, fmt,
                          a[11] == Py_None ? 1.f : number(a[11]), cache.data_ptr(), q_out ? q_out->data_ptr() : nullptr, os,
                          oh, kv_out ? kv_out->data_ptr() : nullptr, err_word, stream.raw());
@@ -247,20 +253,25 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // ---------------------------------------------------------------- partials over E2M1 pages
 // The default workspace: one per (device, stream), as calls on one stream run
-// one after another; its size depends on the device alone.  (Never destroyed:
-// at the interpreter's end the allocator may be gone first.)
+// one after another; its size depends on the device alone.  A captured call gets
+// one of its own, from its graph's memory: graphs captured on one stream may
+// replay at once on others.  (Never destroyed: at the interpreter's end the
+// allocator may be gone first.)
 at::Tensor default_workspace(const at::Tensor& like, int dev, const Stream& stream, int B, int q_len, int shards, int cur) {
   static auto* kept = new std::map<std::pair<int, const void*>, at::Tensor>();
   static std::mutex mu;
   const std::pair<int, const void*> key{dev, stream.raw()};
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  cudaStreamIsCapturing(stream.s.stream(), &capture);
+  const bool keep = capture == cudaStreamCaptureStatusNone;
   std::lock_guard<std::mutex> lock(mu);
   const auto it = kept->find(key);
-  if (it != kept->end()) return it->second;
+  if (keep && it != kept->end()) return it->second;
   const uint64_t need = mla_dcp_decode_partial_fp4_workspace_size(B, q_len, shards, cur);
   if (need == 0) return at::Tensor();   // invalid sizes: the call itself reports them
   const c10::cuda::CUDAStreamGuard g(stream.s);
   at::Tensor t = make({static_cast<int64_t>(need)}, at::kByte, like);
-  kept->emplace(key, t);
+  if (keep) kept->emplace(key, t);
   return t;
 }
 

@@ -80,7 +80,9 @@ def test_fp4_host_checks(lib):
     for o, st in ((dict(q=None), 1), (dict(idt=2), 3), (dict(pdt=3), 3), (dict(H=129), 2), (dict(q_len=65), 2),
                   (dict(S=65), 5), (dict(bs=48), 6), (dict(kv=ODD), 4), (dict(cur=ODD), 4), (dict(slices=3), 2),
                   (dict(ws=ctypes.c_void_p(0x10010)), 4), (dict(kv_scale=0.0), 2), (dict(kv_scale=-1.0), 2),
-                  (dict(kv_scale=float("nan")), 2), (dict(kv_scale=float("inf")), 2)):
+                  (dict(kv_scale=float("nan")), 2), (dict(kv_scale=float("inf")), 2),
+                  # past the kernel's 32-bit counts: tokens with a round of shards, units, tiles
+                  (dict(mb=(1 << 26) - 2), 2), (dict(B=1 << 20, q_len=64, S=64), 2), (dict(B=1 << 16, mb=1 << 20), 2)):
         assert part(**o) == st, o
     assert lib.mla_dcp_decode_partial_fp4_workspace_size(0, 1, 2, 0) == 0
     assert lib.mla_dcp_decode_partial_fp4_workspace_size(2, 1, 65, 1) == 0

@@ -257,6 +257,48 @@ def test_fp4_graph_stream_and_two_workspaces():
         c.check(o, lse)
 
 
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("H,at", [(4, 3), (16, 511), (40, 256), (128, 100), (16, 575)])
+def test_fp4_current_rows_before_a_bad_token_stay_clean(value, H, at):
+    """A value of CURRENT token 2 that is not finite: query tokens 0 and 1 do not see
+    it, the others answer NaN (or, a score of -inf, as without it)."""
+    c = Fp4([70, 5], H, q_len=4, cur=True, seed=20, shards=1)
+    o1, l1 = c.run()
+    c.kv_cur[1, 2, at] = value
+    o2, l2 = c.run()
+    torch.cuda.synchronize()
+    assert c.err.item() == 0
+    assert torch.equal(o1[0], o2[0]) and torch.equal(l1[0], l2[0])
+    assert torch.equal(o1[1, :2], o2[1, :2]) and torch.equal(l1[1, :2], l2[1, :2])
+    assert torch.equal(o1[1, 2:, 0], o2[1, 2:, 0])     # (the history's part has no such token)
+    if at < 512:
+        assert torch.isnan(o2[1, 2:, 1]).all() and torch.isnan(l2[1, 2:, 1]).all()
+
+
+def test_fp4_graphs_with_default_workspaces():
+    """Graphs captured on one stream with the default workspace replay at once on two."""
+    cs = [Fp4([3000, 500], 16, shards=1, seed=12), Fp4([2500, 700], 64, shards=1, seed=13)]
+    graphs, outs, side = [], [], torch.cuda.Stream()
+    for c in cs:
+        o, lse = c.run()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            c.run(o_part=o, lse_part=lse)
+        graphs.append(g)
+        outs.append((o, lse))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        for (o, lse), s, g in zip(outs, streams, graphs):
+            with torch.cuda.stream(s):
+                o.zero_()
+                lse.zero_()
+                g.replay()
+    torch.cuda.synchronize()
+    for c, (o, lse) in zip(cs, outs):
+        c.check(o, lse)
+
+
 def test_fp4_decode_step_and_refusals():
     c = Fp4([300, 20], 16, cur=True, seed=14)
     W = torch.randn(16, 512, 128, device=DEV).to(torch.bfloat16)
