@@ -78,7 +78,7 @@ struct Smem4 {
   static constexpr int kPOff = kQOff + kQ;
   static constexpr int kP = kTile4 * N * 2;
   static constexpr int kStageOff = kPOff + kP;               // 16 rows: the epilogue's staging
-  static constexpr int kRawOff = kStageOff + (N == 16 ? 4096 : 0);
+  static constexpr int kRawOff = kStageOff + (N == 16 ? 8192 : 0);
   static constexpr int kMOff = kRawOff + 2 * kRawStage;      // reference maxima [N]
   static constexpr int kRedOff = kMOff + N * 4;              // reductions over the warps, [4][rows] for each pass
   static constexpr int kFlagOff = kRedOff + N * 16;          // [3 tiles][2 groups]: weights past the limit
@@ -225,89 +225,86 @@ struct PartScratch {
   int4 pre[1024];                  // of each thread's units: tiles and cost before, tiles of the first
   int bound[kFp4MaxCtas + 1];      // first tile of each CTA's share
   int whole[kFp4MaxCtas + 1];      // cost before the first unit that starts at or behind it
-  int4 rng;
+  int4 at[kFp4MaxCtas + 1];        // where that is: a unit, its tiles, the tiles before it, those of it before the boundary
+  Range4 rng;
 };
 
 template <int N, int NT>
-__device__ __forceinline__ Range4 partition4(const Fp4Params& fp, PartScratch* ps, int cid, int ncta) {
+__device__ __forceinline__ Range4 partition4(const Fp4Params& fp, PartScratch* ps, UnitTable* tab, int cid, int ncta) {
   constexpr int kWarps = NT / 32;
   static_assert(NT <= 1024 && NT > kFp4MaxCtas, "block size");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int U = fp.num_units;
   const int per = (U + NT - 1) / NT;
   auto cost_of = [](int nt) { return nt > 0 ? kCostTile * nt + kCostUnit<N> : 0; };
+  Unit4 mine = {0, 0, 0, 0, 0};      // the thread's first unit
+  int cnt = 0, cost = 0, ntiles = 0;
   {
-    int cnt = 0, cost = 0, first = 0;
     const int a = min(U, tid * per), e = min(U, a + per);
     for (int u = a; u < e; ++u) {
-      const int nt = tiles4(unit4<N>(fp, u));
-      if (u == a) first = nt;
+      const Unit4 ui = unit4<N>(fp, u);
+      const int nt = tiles4(ui);
+      if (u == a) {
+        mine = ui;
+        ntiles = nt;
+      }
       cnt += nt;
       cost += cost_of(nt);
     }
-    const unsigned long long mine = (static_cast<unsigned long long>(cost) << 32) | static_cast<unsigned>(cnt);
-    unsigned long long incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const unsigned long long y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
-    }
-    if (lane == 31) ps->scan[warp] = incl;
-    if (tid == 0) ps->rng = make_int4(0, 0, -1, 0);
-    __syncthreads();
-    unsigned long long base = 0;
-    for (int w = 0; w < warp; ++w) base += ps->scan[w];
-    const unsigned long long before = base + incl - mine;
-    ps->pre[tid] = make_int4(static_cast<int>(before & 0xffffffffu), static_cast<int>(before >> 32), first, 0);
   }
-  unsigned long long all = 0;
+  const unsigned long long own = (static_cast<unsigned long long>(cost) << 32) | static_cast<unsigned>(cnt);
+  unsigned long long incl = own, before = 0, all = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) all += ps->scan[w];
-  const int total = static_cast<int>(all & 0xffffffffu), all_cost = static_cast<int>(all >> 32);
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned long long y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) ps->scan[warp] = incl;
+  if (tid == 0) ps->rng = {0, 0, -1, 0};
   __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const unsigned long long x = ps->scan[w];
+    before += w < warp ? x : 0;
+    all += x;
+  }
+  before += incl - own;
+  ps->pre[tid] = make_int4(static_cast<int>(before & 0xffffffffu), static_cast<int>(before >> 32), ntiles, 0);
+  const int total = static_cast<int>(all & 0xffffffffu), all_cost = static_cast<int>(all >> 32);
   if (total == 0) {
     if (fp.split && tid == 0) {
       fp.ws_units[cid] = make_int4(-1, 0, 0, 0);
       fp.ws_bounds[cid] = 0;
       if (cid == 0) fp.ws_bounds[ncta] = 0;
     }
+    if (tid == 0) tab->first = tab->n = 0;
     return {0, 0, -1, 0};
   }
-  // The unit with tiles that holds tile (COST false) or cost (true) x: the
-  // thread whose units hold it, by bisection, then a walk along them.
-  struct Found {
-    int u, nt, t0, c0;   // unit, its tiles, tiles and cost before it
-  };
-  auto find = [&](int x, bool by_cost) {
-    int lo = 0, hi = min(U, NT) - 1;   // the last thread with pre <= x
+  __syncthreads();
+  // boundary c: the tiles that start below the cost c * all_cost / ncta
+  if (tid <= ncta) {
+    const int share = all_cost / ncta, rest = all_cost - share * ncta;
+    const int tc = tid == ncta ? all_cost - 1 : tid * share + tid * rest / ncta;
+    // the unit that holds it: the thread with its tiles by bisection, then a walk along the thread's units
+    int lo = 0, hi = min(U, NT) - 1;   // the last thread with a cost before it of at most tc
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if ((by_cost ? ps->pre[mid].y : ps->pre[mid].x) <= x) lo = mid;
+      if (ps->pre[mid].y <= tc) lo = mid;
       else hi = mid - 1;
     }
     const int4 p = ps->pre[lo];
-    Found f{lo * per, p.z, p.x, p.y};
-    for (;;) {
-      const int c = cost_of(f.nt);
-      if (by_cost ? x < f.c0 + c : x < f.t0 + f.nt) return f;
-      f.t0 += f.nt;
-      f.c0 += c;
-      f.nt = tiles4(unit4<N>(fp, ++f.u));
+    int u = lo * per, nt = p.z, t0 = p.x, c0 = p.y;
+    while (tc >= c0 + cost_of(nt)) {
+      t0 += nt;
+      c0 += cost_of(nt);
+      nt = tiles4(unit4<N>(fp, ++u));
     }
-  };
-  // boundary c: the tiles that start below the cost c * all_cost / ncta
-  if (tid <= ncta) {
-    const int tc = static_cast<int>(static_cast<int64_t>(tid) * all_cost / ncta);
-    int bound = total, whole = all_cost;
-    if (tid < ncta) {
-      const Found f = find(tc, true);
-      const int into = tc - f.c0 - kCostUnit<N>;
-      const int j = tid == 0 || into <= 0 ? 0 : min(f.nt, (into + kCostTile - 1) / kCostTile);
-      bound = tid == 0 ? 0 : f.t0 + j;
-      whole = tid == 0 ? 0 : j == 0 ? f.c0 : f.c0 + cost_of(f.nt);
-    }
-    ps->bound[tid] = bound;
-    ps->whole[tid] = whole;
+    const int into = tc - c0 - kCostUnit<N>;
+    int j = tid == 0 || into <= 0 ? 0 : min(nt, (into + kCostTile - 1) / kCostTile);
+    if (tid == ncta) j = nt;
+    ps->bound[tid] = t0 + j;
+    ps->whole[tid] = j == 0 ? c0 : c0 + cost_of(nt);
+    ps->at[tid] = make_int4(u, nt, t0, j);
   }
   __syncthreads();
   bool split = false;
@@ -317,42 +314,60 @@ __device__ __forceinline__ Range4 partition4(const Fp4Params& fp, PartScratch* p
     split = __syncthreads_or(over) != 0;
   }
   const int lo = ps->bound[cid], hi = ps->bound[cid + 1];
-  if (lo < hi && tid < 2) {
-    // thread 0 finds the first piece, thread 1 the last
-    Found f = find(tid == 0 ? lo : hi - 1, false);
-    if (tid == 0) {
-      if (!split && f.t0 < lo) {   // the first unit that starts in the share
-        f.t0 += f.nt;
-        do f.nt = ++f.u < U ? tiles4(unit4<N>(fp, f.u)) : 1;
-        while (f.nt == 0);
+  if (tid == 0) {
+    // the share's first unit and tile: the boundary's, or the next unit with tiles
+    if (lo < hi) {
+      const int4 f = ps->at[cid];
+      int u = f.x, j = f.w;
+      if (split ? j >= f.y : j > 0) {
+        j = 0;
+        do ++u;
+        while (u < U && tiles4(unit4<N>(fp, u)) == 0);
       }
-      ps->rng.x = f.u;
-      ps->rng.y = split ? lo - f.t0 : 0;
-      // the record of a unit cut before this share that ends inside it
-      int4 rec = make_int4(-1, 0, 0, 0);
-      if (split && lo > f.t0 && f.t0 + f.nt <= hi) {
-        int a = 0, e = ncta - 1;   // the CTA that holds the unit's first tile: the last with bound <= t0
-        while (a < e) {
-          const int mid = (a + e + 1) >> 1;
-          if (ps->bound[mid] <= f.t0) a = mid;
-          else e = mid - 1;
-        }
-        rec = make_int4(f.u, f.t0, a, cid);
-      }
-      if (fp.split) fp.ws_units[cid] = rec;
-    } else {
-      ps->rng.z = f.u;
-      ps->rng.w = split ? hi - f.t0 : f.nt;
+      ps->rng.u_begin = u;
+      ps->rng.j_begin = j;
     }
-  } else if (fp.split && tid == 0) {
-    fp.ws_units[cid] = make_int4(-1, 0, 0, 0);
-  }
-  if (fp.split && tid == 0) {
+  } else if (tid == 32) {
+    // the last unit, and how many of its tiles: those before the next boundary
+    if (lo < hi) {
+      const int4 f = ps->at[cid + 1];
+      int u = f.x, nt = f.y, j = f.w;
+      if (j == 0) {
+        do nt = tiles4(unit4<N>(fp, --u));
+        while (nt == 0);
+        j = nt;
+      }
+      ps->rng.u_last = u;
+      ps->rng.j_stop = split ? j : nt;
+    }
+  } else if (tid == 64 && fp.split) {
+    // the record of a unit cut before this share that ends inside it
+    const int4 f = ps->at[cid];
+    int4 rec = make_int4(-1, 0, 0, 0);
+    if (split && lo < hi && f.w > 0 && f.w < f.y && f.z + f.y <= hi) {
+      // the CTA with its first tile: the last whose boundary lies at most a unit's
+      // fixed cost behind the cost before it
+      const int64_t x = ps->whole[cid] - cost_of(f.y) + kCostUnit<N>;
+      rec = make_int4(f.x, f.z, static_cast<int>(((x + 1) * ncta + all_cost - 1) / all_cost) - 1, cid);
+    }
+    fp.ws_units[cid] = rec;
     fp.ws_bounds[cid] = lo;
     if (cid == 0) fp.ws_bounds[ncta] = total;
   }
   __syncthreads();
-  return {ps->rng.x, ps->rng.y, ps->rng.z, ps->rng.w};
+  const Range4 r = ps->rng;
+  // the geometry of the first units (mostly threads' own)
+  const int n = r.u_begin <= r.u_last ? min(r.u_last - r.u_begin + 1, kUnits4) : 0;
+  if (per == 1) {
+    if (static_cast<unsigned>(tid - r.u_begin) < static_cast<unsigned>(n)) tab->u[tid - r.u_begin] = mine;
+  } else if (tid < n) {
+    tab->u[tid] = unit4<N>(fp, r.u_begin + tid);
+  }
+  if (tid == 0) {
+    tab->first = r.u_begin;
+    tab->n = n;
+  }
+  return r;
 }
 
 // Row of o_part / lse_part of query row r (of R) of sequence b in part p.
@@ -588,15 +603,7 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
   // merge grid's start this one; each waits for the other to be done)
   griddep_launch_dependents();
   griddep_wait();
-  const Range4 rng = partition4<N, L::kThreads>(fp, reinterpret_cast<PartScratch*>(smem), cid, ncta);
-  {
-    const int n = rng.u_begin <= rng.u_last ? min(rng.u_last - rng.u_begin + 1, kUnits4) : 0;
-    if (static_cast<int>(threadIdx.x) < n) tab->u[threadIdx.x] = unit4<N>(fp, rng.u_begin + threadIdx.x);
-    if (threadIdx.x == 0) {
-      tab->first = rng.u_begin;
-      tab->n = n;
-    }
-  }
+  const Range4 rng = partition4<N, L::kThreads>(fp, reinterpret_cast<PartScratch*>(smem), tab, cid, ncta);
   tc_fence_before();
   __syncthreads();   // barriers, TMEM address, table; the scratch is free
   tc_fence_after();
@@ -801,17 +808,23 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
     const int tok = wq * 16 + (lane & 15);     // token of the tile
     const int cg = (lane >> 4) * NC;           // first column of this thread in a pass
     const int cr = cg + (lane & 15) / (16 / NC);   // column that col_reduce leaves here
+    auto col0 = [&](int q) { return (grp * PASSES + q) * NG; };   // first column of pass q
     auto red_of = [&](int q) { return reinterpret_cast<float*>(smem + L::kRedOff) + (grp * PASSES + q) * (4 * NG); };   // [4][NG]
     volatile int* flags = reinterpret_cast<volatile int*>(smem + L::kFlagOff);
-    float l[PASSES][NC], m[PASSES][NC];
+    float l[PASSES][NC];
+    // Reference maxima of pass q, in shared memory; the 64-row kernel, which would
+    // spill them, reads them there, the others keep a copy in registers (64 rows, 32 x
+    // 4096 tokens x 128 heads: 93 us with registers, 86 without; 16 rows, 16 x 131072
+    // tokens: 306 and 312).
+    constexpr bool kKeepM = PASSES == 1;
+    alignas(16) float m[NC];
+    auto m_of = [&](int q) { return reinterpret_cast<float*>(smem + L::kMOff) + col0(q) + cg; };
     Iter4<N> it;
     it.start(fp, tab, rng);
     int g = 0;
     bool ok = true;
-    // first column of pass q, where this token's weights go in P^T, and a warp's
-    // staging of the epilogue: its quarter of the pass's block of P, which no MMA
+    // where this token's weights go in P^T, and a warp's staging of the epilogue: its quarter of the pass's block of P, which no MMA
     // reads then (16 rows: both groups are in one block, so a region of its own)
-    auto col0 = [&](int q) { return (grp * PASSES + q) * NG; };
     auto put = [&](int q, const uint32_t (&w)[NC / 2]) {
       uint8_t* block = smem + L::kPOff + (N == 16 ? 0 : (grp * PASSES + q) * kPBlock);
       if constexpr (NC == 4)
@@ -819,25 +832,34 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
       else
         *reinterpret_cast<uint4*>(block + p_offset(tok, lane >> 4)) = make_uint4(w[0], w[1], w[2], w[3]);
     };
-    auto stage_of = [&](int q) {
-      return N == 16 ? smem + L::kStageOff + (warp - kSoftWarp) * 512
-                     : smem + L::kPOff + (grp * PASSES + q) * kPBlock + wq * (kPBlock / 4);
+    auto stage_of = [&](int i) {
+      return N == 16 ? smem + L::kStageOff + (warp - kSoftWarp) * 1024 + i * 512
+                     : smem + L::kPOff + (grp * PASSES + i) * kPBlock + wq * (kPBlock / 4);
     };
     // the tile's scores of pass q in the log2 domain, relative to mq, columns
     // below nmin masked (`all`: there are none)
-    auto scores = [&](int q, float sl, bool all, int nmin, const float (&mq)[NC], float (&x)[NC]) {
+    auto scores = [&](int q, float sl, bool all, int nmin, bool first, float (&x)[NC]) {
       uint32_t v[NC];
       tmem_half(tmem + lanes + L::kTmemS + (g & 1) * N + col0(q), v);
+      if (first) {
 #pragma unroll
-      for (int k = 0; k < NC; ++k) x[k] = fmaf(__uint_as_float(v[k]), sl, -mq[k]);
+        for (int k = 0; k < NC; ++k) x[k] = __uint_as_float(v[k]) * sl;
+      } else {
+        if constexpr (!kKeepM) {
+#pragma unroll
+          for (int k = 0; k < NC; k += 4) *reinterpret_cast<float4*>(m + k) = *reinterpret_cast<const float4*>(m_of(q) + k);
+        }
+#pragma unroll
+        for (int k = 0; k < NC; ++k) x[k] = fmaf(__uint_as_float(v[k]), sl, -m[k]);
+      }
       if (!all) {
 #pragma unroll
         for (int k = 0; k < NC; ++k) x[k] = col0(q) + cg + k >= nmin ? x[k] : -INFINITY;
       }
     };
-    // New reference maxima of 16 rows from the tile's scores x, with O and l
-    // brought to them (not for a piece's first tile).
-    auto new_maxima = [&](int q, const float (&x)[NC], float (&lq)[NC], float (&mq)[NC], bool first) {
+    // New reference maxima of a pass's rows from the tile's scores x, with O and l
+    // brought to them (the maxima of a piece's first tile are taken below).
+    auto new_maxima = [&](int q, const float (&x)[NC], float (&lq)[NC]) {
       float* red = red_of(q);
       float y[NC];
 #pragma unroll
@@ -851,42 +873,36 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
         const float* r = red + cg + k;
         const float t = fmaxf(fmaxf(r[0], r[NG]), fmaxf(r[2 * NG], r[3 * NG]));
         a[k] = 1.f;
-        if (first) {
-          mq[k] = t == -INFINITY ? 0.f : t;
-          lq[k] = 0.f;
-        } else if (t > kThresh) {   // (t is relative to mq)
-          const float mn = mq[k] + t;
-          a[k] = fast_exp2(mq[k] - mn);
-          mq[k] = mn;
+        if (t > kThresh) {   // (t is relative to m, which `scores` left here)
+          const float mn = m[k] + t;
+          a[k] = fast_exp2(m[k] - mn);
+          m[k] = mn;
           lq[k] *= a[k];
         }
       }
-      named_bar_sync(barid, 128);   // red has been read
+      named_bar_sync(barid, 128);   // red and the maxima have been read
       if (wq == 0 && (lane & 15) == 0) {
-        float* s_m = reinterpret_cast<float*>(smem + L::kMOff) + col0(q) + cg;
 #pragma unroll
         for (int k = 0; k < NC; ++k) {
-          s_m[k] = mq[k];
+          m_of(q)[k] = m[k];
           red[cg + k] = a[k];
         }
       }
       named_bar_sync(barid, 128);
-      if (!first) {
-        // O *= alpha (the PV product of the tile before is done)
-        tc_fence_after();
+      // O *= alpha (the PV product of the tile before is done)
+      tc_fence_after();
 #pragma unroll 1
-        for (int c = 0; c < 4 * NG; c += NO) {
-          uint32_t o[NO];
-          const uint32_t oa = tmem + lanes + L::kTmemO + (c / NG) * N + col0(q) + c % NG;
-          tmem_get(oa, o);
+      for (int c = 0; c < 4 * NG; c += NO) {
+        uint32_t o[NO];
+        const uint32_t oa = tmem + lanes + L::kTmemO + (c / NG) * N + col0(q) + c % NG;
+        tmem_get(oa, o);
 #pragma unroll
-          for (int k = 0; k < NO; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * red[c % NG + k]);
-          tmem_put(oa, o);
-        }
-        tmem_wait_st();
-        tc_fence_before();
-        named_bar_sync(barid, 128);   // alpha has been read
+        for (int k = 0; k < NO; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * red[c % NG + k]);
+        tmem_put(oa, o);
       }
+      tmem_wait_st();
+      tc_fence_before();
+      named_bar_sync(barid, 128);   // alpha has been read
     };
     // weights of the scores, in place (masked: exp2(-inf) = 0), and in 16 bits
     auto weights = [&](float (&x)[NC], uint32_t (&pk)[NC / 2]) {
@@ -910,14 +926,26 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
       ok = __all_sync(0xffffffffu, ok && waits.lazy(&bar[L::B_S_FULL + sb], (g >> 1) & 1)) != 0;
       tc_fence_after();
       if (first) {
-        if (!named_bar_and(barid, 128, ok)) break;
+        // reference maxima of the piece
 #pragma unroll
         for (int q = 0; q < PASSES; ++q) {
           float x[NC];
 #pragma unroll
-          for (int k = 0; k < NC; ++k) m[q][k] = 0.f;
-          scores(q, sl, all, nmin, m[q], x);
-          new_maxima(q, x, l[q], m[q], true);
+          for (int k = 0; k < NC; ++k) l[q][k] = 0.f;
+          scores(q, sl, all, nmin, true, x);
+          const float mx = col_reduce<NC, true>(x, lane);
+          red_of(q)[wq * NG + cr] = mx;
+        }
+        if (!named_bar_and(barid, 128, ok)) break;
+        if (wq == 0 && lane < NG * PASSES) {
+          const float* r = red_of(0) + (lane / NG) * (4 * NG) + lane % NG;
+          const float t = fmaxf(fmaxf(r[0], r[NG]), fmaxf(r[2 * NG], r[3 * NG]));
+          reinterpret_cast<float*>(smem + L::kMOff)[col0(0) + lane] = t == -INFINITY ? 0.f : t;
+        }
+        named_bar_sync(barid, 128);
+        if constexpr (kKeepM) {
+#pragma unroll
+          for (int k = 0; k < NC; ++k) m[k] = m_of(0)[k];
         }
       }
       // The weights are made and handed over against the reference maxima as
@@ -930,7 +958,7 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
 #pragma unroll
       for (int q = 0; q < PASSES; ++q) {
         float x[NC];
-        scores(q, sl, all, nmin, m[q], x);
+        scores(q, sl, all, nmin, false, x);
         float top = fmaxf(x[0], x[1]);
 #pragma unroll
         for (int k = 2; k < NC; ++k) top = fmaxf(top, x[k]);
@@ -966,9 +994,9 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
 #pragma unroll
             for (int q = 0; q < PASSES; ++q) {
               float x[NC];
-              scores(q, sl, all, nmin, m[q], x);
-              new_maxima(q, x, l[q], m[q], false);   // (scales what l has of this tile, too)
-              scores(q, sl, all, nmin, m[q], x);
+              scores(q, sl, all, nmin, false, x);
+              new_maxima(q, x, l[q]);   // (scales what l has of this tile, too)
+              scores(q, sl, all, nmin, false, x);
               weights(x, pk[q]);
               put(q, pk[q]);
               if (over >> q & 1) {
@@ -986,12 +1014,9 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar[L::B_S_EMPTY + sb]);
       if (it.last()) {
-        // ---- epilogue of the piece: row sums over the tokens, O / l, LSE
-        ok = __all_sync(0xffffffffu, ok && waits.lazy(&bar[L::B_P_EMPTY], g & 1)) != 0;
-        if (!named_bar_and(barid, 128, ok)) break;
-        tc_fence_after();
+        // ---- epilogue of the piece: row sums over the tokens, O / l, LSE.  The sums,
+        // factors and places are worked out while the last PV product runs.
         const bool whole = it.whole();
-        const int slot = 2 * cid + (it.u == rng.u_begin ? 0 : 1);
         const int esz = fp.part_dtype == kFP32 ? 4 : 2;
         char* out = static_cast<char*>(whole ? fp.o_part : fp.ws_o);
 #pragma unroll
@@ -999,36 +1024,43 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
           const float part = col_reduce<NC, false>(l[q], lane);
           red_of(q)[wq * NG + cr] = part;
         }
-        named_bar_sync(barid, 128);
-        // row `lane` of the group's: its sum, then its factor and where it goes
+        if (!named_bar_and(barid, 128, ok)) break;
+        // row `lane` of the group's, by one warp: its sum, then its factor and where it goes
         constexpr int NR = NG * PASSES;
-        const float* rl = red_of(0) + (lane / NG) * (4 * NG) + lane % NG;
-        float sum = 1.f;
-        if (lane < NR) sum = (rl[0] + rl[NG]) + (rl[2 * NG] + rl[3 * NG]);
-        named_bar_sync(barid, 128);
         float* inv = red_of(0);                                  // [NR]
-        int64_t* dst = reinterpret_cast<int64_t*>(inv + NR);     // [NR] byte offset of the row, -1: none
-        if (wq == 0 && lane < NR) {
-          const int n = col0(0) + lane, r = ui.g * N + n;
-          const float lse2 = reinterpret_cast<const float*>(smem + L::kMOff)[n] + log2f(sum);
-          int64_t row = -1;
-          if (r < fp.R) {
-            row = whole ? out_row4(fp, ui.b, r, ui.p) : static_cast<int64_t>(slot) * N + n;
-            if (whole) fp.lse_part[row] = lse2 * kLn2;
-            else fp.ws_lse[row] = lse2;
+        int* dst = reinterpret_cast<int*>(inv + NR);             // [NR] row of the output, -1: none
+        if (wq == 0) {
+          const float* rl = red_of(0) + (lane / NG) * (4 * NG) + lane % NG;
+          float sum = 1.f;
+          if (lane < NR) sum = (rl[0] + rl[NG]) + (rl[2 * NG] + rl[3 * NG]);
+          __syncwarp();
+          if (lane < NR) {
+            const int n = col0(0) + lane, r = ui.g * N + n;
+            const int slot = 2 * cid + (it.u == rng.u_begin ? 0 : 1);
+            const float lse2 = reinterpret_cast<const float*>(smem + L::kMOff)[n] + log2f(sum);
+            int row = -1;
+            if (r < fp.R) {
+              row = whole ? static_cast<int>(out_row4(fp, ui.b, r, ui.p)) : slot * N + n;
+              if (whole) fp.lse_part[row] = lse2 * kLn2;
+              else fp.ws_lse[row] = lse2;
+            }
+            inv[lane] = (cur ? 1.f : fp.kv_scale) / sum;
+            dst[lane] = row;
           }
-          inv[lane] = (cur ? 1.f : fp.kv_scale) / sum;
-          dst[lane] = row < 0 ? -1 : row * 512 * esz;
         }
-        named_bar_sync(barid, 128);
+        ok = __all_sync(0xffffffffu, waits.lazy(&bar[L::B_P_EMPTY], g & 1)) != 0;
+        if (!named_bar_and(barid, 128, ok)) break;
+        tc_fence_after();
         if (esz == 2) {
           // 32 latents of 8 rows at a time: read as matrix fragments, scaled,
           // stored transposed into the warp's staging (16-byte unit j of row k at
           // unit j ^ (k / 2 & 3): no bank conflicts) and from there to the rows,
           // 16 bytes a lane
           constexpr int NF = NG / 2;             // registers of a fragment: 4 for 8 rows
+          constexpr int CU = N == 16 ? 2 : 1;    // blocks of 128 latents at a time
+          constexpr int KA = N == 64 ? 2 : 1;    // eights of rows at a time
           float f[PASSES][NG / 4];
-          char* to[PASSES][NG / 8];
+          int to[PASSES][NG / 8];                // rows of the output
           const int row = lane >> 2, unit = (lane & 3) ^ ((lane >> 3) & 3);
           const int mrow = lane & 7, munit = (lane >> 3) ^ ((mrow >> 1) & 3);
 #pragma unroll
@@ -1037,38 +1069,51 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
             for (int k = 0; k < NG / 8; ++k) {
               f[q][2 * k] = inv[q * NG + 8 * k + 2 * (lane & 3)];
               f[q][2 * k + 1] = inv[q * NG + 8 * k + 2 * (lane & 3) + 1];
-              const int64_t d = dst[q * NG + 8 * k + row];
-              to[q][k] = d < 0 ? nullptr : out + d + wq * 64 + (lane & 3) * 16;
+              to[q][k] = dst[q * NG + 8 * k + row];
             }
           }
+          named_bar_sync(barid, 128);   // red has been read
+          out += wq * 64 + (lane & 3) * 16;
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < 4; c += CU) {
 #pragma unroll
             for (int q = 0; q < PASSES; ++q) {
-              uint32_t lo[NF], hi[NF];           // latents 0-15 and 16-31 of the warp's 32
-              const uint32_t oa = tmem + lanes + L::kTmemO + c * N + col0(q);
-              tmem_ld_frag(oa, lo);
-              tmem_ld_frag(oa + (16u << 16), hi);
-              tmem_wait_frag(lo, hi);
-              const uint32_t stage = smem_u32(stage_of(q));
+              uint32_t lo[CU][NF], hi[CU][NF];   // latents 0-15 and 16-31 of the warp's 32
 #pragma unroll
-              for (int k = 0; k < NG / 8; ++k) {
-                uint32_t w[4];
+              for (int e = 0; e < CU; ++e) {
+                const uint32_t oa = tmem + lanes + L::kTmemO + (c + e) * N + col0(q);
+                tmem_ld_frag(oa, lo[e]);
+                tmem_ld_frag(oa + (16u << 16), hi[e]);
+              }
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                  w[j] = pack2_dt(__uint_as_float(lo[4 * k + 2 * j]) * f[q][2 * k],
-                                  __uint_as_float(lo[4 * k + 2 * j + 1]) * f[q][2 * k + 1], fp.part_dtype);
-                  w[2 + j] = pack2_dt(__uint_as_float(hi[4 * k + 2 * j]) * f[q][2 * k],
-                                      __uint_as_float(hi[4 * k + 2 * j + 1]) * f[q][2 * k + 1], fp.part_dtype);
-                }
+              for (int e = 0; e < CU; ++e) tmem_wait_frag(lo[e], hi[e]);
+#pragma unroll
+              for (int k0 = 0; k0 < NG / 8; k0 += KA) {
                 __syncwarp();   // the staging has been read
-                stmatrix_x4_trans(stage + mrow * 64 + munit * 16, w[0], w[1], w[2], w[3]);
+#pragma unroll
+                for (int i = 0; i < CU * KA; ++i) {
+                  const int e = i / KA, k = k0 + i % KA;
+                  uint32_t w[4];
+#pragma unroll
+                  for (int j = 0; j < 2; ++j) {
+                    w[j] = pack2_dt(__uint_as_float(lo[e][4 * k + 2 * j]) * f[q][2 * k],
+                                    __uint_as_float(lo[e][4 * k + 2 * j + 1]) * f[q][2 * k + 1], fp.part_dtype);
+                    w[2 + j] = pack2_dt(__uint_as_float(hi[e][4 * k + 2 * j]) * f[q][2 * k],
+                                        __uint_as_float(hi[e][4 * k + 2 * j + 1]) * f[q][2 * k + 1], fp.part_dtype);
+                  }
+                  stmatrix_x4_trans(smem_u32(stage_of(i)) + mrow * 64 + munit * 16, w[0], w[1], w[2], w[3]);
+                }
                 __syncwarp();
-                const uint4 x = ld_shared_v4(stage + row * 64 + unit * 16);
-                if (to[q][k]) *reinterpret_cast<uint4*>(to[q][k] + c * 256) = x;
+#pragma unroll
+                for (int i = 0; i < CU * KA; ++i) {
+                  const int e = i / KA, k = k0 + i % KA;
+                  const uint4 x = ld_shared_v4(smem_u32(stage_of(i)) + row * 64 + unit * 16);
+                  if (to[q][k] >= 0) *reinterpret_cast<uint4*>(out + to[q][k] * int64_t{1024} + (c + e) * 256) = x;
+                }
               }
             }
           }
+          tc_fence_before();
         } else {
           // fp32 rows: 8 rows of 32 latents at a time, written a latent per lane
 #pragma unroll 1
@@ -1088,14 +1133,14 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
                 __syncwarp();
                 const uint4 x = *reinterpret_cast<const uint4*>(stage + lane * 16);
                 const int64_t d = dst[q * NG + n0 + h + (lane >> 3)];
-                if (d >= 0) *reinterpret_cast<uint4*>(out + d + lat0 * 4 + (lane & 7) * 16) = x;
+                if (d >= 0) *reinterpret_cast<uint4*>(out + d * 2048 + lat0 * 4 + (lane & 7) * 16) = x;
                 __syncwarp();
               }
             }
           }
+          tc_fence_before();
+          named_bar_sync(barid, 128);   // red has been read
         }
-        tc_fence_before();
-        named_bar_sync(barid, 128);   // red has been read
       }
       it.advance(fp);
       ++g;
