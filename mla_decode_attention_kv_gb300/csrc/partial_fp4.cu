@@ -56,7 +56,6 @@ constexpr int kUnpackWarps = 16;                 // eight for each half of a til
 constexpr int kRawCodes = kTile4 * kE2m1Codes;   // 18432
 constexpr int kRawStage = kTile4 * kE2m1Row;     // 20736
 constexpr int kChunk = kTile4 * 128;             // 8 KB: 64 columns of a tile
-constexpr int kHalf = 4 * kChunk;                // 32 KB: 256 latents of a tile, two M blocks of the PV product
 constexpr int kUnits4 = 8;                       // units whose geometry is kept in shared memory
 
 struct Unit4 {
@@ -65,21 +64,24 @@ struct Unit4 {
 
 template <int N>
 struct Smem4 {
-  static constexpr int kNH = N == 64 ? 3 : 4;    // half slots (a tile takes two)
+  static constexpr int kParts = N == 64 ? 4 : 2;             // parts that a tile's latents are unpacked in
+  static constexpr int kPart = 8 * kChunk / kParts;          // bytes of one
+  static constexpr int kSlots = N == 64 ? 7 : 4;             // of them in the ring
+  static constexpr int kNRaw = N == 64 ? 1 : 2;              // raw tiles
   static constexpr int kNR = N == 64 ? 1 : 2;    // RoPE slots
   static constexpr int kRows = N == 16 ? 8 : 16;               // rows (columns of S^T) that a group takes at a time
   static constexpr int kPasses = N / (kGroups4 * kRows);
   static constexpr int kUnpackWarp = kSoftWarp + 4 * kGroups4;
   static constexpr int kThreads = (kUnpackWarp + kUnpackWarps) * 32;
   static constexpr int kQ = N * 128 * 9;
-  static constexpr int kHalfOff = 0;
-  static constexpr int kRopeOff = kHalfOff + kNH * kHalf;
+  static constexpr int kLatOff = 0;
+  static constexpr int kRopeOff = kLatOff + kSlots * kPart;
   static constexpr int kQOff = kRopeOff + kNR * kChunk;
   static constexpr int kPOff = kQOff + kQ;
   static constexpr int kP = kTile4 * N * 2;
   static constexpr int kStageOff = kPOff + kP;               // 16 rows: the epilogue's staging
   static constexpr int kRawOff = kStageOff + (N == 16 ? 8192 : 0);
-  static constexpr int kMOff = kRawOff + 2 * kRawStage;      // reference maxima [N]
+  static constexpr int kMOff = kRawOff + kNRaw * kRawStage;  // reference maxima [N]
   static constexpr int kRedOff = kMOff + N * 4;              // reductions over the warps, [4][rows] for each pass
   static constexpr int kFlagOff = kRedOff + N * 16;          // [3 tiles][2 groups]: weights past the limit
   static constexpr int kUnitOff = kFlagOff + 32;
@@ -87,10 +89,10 @@ struct Smem4 {
   // barrier slots
   enum : int {
     B_RAW_FULL = 0,
-    B_RAW_EMPTY = 2,
-    B_FULL = 4,
-    B_EMPTY = B_FULL + kNH,
-    B_Q_FULL = B_EMPTY + kNH,
+    B_RAW_EMPTY = kNRaw,
+    B_FULL = 2 * kNRaw,
+    B_EMPTY = B_FULL + kSlots,
+    B_Q_FULL = B_EMPTY + kSlots,
     B_Q_EMPTY,
     B_S_FULL,
     B_S_EMPTY = B_S_FULL + 2,
@@ -387,18 +389,24 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 
 // Columns [c, c + NC) of an M = 64 accumulator for lanes 0-15 of the warp and
 // [c + NC, c + 2 NC) for lanes 16-31, both of the rows in TMEM lanes 0-15.
-__device__ __forceinline__ void tmem_half(uint32_t a, uint32_t (&r)[4]) {
-  asm volatile("tcgen05.ld.sync.aligned.16x32bx2.x4.b32 {%0,%1,%2,%3}, [%4], 4;\n tcgen05.wait::ld.sync.aligned;"
+__device__ __forceinline__ void tmem_half_issue(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x32bx2.x4.b32 {%0,%1,%2,%3}, [%4], 4;"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(a)
-               : "memory");
+               : "r"(a));
 }
-__device__ __forceinline__ void tmem_half(uint32_t a, uint32_t (&r)[8]) {
+__device__ __forceinline__ void tmem_half_issue(uint32_t a, uint32_t (&r)[8]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.16x32bx2.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8], 8;\n tcgen05.wait::ld.sync.aligned;"
+      "tcgen05.ld.sync.aligned.16x32bx2.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8], 8;"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-      : "r"(a)
-      : "memory");
+      : "r"(a));
+}
+
+template <int K>
+__device__ __forceinline__ void tmem_half(uint32_t a, uint32_t (&r)[K]) {
+  tmem_half_issue(a, r);
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int k = 0; k < K; ++k) asm volatile("" : "+r"(r[k])::"memory");
 }
 
 // Eight columns of this warp's 32 lanes, loaded and waited for
@@ -569,14 +577,16 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
   int* err = fp.err;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < L::kNRaw; ++s) {
       mbar_init(&bar[L::B_RAW_FULL + s], 1);
       mbar_init(&bar[L::B_RAW_EMPTY + s], kUnpackWarps);
+    }
+    for (int s = 0; s < 2; ++s) {
       mbar_init(&bar[L::B_S_FULL + s], 1);
       mbar_init(&bar[L::B_S_EMPTY + s], 4 * kGroups4);
     }
-    for (int s = 0; s < L::kNH; ++s) {
-      mbar_init(&bar[L::B_FULL + s], kUnpackWarps / 2);
+    for (int s = 0; s < L::kSlots; ++s) {
+      mbar_init(&bar[L::B_FULL + s], kUnpackWarps / L::kParts);
       mbar_init(&bar[L::B_EMPTY + s], 1);
     }
     mbar_init(&bar[L::B_Q_FULL], 1);
@@ -628,8 +638,9 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
       nx.advance(fp);
       const int id_next = fetch(nx);
       if (it.ui.p != fp.S) {
-        const int st = rs & 1;
-        if (rs >= 2 && !__all_sync(0xffffffffu, waits.wait(&bar[L::B_RAW_EMPTY + st], ((rs >> 1) - 1) & 1))) break;
+        const int st = rs % L::kNRaw;
+        if (rs >= L::kNRaw && !__all_sync(0xffffffffu, waits.wait(&bar[L::B_RAW_EMPTY + st], (rs / L::kNRaw - 1) & 1)))
+          break;
         uint8_t* raw = smem + L::kRawOff + st * kRawStage;
         if (lane == 0) mbar_arrive_expect_tx(&bar[L::B_RAW_FULL + st], kRawStage);
         __syncwarp();
@@ -666,9 +677,9 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
       it = nx;
     }
     if (lane == 0) {   // what was issued has landed before the CTA ends
-      for (int s = 0; s < 2 && s < rs; ++s) {
-        const int last = rs - 1 - ((rs - 1 - s) & 1);
-        mbar_wait(&bar[L::B_RAW_FULL + s], (last >> 1) & 1, err);
+      for (int s = 0; s < L::kNRaw && s < rs; ++s) {
+        const int last = rs - 1 - (rs - 1 - s) % L::kNRaw;
+        mbar_wait(&bar[L::B_RAW_FULL + s], (last / L::kNRaw) & 1, err);
       }
       if (qloads > 0) mbar_wait(&bar[L::B_Q_FULL], (qloads - 1) & 1, err);
     }
@@ -680,7 +691,7 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
     // changes at a unit's end is worked out once per piece, not per tile.
     const bool leader = elect_one();
     constexpr uint32_t idesc = make_idesc_f16(64, N, BF16, false, false);
-    const uint64_t a0 = make_desc_sw128(smem_u32(smem + L::kHalfOff), 16, 1024);
+    const uint64_t a0 = make_desc_sw128(smem_u32(smem + L::kLatOff), 16, 1024);
     const uint64_t r0 = make_desc_sw128(smem_u32(smem + L::kRopeOff), 16, 1024);
     const uint64_t q0 = make_desc_sw128(smem_u32(smem + L::kQOff), 16, 1024);
     auto wait = [&](uint64_t* b, uint32_t parity) { return __all_sync(0xffffffffu, waits.wait(b, parity)) != 0; };
@@ -701,26 +712,27 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
         }
         const uint32_t d = tmem + L::kTmemS + sb * N;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int hc = 2 * g + h, sl = hc % L::kNH;
-          if (!wait(&bar[L::B_FULL + sl], (hc / L::kNH) & 1)) {
+        for (int h = 0; h < L::kParts; ++h) {
+          const int hc = L::kParts * g + h, sl = hc % L::kSlots;
+          if (!wait(&bar[L::B_FULL + sl], (hc / L::kSlots) & 1)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          if (h == 0) {   // the RoPE columns come with the first half
+          constexpr int kOps = 32 / L::kParts;
+          const uint64_t a = a0 + sl * (L::kPart >> 4);
+#pragma unroll
+          for (int kk = 0; kk < kOps; ++kk)
+            if (leader)
+              umma_ss(d, a + (kk >> 2) * (kChunk >> 4) + (kk & 3) * 2,
+                      q0 + ((kOps / 4) * h + (kk >> 2)) * (N * 8) + (kk & 3) * 2, idesc, h || kk ? 1u : 0u);
+          if (h == L::kParts / 2 - 1) {   // the RoPE columns come with the first half
             const uint64_t r = r0 + (g % L::kNR) * (kChunk >> 4);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              if (leader) umma_ss(d, r + kk * 2, q0 + 8 * (N * 8) + kk * 2, idesc, kk ? 1u : 0u);
+              if (leader) umma_ss(d, r + kk * 2, q0 + 8 * (N * 8) + kk * 2, idesc, 1u);
             if (L::kNR == 1 && leader) umma_commit(&bar[L::B_ROPE_EMPTY]);
           }
-          const uint64_t a = a0 + sl * (kHalf >> 4);
-#pragma unroll
-          for (int kk = 0; kk < 16; ++kk)
-            if (leader)
-              umma_ss(d, a + (kk >> 2) * (kChunk >> 4) + (kk & 3) * 2, q0 + (4 * h + (kk >> 2)) * (N * 8) + (kk & 3) * 2,
-                      idesc, 1u);
         }
         if (!ok) break;
         if (leader) {
@@ -736,7 +748,7 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
     // ------------------------------------------------ PV issuer: O^T += V^T P^T
     const bool leader = elect_one();
     constexpr uint32_t idesc = make_idesc_f16(128, N, BF16, true, true);
-    const uint64_t v0 = make_desc_sw128(smem_u32(smem + L::kHalfOff), kChunk, 1024);
+    const uint64_t v0 = make_desc_sw128(smem_u32(smem + L::kLatOff), kChunk, 1024);
     const uint64_t p0 = p_desc(smem_u32(smem + L::kPOff));
     auto wait = [&](uint64_t* b, uint32_t parity) { return __all_sync(0xffffffffu, waits.wait(b, parity)) != 0; };
     Iter4<N> it;
@@ -762,16 +774,17 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
         tc_fence_after();
         const uint32_t more = k > 0 ? 1u : 0u;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int sl = (2 * g + h) % L::kNH;
-          const uint64_t v = v0 + sl * (kHalf >> 4);
+        for (int h = 0; h < L::kParts; ++h) {
+          const int sl = (L::kParts * g + h) % L::kSlots;
+          const uint64_t v = v0 + sl * (L::kPart >> 4);
+          constexpr int kBlocks = 4 / L::kParts;
 #pragma unroll
-          for (int p = 0; p < 2; ++p) {
+          for (int p = 0; p < kBlocks; ++p) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
               if (leader)
-                umma_ss(tmem + L::kTmemO + (2 * h + p) * N, v + p * (2 * kChunk >> 4) + kk * 128, p0 + kk * (kPStep >> 4), idesc,
-                        kk ? 1u : more);
+                umma_ss(tmem + L::kTmemO + (kBlocks * h + p) * N, v + p * (2 * kChunk >> 4) + kk * 128,
+                        p0 + kk * (kPStep >> 4), idesc, kk ? 1u : more);
           }
           if (leader) umma_commit(&bar[L::B_EMPTY + sl]);
         }
@@ -838,6 +851,18 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
     };
     // the tile's scores of pass q in the log2 domain, relative to mq, columns
     // below nmin masked (`all`: there are none)
+    auto rel = [&](int q, float sl, bool all, int nmin, const uint32_t (&v)[NC], float (&x)[NC]) {
+      if constexpr (!kKeepM) {
+#pragma unroll
+        for (int k = 0; k < NC; k += 4) *reinterpret_cast<float4*>(m + k) = *reinterpret_cast<const float4*>(m_of(q) + k);
+      }
+#pragma unroll
+      for (int k = 0; k < NC; ++k) x[k] = fmaf(__uint_as_float(v[k]), sl, -m[k]);
+      if (!all) {
+#pragma unroll
+        for (int k = 0; k < NC; ++k) x[k] = col0(q) + cg + k >= nmin ? x[k] : -INFINITY;
+      }
+    };
     auto scores = [&](int q, float sl, bool all, int nmin, bool first, float (&x)[NC]) {
       uint32_t v[NC];
       tmem_half(tmem + lanes + L::kTmemS + (g & 1) * N + col0(q), v);
@@ -923,6 +948,10 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
       int nmin = N;
       if (it.tok0() + tok < ui.hi) nmin = cur ? min(N, max(0, tok * fp.H - ui.g * N)) : 0;
       const bool all = !cur && it.tok0() + kTile4 <= ui.hi;
+      // P's place is as a rule free before the scores are there: waited for first, it is
+      // off the path from the scores to the weights (16 rows 307 -> 304 us, 64 rows 862
+      // -> 838 us; with 32 rows it is the other way round, 324 -> 343 us)
+      if (N != 32 && g >= 1) ok = ok && waits.lazy(&bar[L::B_P_EMPTY], (g - 1) & 1);
       ok = __all_sync(0xffffffffu, ok && waits.lazy(&bar[L::B_S_FULL + sb], (g >> 1) & 1)) != 0;
       tc_fence_after();
       if (first) {
@@ -954,11 +983,19 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
       // looks at the flags, reads them.  (A barrier to agree first cost 500
       // cycles of every tile.)
       uint32_t pk[PASSES][NC / 2];
+      uint32_t sv[PASSES][NC];
+#pragma unroll
+      for (int q = 0; q < PASSES; ++q) tmem_half_issue(tmem + lanes + L::kTmemS + (g & 1) * N + col0(q), sv[q]);
+      tmem_wait_ld();
+#pragma unroll
+      for (int q = 0; q < PASSES; ++q)
+#pragma unroll
+        for (int k = 0; k < NC; ++k) asm volatile("" : "+r"(sv[q][k])::"memory");
       uint32_t over = 0;   // passes of this warp with such a weight: not in l yet
 #pragma unroll
       for (int q = 0; q < PASSES; ++q) {
         float x[NC];
-        scores(q, sl, all, nmin, false, x);
+        rel(q, sl, all, nmin, sv[q], x);
         float top = fmaxf(x[0], x[1]);
 #pragma unroll
         for (int k = 2; k < NC; ++k) top = fmaxf(top, x[k]);
@@ -970,7 +1007,7 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
           for (int k = 0; k < NC; ++k) l[q][k] += x[k];
         }
       }
-      if (g >= 1) ok = __all_sync(0xffffffffu, ok && waits.lazy(&bar[L::B_P_EMPTY], (g - 1) & 1)) != 0;
+      if (N == 32 && g >= 1) ok = __all_sync(0xffffffffu, ok && waits.lazy(&bar[L::B_P_EMPTY], (g - 1) & 1)) != 0;
       if (ok) {
 #pragma unroll
         for (int q = 0; q < PASSES; ++q) put(q, pk[q]);
@@ -1153,7 +1190,8 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
     // stores alone.  One fence and one arrival a tile and warp.
     const int w = warp - L::kUnpackWarp;
     const int h = w >> 3, t = (w & 1) * 32 + lane, grp = (w >> 1) & 3;
-    uint8_t* half0 = smem + L::kHalfOff;
+    const int part = L::kParts == 2 ? h : 2 * h + (grp >> 1);
+    uint8_t* lat0 = smem + L::kLatOff + (L::kParts == 2 ? grp : grp & 1) * kChunk;   // (a chunk is the thread's two units)
     Iter4<N> it;
     it.start(fp, tab, rng);
     int g = 0, rs = 0;
@@ -1162,8 +1200,8 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
       const bool valid = it.tok0() + t < it.ui.hi;
       uint4 x[2][4], xr[2];
       if (!cur) {
-        const int st = rs & 1;
-        if (!__all_sync(0xffffffffu, waits.wait(&bar[L::B_RAW_FULL + st], (rs >> 1) & 1))) break;
+        const int st = rs % L::kNRaw;
+        if (!__all_sync(0xffffffffu, waits.wait(&bar[L::B_RAW_FULL + st], (rs / L::kNRaw) & 1))) break;
         const uint8_t* codes = smem + L::kRawOff + st * kRawStage + t * kE2m1Codes;
         const uint8_t* scales = smem + L::kRawOff + st * kRawStage + kRawCodes + t * kE2m1Scales;
         uint4 c[2];
@@ -1222,15 +1260,15 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
         for (int j = 0; j < 2; ++j) xr[j] = valid && h == 0 ? row[64 + grp * 2 + j] : none;
         if (!clean) xr[0].x = 0x7FFF7FFFu;
       }
-      const int hc = 2 * g + h, sl = hc % L::kNH;
-      if (hc >= L::kNH && !__all_sync(0xffffffffu, waits.wait(&bar[L::B_EMPTY + sl], ((hc / L::kNH) - 1) & 1))) break;
-      // (with two RoPE slots the last reader of this one was done before the half slot's)
+      const int hc = L::kParts * g + part, sl = hc % L::kSlots;
+      if (hc >= L::kSlots && !__all_sync(0xffffffffu, waits.wait(&bar[L::B_EMPTY + sl], ((hc / L::kSlots) - 1) & 1))) break;
+      // (with two RoPE slots the last reader of this one was done before the part's slot)
       if (L::kNR == 1 && h == 0 && g >= 1 &&
           !__all_sync(0xffffffffu, waits.wait(&bar[L::B_ROPE_EMPTY], (g - 1) & 1)))
         break;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        uint8_t* d = half0 + sl * kHalf + grp * kChunk;       // (a chunk is the thread's two units)
+        uint8_t* d = lat0 + sl * L::kPart;
 #pragma unroll
         for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(d + sw128_offset(t, k * 4 + j)) = x[k][j];
       }
