@@ -369,6 +369,9 @@ int mla_dcp_decode_partial_fp4(const void* q_abs, const void* q_pe, const void* 
   fp.S = num_shards;
   fp.P = P;
   fp.head_slices = head_slices;
+  fp.hs = H / head_slices;
+  fp.inv_H = H > 1 ? static_cast<uint32_t>(0xFFFFFFFFu / H + 1) : 0;
+  fp.inv_hs = fp.hs > 1 ? static_cast<uint32_t>(0xFFFFFFFFu / fp.hs + 1) : 0;
   fp.T = B * q_len;
   fp.R = static_cast<int>(R);
   fp.G = static_cast<int>(G);

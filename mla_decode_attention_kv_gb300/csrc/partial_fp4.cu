@@ -41,6 +41,7 @@
 //
 // Every wait is bounded, as in the 16-bit kernel.
 #include <mutex>
+#include <type_traits>
 #include "cache_kernels.cuh"
 #include "partial_fp4.cuh"
 #include "partial_sched.cuh"
@@ -82,8 +83,9 @@ struct Smem4 {
   static constexpr int kStageOff = kPOff + kP;               // 16 rows: the epilogue's staging
   static constexpr int kRawOff = kStageOff + (N == 16 ? 8192 : 0);
   static constexpr int kMOff = kRawOff + kNRaw * kRawStage;  // reference maxima [N]
-  static constexpr int kRedOff = kMOff + N * 4;              // reductions over the warps, [4][rows] for each pass
-  static constexpr int kFlagOff = kRedOff + N * 16;          // [3 tiles][2 groups]: weights past the limit
+  static constexpr int kRedOff = kMOff + N * 4;              // reductions over the warps, [4][rows] for each pass:
+                                                             // maxima, then sums
+  static constexpr int kFlagOff = kRedOff + 2 * N * 16;      // [3 tiles][2 groups]: weights past the limit
   static constexpr int kUnitOff = kFlagOff + 32;
   static constexpr int kBarOff = kUnitOff + ((kUnits4 * 20 + 8 + 15) / 16) * 16;
   // barrier slots
@@ -372,10 +374,13 @@ __device__ __forceinline__ Range4 partition4(const Fp4Params& fp, PartScratch* p
   return r;
 }
 
+// r / d for 0 <= r < 2^13, d <= 128, with inv = 2^32 / d rounded up (0 for d = 1):
+// the product is off by less than 2^-19, and r / d at least 2^-7 below the next integer
+__device__ __forceinline__ int quotient(int r, uint32_t inv) { return inv ? static_cast<int>(__umulhi(r, inv)) : r; }
+
 // Row of o_part / lse_part of query row r (of R) of sequence b in part p.
 __device__ __forceinline__ int64_t out_row4(const Fp4Params& fp, int b, int r, int p) {
-  const int i = r / fp.H, h = r - i * fp.H;
-  const int hs = fp.H / fp.head_slices, s = h / hs;
+  const int hs = fp.hs, i = quotient(r, fp.inv_H), h = r - i * fp.H, s = quotient(h, fp.inv_hs);
   return ((static_cast<int64_t>(s) * fp.T + static_cast<int64_t>(b) * fp.q_len + i) * fp.P + p) * hs + (h - s * hs);
 }
 
@@ -1059,36 +1064,33 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
 #pragma unroll
         for (int q = 0; q < PASSES; ++q) {
           const float part = col_reduce<NC, false>(l[q], lane);
-          red_of(q)[wq * NG + cr] = part;
+          red_of(q)[N * 4 + wq * NG + cr] = part;
         }
         if (!named_bar_and(barid, 128, ok)) break;
-        // row `lane` of the group's, by one warp: its sum, then its factor and where it goes
+        // row `lane` of the group's, in every warp: its sum, its factor and where it goes (-1: nowhere)
         constexpr int NR = NG * PASSES;
-        float* inv = red_of(0);                                  // [NR]
-        int* dst = reinterpret_cast<int*>(inv + NR);             // [NR] row of the output, -1: none
-        if (wq == 0) {
-          const float* rl = red_of(0) + (lane / NG) * (4 * NG) + lane % NG;
-          float sum = 1.f;
-          if (lane < NR) sum = (rl[0] + rl[NG]) + (rl[2 * NG] + rl[3 * NG]);
-          __syncwarp();
-          if (lane < NR) {
-            const int n = col0(0) + lane, r = ui.g * N + n;
+        float inv = 0.f;
+        int dst = -1;
+        if (lane < NR) {
+          const int n = col0(0) + lane, r = ui.g * N + n;
+          const float* rl = red_of(0) + N * 4 + (lane / NG) * (4 * NG) + lane % NG;
+          const float sum = (rl[0] + rl[NG]) + (rl[2 * NG] + rl[3 * NG]);
+          inv = (cur ? 1.f : fp.kv_scale) / sum;
+          if (r < fp.R) {
             const int slot = 2 * cid + (it.u == rng.u_begin ? 0 : 1);
-            const float lse2 = reinterpret_cast<const float*>(smem + L::kMOff)[n] + log2f(sum);
-            int row = -1;
-            if (r < fp.R) {
-              row = whole ? static_cast<int>(out_row4(fp, ui.b, r, ui.p)) : slot * N + n;
-              if (whole) fp.lse_part[row] = lse2 * kLn2;
-              else fp.ws_lse[row] = lse2;
+            dst = whole ? static_cast<int>(out_row4(fp, ui.b, r, ui.p)) : slot * N + n;
+            if (wq == 0) {
+              const float lse2 = reinterpret_cast<const float*>(smem + L::kMOff)[n] + log2f(sum);
+              if (whole) fp.lse_part[dst] = lse2 * kLn2;
+              else fp.ws_lse[dst] = lse2;
             }
-            inv[lane] = (cur ? 1.f : fp.kv_scale) / sum;
-            dst[lane] = row;
           }
         }
+        // (a wait that gives up shows at the group's next barrier)
         ok = __all_sync(0xffffffffu, waits.lazy(&bar[L::B_P_EMPTY], g & 1)) != 0;
-        if (!named_bar_and(barid, 128, ok)) break;
         tc_fence_after();
-        if (esz == 2) {
+        if (!ok) {
+        } else if (esz == 2) {
           // 32 latents of 8 rows at a time: read as matrix fragments, scaled,
           // stored transposed into the warp's staging (16-byte unit j of row k at
           // unit j ^ (k / 2 & 3): no bank conflicts) and from there to the rows,
@@ -1104,26 +1106,33 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
           for (int q = 0; q < PASSES; ++q) {
 #pragma unroll
             for (int k = 0; k < NG / 8; ++k) {
-              f[q][2 * k] = inv[q * NG + 8 * k + 2 * (lane & 3)];
-              f[q][2 * k + 1] = inv[q * NG + 8 * k + 2 * (lane & 3) + 1];
-              to[q][k] = dst[q * NG + 8 * k + row];
+              f[q][2 * k] = __shfl_sync(0xffffffffu, inv, q * NG + 8 * k + 2 * (lane & 3));
+              f[q][2 * k + 1] = __shfl_sync(0xffffffffu, inv, q * NG + 8 * k + 2 * (lane & 3) + 1);
+              to[q][k] = __shfl_sync(0xffffffffu, dst, q * NG + 8 * k + row);
             }
           }
-          named_bar_sync(barid, 128);   // red has been read
           out += wq * 64 + (lane & 3) * 16;
+          auto rows = [&](auto bf16) {   // (a branch for each pair of values otherwise)
+            constexpr bool kToBf16 = decltype(bf16)::value;
 #pragma unroll 1
           for (int c = 0; c < 4; c += CU) {
+            uint32_t lo_[PASSES][CU][NF], hi_[PASSES][CU][NF];
 #pragma unroll
-            for (int q = 0; q < PASSES; ++q) {
-              uint32_t lo[CU][NF], hi[CU][NF];   // latents 0-15 and 16-31 of the warp's 32
+            for (int q = 0; q < PASSES; ++q)
 #pragma unroll
               for (int e = 0; e < CU; ++e) {
                 const uint32_t oa = tmem + lanes + L::kTmemO + (c + e) * N + col0(q);
-                tmem_ld_frag(oa, lo[e]);
-                tmem_ld_frag(oa + (16u << 16), hi[e]);
+                tmem_ld_frag(oa, lo_[q][e]);
+                tmem_ld_frag(oa + (16u << 16), hi_[q][e]);
               }
 #pragma unroll
-              for (int e = 0; e < CU; ++e) tmem_wait_frag(lo[e], hi[e]);
+            for (int q = 0; q < PASSES; ++q)
+#pragma unroll
+              for (int e = 0; e < CU; ++e) tmem_wait_frag(lo_[q][e], hi_[q][e]);
+#pragma unroll
+            for (int q = 0; q < PASSES; ++q) {
+              auto& lo = lo_[q];
+              auto& hi = hi_[q];
 #pragma unroll
               for (int k0 = 0; k0 < NG / 8; k0 += KA) {
                 __syncwarp();   // the staging has been read
@@ -1133,10 +1142,10 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
                   uint32_t w[4];
 #pragma unroll
                   for (int j = 0; j < 2; ++j) {
-                    w[j] = pack2_dt(__uint_as_float(lo[e][4 * k + 2 * j]) * f[q][2 * k],
-                                    __uint_as_float(lo[e][4 * k + 2 * j + 1]) * f[q][2 * k + 1], fp.part_dtype);
-                    w[2 + j] = pack2_dt(__uint_as_float(hi[e][4 * k + 2 * j]) * f[q][2 * k],
-                                        __uint_as_float(hi[e][4 * k + 2 * j + 1]) * f[q][2 * k + 1], fp.part_dtype);
+                    w[j] = pack2<kToBf16>(__uint_as_float(lo[e][4 * k + 2 * j]) * f[q][2 * k],
+                                          __uint_as_float(lo[e][4 * k + 2 * j + 1]) * f[q][2 * k + 1]);
+                    w[2 + j] = pack2<kToBf16>(__uint_as_float(hi[e][4 * k + 2 * j]) * f[q][2 * k],
+                                              __uint_as_float(hi[e][4 * k + 2 * j + 1]) * f[q][2 * k + 1]);
                   }
                   stmatrix_x4_trans(smem_u32(stage_of(i)) + mrow * 64 + munit * 16, w[0], w[1], w[2], w[3]);
                 }
@@ -1150,6 +1159,9 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
               }
             }
           }
+          };
+          if (fp.part_dtype == kBF16) rows(std::true_type{});
+          else rows(std::false_type{});
           tc_fence_before();
         } else {
           // fp32 rows: 8 rows of 32 latents at a time, written a latent per lane
@@ -1166,17 +1178,16 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
               for (int h = 0; h < NO; h += NO / 2) {
 #pragma unroll
                 for (int k = 0; k < NO / 2; ++k)
-                  reinterpret_cast<float*>(stage)[k * 32 + lane] = __uint_as_float(o[h + k]) * inv[q * NG + n0 + h + k];
+                  reinterpret_cast<float*>(stage)[k * 32 + lane] = __uint_as_float(o[h + k]) * __shfl_sync(0xffffffffu, inv, q * NG + n0 + h + k);
                 __syncwarp();
                 const uint4 x = *reinterpret_cast<const uint4*>(stage + lane * 16);
-                const int64_t d = dst[q * NG + n0 + h + (lane >> 3)];
+                const int64_t d = __shfl_sync(0xffffffffu, dst, q * NG + n0 + h + (lane >> 3));
                 if (d >= 0) *reinterpret_cast<uint4*>(out + d * 2048 + lat0 * 4 + (lane & 7) * 16) = x;
                 __syncwarp();
               }
             }
           }
           tc_fence_before();
-          named_bar_sync(barid, 128);   // red has been read
         }
       }
       it.advance(fp);

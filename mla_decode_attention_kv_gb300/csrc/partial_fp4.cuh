@@ -22,6 +22,8 @@ struct Fp4Params {
   float* lse_part;
   int* err;
   int B, q_len, H, num_blocks, bs, max_blocks, S, P, head_slices;
+  int hs;                // heads of a slice
+  uint32_t inv_H, inv_hs;   // 2^32 / H and / hs rounded up, 0 for 1
   int T;                 // B * q_len
   int R;                 // query rows of a sequence: q_len * H
   int G;                 // row groups of a sequence: R / rows, rounded up
