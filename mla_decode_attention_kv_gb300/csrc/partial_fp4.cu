@@ -218,11 +218,11 @@ struct Iter4 {
 // leave the busiest CTA above the even share by more than max(3 tiles, 1/8)),
 // without one a CTA takes the whole units whose first tile lies in its share.
 // Measured over a ragged batch (64 sequences of 512 to 65536 tokens in 16
-// shards) with a unit at 1, 2, 3, 4 and 6 tiles: 16 heads 195, 161, 160, 166
-// and 176 us, 128 heads (units of 64 rows) 648, 573, 478, 460 and 495 us.
+// shards) with a unit at 1, 2, 3 and 4 tiles: 16 heads 162, 146, 152 and 158 us;
+// 128 heads (units of 64 rows) at 2, 3 and 4: 413, 394 and 410 us.
 constexpr int kCostTile = 1;
 template <int N>
-constexpr int kCostUnit = N == 64 ? 4 : 3;
+constexpr int kCostUnit = N == 64 ? 3 : 2;
 
 struct PartScratch {
   unsigned long long scan[32];
