@@ -148,11 +148,18 @@ constexpr float kLess = 1.f - 0x1p-18f, kMore = 1.f + 0x1p-18f;
 // eps 0 stays zeros, and the estimate's square stays in range (a NaN passes).
 constexpr float kLeastMean = 0x1p-120f;
 
+// The larger one, NaN where either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float o;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(o) : "f"(a), "f"(b));
+  return o;
+}
+
 // E4M3 byte of a block's scale, max / (6 kv_scale); NaN where a value is NaN.
 // EXACT: amax is rounded to odd.  Otherwise `same` turns false where amax's
 // error could change the byte.
 template <bool EXACT>
-__device__ __forceinline__ uint32_t block_scale(float amax, bool nan, const AppendParams& ap, bool& same) {
+__device__ __forceinline__ uint32_t block_scale(float amax, const AppendParams& ap, bool& same) {
   uint32_t b;
   if constexpr (EXACT) {
     b = to_e4m3(div_odd(amax, ap.kv6));
@@ -161,7 +168,7 @@ __device__ __forceinline__ uint32_t block_scale(float amax, bool nan, const Appe
     b = to_e4m3(q * kLess);
     same &= b == to_e4m3(q * kMore);
   }
-  return nan ? 0x7Fu : b;
+  return amax != amax ? 0x7Fu : b;
 }
 
 // The signed quotient v / d rounded to odd, 0 (with v's sign) for d = 0.
@@ -225,7 +232,8 @@ __device__ __forceinline__ bool append_row(const AppendParams& ap, int t, int la
   const float co = __ldg(cs + lane), si = __ldg(cs + 32 + lane);
   const int slot = __ldg(ap.slots + t);
 
-  float y[16];   // the row's values (EXACT: rounded to odd)
+  float y[16];       // the row's values: EXACT, rounded to odd; otherwise y * by
+  float by = 1.f;
   bool same = true;
   if (ap.weight) {
     uint32_t ww[8];
@@ -284,12 +292,12 @@ __device__ __forceinline__ bool append_row(const AppendParams& ap, int t, int la
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
       const float mean = fmaf(s, 1.f / 512, ap.eps);
-      const float rs = rsqrtf(mean < kLeastMean ? kLeastMean : mean);
+      by = rsqrtf(mean < kLeastMean ? kLeastMean : mean);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const float2 f = unpack<BF16>(cw[k]), w = unpack<BF16>(ww[k]);
-        y[2 * k] = f.x * w.x * rs;
-        y[2 * k + 1] = f.y * w.y * rs;
+        y[2 * k] = f.x * w.x;
+        y[2 * k + 1] = f.y * w.y;
       }
     }
   } else {
@@ -317,14 +325,12 @@ __device__ __forceinline__ bool append_row(const AppendParams& ap, int t, int la
     float q0 = r0, q1 = r1;
     if constexpr (KIND == kKvE2M1) {
       // latent: the lane's 16 values are one block
-      float am = 0.f;
-      bool nan = false;
+      float am = fabsf(y[0]);
 #pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        am = fmaxf(am, fabsf(y[k]));
-        nan |= y[k] != y[k];
-      }
-      const uint32_t sb = block_scale<EXACT>(am, nan, ap, same);
+      for (int k = 1; k < 16; ++k) am = max_nan(am, fabsf(y[k]));
+      am *= by;
+      const bool nan = am != am;
+      const uint32_t sb = block_scale<EXACT>(am, ap, same);
       const float d = from_e4m3(sb) * ap.kv_scale;
       uint32_t code[2];
       if constexpr (EXACT) {
@@ -334,7 +340,8 @@ __device__ __forceinline__ bool append_row(const AppendParams& ap, int t, int la
         code[0] = to_e2m1x8(q, 1.f);
         code[1] = to_e2m1x8(q + 8, 1.f);
       } else {
-        const float rd = d > 0.f ? __frcp_rn(d) : 0.f;
+        const float rd = d > 0.f ? __frcp_rn(d) * by : 0.f;
+        same &= rd < INFINITY || nan;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           code[k] = to_e2m1x8(y + 8 * k, rd * kLess);
@@ -348,26 +355,23 @@ __device__ __forceinline__ bool append_row(const AppendParams& ap, int t, int la
       // key: a block is 8 lanes' pairs (interleaved) or 16 lanes' first or
       // second values (halves)
       float a0 = fabsf(r0), a1 = fabsf(r1);
-      bool n0 = r0 != r0, n1 = r1 != r1;
-      if (ap.interleaved) {
-        a0 = a1 = fmaxf(a0, a1);
-        n0 = n1 = n0 || n1;
-      }
-#pragma unroll
-      for (int o = 1; o < 16; o <<= 1) {
-        const float x0 = __shfl_xor_sync(0xffffffffu, a0, o), x1 = __shfl_xor_sync(0xffffffffu, a1, o);
-        const int m0 = __shfl_xor_sync(0xffffffffu, static_cast<int>(n0), o);
-        const int m1 = __shfl_xor_sync(0xffffffffu, static_cast<int>(n1), o);
-        if (o < 8 || !ap.interleaved) {
-          a0 = fmaxf(a0, x0);
-          a1 = fmaxf(a1, x1);
-          n0 |= m0 != 0;
-          n1 |= m1 != 0;
-        }
-      }
       // (the key's values are exact in either form, so its codes are taken once)
       bool unused = true;
-      const uint32_t sb0 = block_scale<true>(a0, n0, ap, unused), sb1 = block_scale<true>(a1, n1, ap, unused);
+      uint32_t sb0, sb1;
+      if (ap.interleaved) {
+        a0 = max_nan(a0, a1);
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) a0 = max_nan(a0, __shfl_xor_sync(0xffffffffu, a0, o));
+        sb0 = sb1 = block_scale<true>(a0, ap, unused);
+      } else {
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) {
+          a0 = max_nan(a0, __shfl_xor_sync(0xffffffffu, a0, o));
+          a1 = max_nan(a1, __shfl_xor_sync(0xffffffffu, a1, o));
+        }
+        sb0 = block_scale<true>(a0, ap, unused);
+        sb1 = block_scale<true>(a1, ap, unused);
+      }
       const float d0 = from_e4m3(sb0) * ap.kv_scale, d1 = from_e4m3(sb1) * ap.kv_scale;
       const uint32_t kc = to_e2m1x2(div_signed(r0, d0), div_signed(r1, d1));
       {
@@ -435,10 +439,12 @@ __device__ __forceinline__ bool append_row(const AppendParams& ap, int t, int la
 #pragma unroll
       for (int k = 0; k < 4; ++k) w[k] = to_e4m3x4(q + 4 * k, 1.f);
     } else {
+      const float rd = ap.inv_kv * by;
+      same &= rd < INFINITY || by != by;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        w[k] = to_e4m3x4(y + 4 * k, ap.inv_kv * kLess);
-        same &= w[k] == to_e4m3x4(y + 4 * k, ap.inv_kv * kMore);
+        w[k] = to_e4m3x4(y + 4 * k, rd * kLess);
+        same &= w[k] == to_e4m3x4(y + 4 * k, rd * kMore);
       }
       if (!__all_sync(0xffffffffu, same)) return false;
     }
@@ -536,7 +542,7 @@ __device__ void rotate_queries(const AppendParams& ap, int64_t item, int lane) {
 }  // namespace
 
 template <bool BF16, int KIND>
-__global__ void __launch_bounds__(kAppendThreads, 4) mla_kv_append_kernel(const __grid_constant__ AppendParams ap) {
+__global__ void __launch_bounds__(kAppendThreads, 16) mla_kv_append_kernel(const __grid_constant__ AppendParams ap) {
   const int blk = static_cast<int>(blockIdx.x);
   if (blk < ap.row_blocks) {
     const int t = blk * (kAppendThreads / 32) + (threadIdx.x >> 5);

@@ -15,7 +15,7 @@ constexpr int kE2m1Codes = 288;
 constexpr int kE2m1Scales = 36;
 constexpr int kE2m1Row = kE2m1Codes + kE2m1Scales;
 
-constexpr int kAppendThreads = 256;
+constexpr int kAppendThreads = 64;      // (32 sequences' tokens, 128 heads: 4.0 us, 4.4 with 256)
 constexpr int kQueryHeads = 16;         // heads of one token that a warp rotates
 constexpr int kMaxForkRows = 65536;   // rows of a block table that mla_kv_fork takes
 
