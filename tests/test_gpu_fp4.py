@@ -144,6 +144,26 @@ def test_fp4_growing_scores():
     c.check(*c.run())
 
 
+@pytest.mark.parametrize("H", [1, 5, 24, 32, 64, 100])
+@pytest.mark.parametrize("rise", [3.0, 12.0])
+def test_fp4_growing_scores_of_some_rows(H, rise):
+    """Scores that rise tile after tile, in steps or by jumps, for every third row; the
+    others' stay flat."""
+    c = Fp4([1500], H, shards=1, seed=21, kv_scale=2.0 ** -4)
+    n = len(c.table[0])
+    grow = torch.linspace(0.02, rise, n, device=DEV)
+    grow[n // 3: n // 2] = 0.02                       # a dip between
+    sc = c.pages.view(c.pages.shape[0], -1)[:, 32 * 288:]
+    for j, page in enumerate(c.table[0]):
+        sc[page] = (sc[page].view(torch.float8_e4m3fn).float() * grow[j]).to(torch.float8_e4m3fn).view(torch.uint8)
+    codes, scales = cu.split_pages(c.pages.cpu().numpy())
+    c.hist[0] = cu.e2m1_values(codes[c.table[0]].reshape(-1, 288), scales[c.table[0]].reshape(-1, 36), c.kv_scale)[:1500]
+    along = torch.from_numpy(c.hist[0][-1] / np.abs(c.hist[0][-1]).max() * 3).to(torch.bfloat16).to(DEV)
+    c.q_abs[:, :, ::3] = along[:512]
+    c.q_pe[:, :, ::3] = along[512:]
+    c.check(*c.run())
+
+
 @pytest.mark.parametrize("H", [16, 32, 64, 128])
 def test_fp4_split_and_whole_shards(H):
     """One long shard a sequence, cut between blocks with a workspace, whole without."""
