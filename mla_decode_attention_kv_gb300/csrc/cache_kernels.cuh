@@ -6,6 +6,15 @@
 
 namespace mla {
 
+// Device error codes of the cache operators, after those of ptx.cuh.
+enum CacheError : int {
+  kDevBadSlot = 4,        // slots entry outside [-1, num_blocks * block_size)
+  kDevBadPosition = 5,    // positions entry outside [0, max_pos)
+  kDevBadRow = 6,         // a row id out of range, or a fork into a row that is taken
+  kDevNoFreePage = 7,     // fewer free pages than a fork needs
+  kDevBadRefCount = 8,    // a page given back that no row holds
+};
+
 // Formats of a cached row (mla_kv_format of the header).
 enum KvKind : int { kKvModel = 0, kKvE4M3 = 1, kKvE2M1 = 2 };
 

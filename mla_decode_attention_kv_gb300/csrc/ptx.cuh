@@ -25,11 +25,6 @@ enum DeviceError : int {
   kDevBadBlockId = 1,     // block_table entry outside [0, num_blocks)
   kDevWaitTimeout = 2,    // a pipeline wait exceeded its spin budget
   kDevBadSeqLen = 3,      // seq_lens entry outside [0, max_blocks * block_size]
-  kDevBadSlot = 4,        // slots entry outside [-1, num_blocks * block_size)
-  kDevBadPosition = 5,    // positions entry outside [0, max_pos)
-  kDevBadRow = 6,         // a row id out of range, or a fork into a row that is taken
-  kDevNoFreePage = 7,     // fewer free pages than a fork needs
-  kDevBadRefCount = 8,    // a page given back that no row holds
 };
 
 __device__ __forceinline__ void set_error(int* err, int code) {
