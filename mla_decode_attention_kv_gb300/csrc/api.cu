@@ -622,6 +622,7 @@ int mla_kv_append(const void* c_kv, int64_t c_stride, const void* k_pe, int64_t 
   if (T < 1 || max_pos < 1 || num_blocks < 1 || num_axes < 1 || num_axes > 3 ||
       (q_pe && (H < 1 || H > MLA_MAX_HEADS)))
     return MLA_ERR_BAD_SHAPE;
+  if (mla::append_blocks(T, q_pe ? H : 0) > INT32_MAX) return MLA_ERR_BAD_SHAPE;
   if (norm_weight && (!(eps >= 0.f) || !std::isfinite(eps))) return MLA_ERR_BAD_SHAPE;
   if (!is_block_size(block_size)) return MLA_ERR_BAD_BLOCK;
   if (static_cast<int64_t>(num_blocks) * block_size > INT32_MAX) return MLA_ERR_BAD_SHAPE;

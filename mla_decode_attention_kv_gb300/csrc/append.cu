@@ -573,7 +573,7 @@ static int launch_append_t(const AppendParams& ap, int kind, unsigned blocks, cu
 int launch_append(AppendParams ap, int kind, bool bf16, cudaStream_t stream) {
   ap.row_blocks = ceil_div(ap.T, kAppendThreads / 32);
   ap.q_groups = ap.q_pe ? ceil_div(ap.H, kQueryHeads) : 0;
-  const int64_t blocks = ap.row_blocks + (static_cast<int64_t>(ap.T) * ap.q_groups + kAppendThreads / 32 - 1) / (kAppendThreads / 32);
+  const int64_t blocks = append_blocks(ap.T, ap.q_pe ? ap.H : 0);
   return bf16 ? launch_append_t<true>(ap, kind, static_cast<unsigned>(blocks), stream)
               : launch_append_t<false>(ap, kind, static_cast<unsigned>(blocks), stream);
 }

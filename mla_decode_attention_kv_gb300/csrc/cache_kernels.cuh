@@ -48,6 +48,11 @@ struct AppendParams {
   float inv_kv, inv_kv6;      // their reciprocals, rounded
   int row_blocks, q_groups;   // blocks that make rows; warps per token that rotate queries
 };
+// Blocks of a launch: those that make rows, a warp a token, then those that rotate queries.
+inline int64_t append_blocks(int64_t T, int64_t H) {
+  constexpr int64_t kWarps = kAppendThreads / 32;
+  return (T + kWarps - 1) / kWarps + (T * ((H + kQueryHeads - 1) / kQueryHeads) + kWarps - 1) / kWarps;
+}
 int launch_append(AppendParams ap, int kind, bool bf16, cudaStream_t stream);
 
 // Pages of `page_bytes` in `layers` pools, `*_layer` bytes apart.

@@ -85,9 +85,10 @@ def dcp_decode_step(q_abs, q_pe, kv_cache, block_table, seq_lens, W_UV, num_shar
     that piece (``local_block_table`` builds them from a whole table), split
     into ``num_shards`` shards on this GPU.  H must be a multiple of the group
     size N.  An E4M3 cache (uint8 / float8_e4m3fn bytes, with ``kv_scale``)
-    takes the FP8 partial kernel, as in ``api.mla_dcp_decode_partial``.  Returns this rank's heads [r*H/N, (r+1)*H/N): the output
-    [B*q, (H/N)*128], the combined latent [B*q, H/N, 512] and its LSE
-    [B*q, H/N]."""
+    takes the FP8 partial kernel and one of E2M1 pages the 4-bit one, as in
+    ``api.mla_dcp_decode_partial``.  Returns this rank's heads [r*H/N,
+    (r+1)*H/N): the output [B*q, (H/N)*128], the combined latent
+    [B*q, H/N, 512] and its LSE [B*q, H/N]."""
     world = dist.get_world_size(group)
     rank = dist.get_rank(group)
     H = q_abs.shape[2]

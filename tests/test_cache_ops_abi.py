@@ -37,7 +37,7 @@ def _append(lib, **over):
     (dict(T=0), 2), (dict(H=129), 2), (dict(H=0), 2), (dict(axes=4), 2), (dict(axes=0), 2), (dict(sec=[31]), 2),
     (dict(axes=2, sec=[40, -8]), 2), (dict(mp=0), 2), (dict(eps=-1.0), 2), (dict(eps=float("nan")), 2),
     (dict(scale=0.0), 2), (dict(scale=float("inf")), 2), (dict(scale=float("nan")), 2), (dict(cs=577), 2),
-    (dict(ks=-8), 2), (dict(qh=60), 2), (dict(nb=1 << 28, bs=256), 2), (dict(bs=48), 6), (dict(bs=0), 6),
+    (dict(ks=-8), 2), (dict(qh=60), 2), (dict(nb=1 << 28, bs=256), 2), (dict(T=1 << 30, H=128), 2), (dict(bs=48), 6), (dict(bs=0), 6),
     (dict(c=ODD), 4), (dict(w=ODD), 4), (dict(table=ODD), 4), (dict(kv=ODD), 4),
 ])
 def test_append_host_checks(lib, over, status):
