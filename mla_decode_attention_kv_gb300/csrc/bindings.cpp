@@ -6,7 +6,8 @@
 // Each function takes its arguments by position (api.py gives them names and
 // documents them) and returns the library's status first, then its tensors.
 // Wrong types raise TypeError, wrong shapes, strides and devices ValueError.
-#include <ATen/ops/empty.h>
+#include <ATen/Tensor.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -130,8 +131,9 @@ Stream stream_of(PyObject* o, int dev) {
   return {c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(v), static_cast<c10::DeviceIndex>(dev))};
 }
 
+// (past the dispatcher, which has nothing to choose here)
 at::Tensor make(c10::IntArrayRef shape, at::ScalarType dt, const at::Tensor& like) {
-  return at::empty(shape, at::TensorOptions().dtype(dt).device(like.device()));
+  return at::Tensor(at::detail::empty_cuda(shape, dt, like.device(), std::nullopt));
 }
 
 PyObject* result(int status, std::initializer_list<std::optional<at::Tensor>> out) {
