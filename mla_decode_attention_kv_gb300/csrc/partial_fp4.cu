@@ -385,6 +385,21 @@ __device__ __forceinline__ Range4 partition4(const Fp4Params& fp, PartScratch* p
   return r;
 }
 
+// A CTA for every unit (no unit cut, no more units than CTAs): nothing to share out.
+// (256 tokens, 16 heads: 10.7 us with the partition, 8.3 so.  As a branch of the one
+// kernel it cost the 64-row kernel registers, 2 % of the time of long calls.)
+template <int N>
+__device__ __forceinline__ Range4 single4(const Fp4Params& fp, UnitTable* tab, int cid) {
+  const Unit4 ui = unit4<N>(fp, cid);
+  const int nt = tiles4(ui);
+  if (threadIdx.x == 0) {
+    tab->first = cid;
+    tab->n = 1;
+    tab->u[0] = ui;
+  }
+  return nt > 0 ? Range4{cid, 0, cid, nt} : Range4{0, 0, -1, 0};
+}
+
 // r / d for 0 <= r < 2^13, d <= 128, with inv = 2^32 / d rounded up (0 for d = 1):
 // the product is off by less than 2^-19, and r / d at least 2^-7 below the next integer
 __device__ __forceinline__ int quotient(int r, uint32_t inv) { return inv ? static_cast<int>(__umulhi(r, inv)) : r; }
@@ -574,7 +589,7 @@ __device__ __noinline__ bool current_bad(const uint4* row, int h) {
 }  // namespace
 
 // ---------------------------------------------------------------- the kernel
-template <bool BF16, int N>
+template <bool BF16, int N, bool SHARES>
 __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
     mla_partial_fp4_kernel(const __grid_constant__ CUtensorMap tm_qlat, const __grid_constant__ CUtensorMap tm_qpe,
                            const Fp4Params fp) {
@@ -629,7 +644,9 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
   // merge grid's start this one; each waits for the other to be done)
   griddep_launch_dependents();
   griddep_wait();
-  const Range4 rng = partition4<N, L::kThreads>(fp, reinterpret_cast<PartScratch*>(smem), tab, cid, ncta);
+  Range4 rng;
+  if constexpr (SHARES) rng = partition4<N, L::kThreads>(fp, reinterpret_cast<PartScratch*>(smem), tab, cid, ncta);
+  else rng = single4<N>(fp, tab, cid);
   tc_fence_before();
   __syncthreads();   // barriers, TMEM address, table; the scratch is free
   tc_fence_after();
@@ -1411,13 +1428,13 @@ __global__ void __launch_bounds__(256) mla_partial_fp4_merge_kernel(const Fp4Par
 }
 
 // ---------------------------------------------------------------- launcher
-template <bool BF16, int N>
+template <bool BF16, int N, bool SHARES>
 static bool prepare4(int dev) {
   static bool done[64] = {false};
   static std::mutex mu;
   std::lock_guard<std::mutex> lock(mu);
   if (!done[dev]) {
-    if (cudaFuncSetAttribute(mla_partial_fp4_kernel<BF16, N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(mla_partial_fp4_kernel<BF16, N, SHARES>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              Smem4<N>::kTotal) != cudaSuccess)
       return false;
     done[dev] = true;
@@ -1439,12 +1456,10 @@ int fp4_max_ctas() {
   return cache[dev];
 }
 
-template <bool BF16, int N>
-static int launch4(const CUtensorMap& qlat, const CUtensorMap& qpe, const Fp4Params& fp, cudaStream_t stream) {
+template <bool BF16, int N, bool SHARES>
+static int launch4(const CUtensorMap& qlat, const CUtensorMap& qpe, const Fp4Params& fp, int ctas, cudaStream_t stream) {
   int dev = 0;
-  const int most = fp4_max_ctas();
-  if (most < 1 || cudaGetDevice(&dev) != cudaSuccess || !prepare4<BF16, N>(dev)) return -1;
-  const int ctas = fp.split ? fp.split : std::max(1, std::min(fp.num_units, most));
+  if (cudaGetDevice(&dev) != cudaSuccess || !prepare4<BF16, N, SHARES>(dev)) return -1;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1455,12 +1470,21 @@ static int launch4(const CUtensorMap& qlat, const CUtensorMap& qpe, const Fp4Par
   cfg.gridDim = dim3(ctas, 1, 1);
   cfg.blockDim = dim3(Smem4<N>::kThreads, 1, 1);
   cfg.dynamicSmemBytes = Smem4<N>::kTotal;
-  if (cudaLaunchKernelEx(&cfg, mla_partial_fp4_kernel<BF16, N>, qlat, qpe, fp) != cudaSuccess) return -1;
+  if (cudaLaunchKernelEx(&cfg, mla_partial_fp4_kernel<BF16, N, SHARES>, qlat, qpe, fp) != cudaSuccess) return -1;
   if (!fp.split) return 0;
   cfg.gridDim = dim3(ctas, N / 8, 1);
   cfg.blockDim = dim3(256, 1, 1);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, mla_partial_fp4_merge_kernel, fp, N) != cudaSuccess ? -1 : 0;
+}
+
+template <bool BF16, int N>
+static int launch4(const CUtensorMap& qlat, const CUtensorMap& qpe, const Fp4Params& fp, cudaStream_t stream) {
+  const int most = fp4_max_ctas();
+  if (most < 1) return -1;
+  if (fp.split) return launch4<BF16, N, true>(qlat, qpe, fp, fp.split, stream);
+  return fp.num_units <= most ? launch4<BF16, N, false>(qlat, qpe, fp, fp.num_units, stream)
+                              : launch4<BF16, N, true>(qlat, qpe, fp, most, stream);
 }
 
 int launch_partial_fp4(const CUtensorMap& qlat, const CUtensorMap& qpe, const Fp4Params& fp, int rows,
