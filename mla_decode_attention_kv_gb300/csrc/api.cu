@@ -387,12 +387,13 @@ int mla_dcp_decode_partial_fp4(const void* q_abs, const void* q_pe, const void* 
     if (ctas < 1) return MLA_ERR_CUDA;
     if (workspace_bytes < mla::fp4_workspace_bytes(ctas)) return MLA_ERR_BAD_SHAPE;
   }
-  // Shards that cannot hold more than two tiles are never cut (the kernel cuts
-  // units three tiles and more above the even share), so the call needs no merge:
-  // one launch fewer, and no more CTAs than units.
+  // Shards that are not worth a cut make the call need no merge: those of so few tiles
+  // that a whole one more is within what the kernel leaves uneven, and longer ones
+  // where every unit has a CTA of its own (then there is no partition either).
   const int64_t chunk = static_cast<int64_t>(num_shards) * block_size;
-  const int64_t shard = (tokens + chunk - 1) / chunk * block_size;
-  if (workspace && shard > 128) {
+  const int64_t tiles = ((tokens + chunk - 1) / chunk * block_size + 63) / 64;
+  const bool whole = tiles <= 5 || (tiles <= mla::kWholeTiles4 && fp.num_units <= mla::fp4_max_ctas());
+  if (workspace && !whole) {
     const int ctas = mla::fp4_max_ctas();
     char* w = static_cast<char*>(workspace);
     fp.split = ctas;

@@ -226,14 +226,19 @@ struct Iter4 {
 // Equal shares of cost, as partition_tiles of the 16-bit kernel: a tile costs
 // kCostTile, a unit kCostUnit besides (its first tile's latency, the epilogue).
 // With a workspace the shares are exact (units are cut where whole ones would
-// leave the busiest CTA above the even share by more than max(3 tiles, 1/8)),
-// without one a CTA takes the whole units whose first tile lies in its share.
+// leave the busiest CTA more than kCut4 tiles above the even share), without one a
+// CTA takes the whole units whose first tile lies in its share.
 // Measured over a ragged batch (64 sequences of 512 to 65536 tokens in 16
 // shards) with a unit at 1, 2, 3 and 4 tiles: 16 heads 162, 146, 152 and 158 us;
 // 128 heads (units of 64 rows) at 2, 3 and 4: 413, 394 and 410 us.
 constexpr int kCostTile = 1;
 template <int N>
 constexpr int kCostUnit = N == 64 ? 3 : 2;
+// What a cut costs in tiles, its pieces' ends among it.  (512 units of 8 tiles, 64
+// rows, whole ones 7 above the even share: cut 83 us, whole 80; 64 units of 12 tiles,
+// 16 rows, 8 above: cut 21 us, whole 26.)
+template <int N>
+constexpr int kCut4 = N == 64 ? 8 : 6;
 
 struct PartScratch {
   unsigned long long scan[32];
@@ -325,7 +330,7 @@ __device__ __forceinline__ Range4 partition4(const Fp4Params& fp, PartScratch* p
   bool split = false;
   if (fp.split) {
     const int even = (all_cost + ncta - 1) / ncta;
-    const bool over = tid < ncta && ps->whole[tid + 1] - ps->whole[tid] > even + max(3 * kCostTile, even / 8);
+    const bool over = tid < ncta && ps->whole[tid + 1] - ps->whole[tid] > even + kCut4<N> * kCostTile;
     split = __syncthreads_or(over) != 0;
   }
   const int lo = ps->bound[cid], hi = ps->bound[cid + 1];

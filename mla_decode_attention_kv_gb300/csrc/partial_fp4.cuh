@@ -9,6 +9,12 @@ namespace mla {
 constexpr int kFp4MaxCtas = 256;     // the partition keeps per-CTA state in arrays of this size
 constexpr int kFp4MaxRows = 64;      // query rows of a unit, at most
 
+// Shards of this many tiles or fewer are not cut where each has a CTA of its own: a
+// cut gains their length at most, and costs the partition, a merge and the pieces'
+// own ends (16 heads, 1 to 128 such shards of 8 tiles: whole 16 us, cut 16 to 21; of
+// 12 and 16 tiles 21 and 26 against 17 to 26 and 17 to 31).
+constexpr int kWholeTiles4 = 8;
+
 // Query rows (query token, head) that a unit carries: the smallest of 16, 32
 // and 64 that holds a sequence's rows, 64 where none does.
 inline int fp4_unit_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
