@@ -24,9 +24,9 @@
 // a unit, and several query tokens' rows share one pass over the history.
 // Measured (16 sequences of 131072 tokens): 16 heads 301 us, 2.26 TB/s of pages
 // and 0.33 of the measured copy bandwidth (2750 cycles a tile of 64 tokens), 32
-// heads 315, 64 heads 408, 128 heads 781 us (two units of 64 rows; 0.39 of the
-// time of the matrix units at the measured bf16 rate).  The 16-bit kernel takes
-// 780 us for 128 heads and as much for 16.
+// heads 313, 64 heads 407, 128 heads 778 us (two units of 64 rows; the products
+// alone would take 305 us at the measured bf16 rate).  The 16-bit kernel takes 780
+// us for 128 heads and as much for 16.
 //
 // One persistent CTA per SM, 896 threads:
 //   w0      producer: raw pages (codes, scales) by bulk copies, queries by TMA
@@ -43,7 +43,7 @@
 // tile and three quarters, and one raw tile instead of two; there the way from the
 // weights of a tile over the slots that they free to the scores of the next sets the
 // pace, and a quarter is the shortest step on it (128 heads: halves in a ring of one
-// and a half tiles 836 us, quarters 801, with the ring above 781).  With 16 rows,
+// and a half tiles 836 us, quarters 801, with the ring above 778).  With 16 rows,
 // where shared memory sets it, quarters are 9 % slower.
 //
 // Only a tile with a weight past 2^8 (and the first of a piece) reduces the rows'
