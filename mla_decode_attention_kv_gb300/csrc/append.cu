@@ -547,6 +547,8 @@ __device__ void rotate_queries(const AppendParams& ap, int64_t item, int lane) {
 
 template <bool BF16, int KIND>
 __global__ void __launch_bounds__(kAppendThreads, 16) mla_kv_append_kernel(const __grid_constant__ AppendParams ap) {
+  griddep_launch_dependents();
+  griddep_wait();
   const int blk = static_cast<int>(blockIdx.x);
   if (blk < ap.row_blocks) {
     const int t = blk * (kAppendThreads / 32) + (threadIdx.x >> 5);
@@ -563,11 +565,10 @@ __global__ void __launch_bounds__(kAppendThreads, 16) mla_kv_append_kernel(const
 
 template <bool BF16>
 static int launch_append_t(const AppendParams& ap, int kind, unsigned blocks, cudaStream_t stream) {
-  switch (kind) {
-    case kKvModel: mla_kv_append_kernel<BF16, kKvModel><<<blocks, kAppendThreads, 0, stream>>>(ap); return 0;
-    case kKvE4M3: mla_kv_append_kernel<BF16, kKvE4M3><<<blocks, kAppendThreads, 0, stream>>>(ap); return 0;
-    default: mla_kv_append_kernel<BF16, kKvE2M1><<<blocks, kAppendThreads, 0, stream>>>(ap); return 0;
-  }
+  auto* kernel = kind == kKvModel  ? mla_kv_append_kernel<BF16, kKvModel>
+                 : kind == kKvE4M3 ? mla_kv_append_kernel<BF16, kKvE4M3>
+                                   : mla_kv_append_kernel<BF16, kKvE2M1>;
+  return launch_overlapped(kernel, dim3(blocks), kAppendThreads, stream, ap) == cudaSuccess ? 0 : -1;
 }
 
 int launch_append(AppendParams ap, int kind, bool bf16, cudaStream_t stream) {

@@ -41,6 +41,8 @@ __device__ __forceinline__ void copy_chunk(const char* src, char* dst, uint64_t 
 
 // ---------------------------------------------------------------- copy
 __global__ void __launch_bounds__(kCopyThreads) mla_copy_pages_kernel(const CopyParams cp) {
+  griddep_launch_dependents();
+  griddep_wait();
   const int i = blockIdx.x / cp.chunks, chunk = blockIdx.x - i * cp.chunks;
   const int a = __ldg(cp.src_ids + i), b = __ldg(cp.dst_ids + i);
   if (a < 0 || a >= cp.src_blocks || b < 0 || b >= cp.dst_blocks) {
@@ -53,8 +55,8 @@ __global__ void __launch_bounds__(kCopyThreads) mla_copy_pages_kernel(const Copy
 
 int launch_copy_pages(CopyParams cp, cudaStream_t stream) {
   cp.chunks = static_cast<int>((cp.page_bytes + kCopyChunk - 1) / kCopyChunk);
-  mla_copy_pages_kernel<<<dim3(static_cast<unsigned>(cp.n) * cp.chunks, cp.layers), kCopyThreads, 0, stream>>>(cp);
-  return 0;
+  const dim3 grid(static_cast<unsigned>(cp.n) * cp.chunks, cp.layers);
+  return launch_overlapped(mla_copy_pages_kernel, grid, kCopyThreads, stream, cp) == cudaSuccess ? 0 : -1;
 }
 
 // ---------------------------------------------------------------- free
@@ -62,7 +64,8 @@ int launch_copy_pages(CopyParams cp, cudaStream_t stream) {
 // first thread, so a row named twice is given back once.
 __global__ void __launch_bounds__(256) mla_kv_free_kernel(const FreeParams fp) {
   __shared__ int s_pages;
-  griddep_launch_dependents();   // (a fork behind it starts meanwhile, and waits)
+  griddep_launch_dependents();
+  griddep_wait();
   const int r = __ldg(fp.rows + blockIdx.x);
   if (r < 0 || r >= fp.num_rows) {
     if (threadIdx.x == 0) set_error(fp.err, kDevBadRow);
@@ -92,8 +95,7 @@ __global__ void __launch_bounds__(256) mla_kv_free_kernel(const FreeParams fp) {
 }
 
 int launch_free(const FreeParams& fp, cudaStream_t stream) {
-  mla_kv_free_kernel<<<fp.n, 256, 0, stream>>>(fp);
-  return 0;
+  return launch_overlapped(mla_kv_free_kernel, dim3(fp.n), 256, stream, fp) == cudaSuccess ? 0 : -1;
 }
 
 // ---------------------------------------------------------------- fork
@@ -217,6 +219,7 @@ __global__ void __launch_bounds__(kPlanThreads) mla_kv_fork_plan_kernel(const Fo
 }
 
 __global__ void __launch_bounds__(kCopyThreads) mla_kv_fork_apply_kernel(const ForkParams fp) {
+  griddep_launch_dependents();
   griddep_wait();   // the plan is complete
   if (fp.ws[0] == 0) return;
   const int per = fp.layers * fp.chunks + 1;
@@ -257,20 +260,8 @@ __global__ void __launch_bounds__(kCopyThreads) mla_kv_fork_apply_kernel(const F
 int launch_fork(ForkParams fp, cudaStream_t stream) {
   fp.chunks = static_cast<int>((fp.page_bytes + kCopyChunk - 1) / kCopyChunk);
   const unsigned blocks = static_cast<unsigned>(fp.n) * (fp.layers * fp.chunks + 1);
-  // programmatic launches: a grid's start overlaps the one before, for which it waits
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  cfg.stream = stream;
-  cfg.gridDim = dim3(1);
-  cfg.blockDim = dim3(kPlanThreads);
-  if (cudaLaunchKernelEx(&cfg, mla_kv_fork_plan_kernel, fp) != cudaSuccess) return -1;
-  cfg.gridDim = dim3(blocks);
-  cfg.blockDim = dim3(kCopyThreads);
-  return cudaLaunchKernelEx(&cfg, mla_kv_fork_apply_kernel, fp) != cudaSuccess ? -1 : 0;
+  if (launch_overlapped(mla_kv_fork_plan_kernel, dim3(1), kPlanThreads, stream, fp) != cudaSuccess) return -1;
+  return launch_overlapped(mla_kv_fork_apply_kernel, dim3(blocks), kCopyThreads, stream, fp) == cudaSuccess ? 0 : -1;
 }
 
 }  // namespace mla
