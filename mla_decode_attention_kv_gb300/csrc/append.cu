@@ -23,10 +23,10 @@
 // which rounds on to fewer bits the same way as hi + lo itself.  16-bit rows
 // are always made the exact way.
 //
-// What bounds it: the launch for few tokens (one token 2.6 us, 32 tokens of 128
-// heads into E2M1 2.7, or 4.1 where a row needs the exact form); for many the row
-// arithmetic, some 700 instructions a token (8192 tokens of 16 heads into E2M1: 13.6
-// us, of which the rows alone 9.8; 57 MB at 4.2 TB/s, 0.62 of the measured copy
+// What bounds it: the launch for few tokens (one token 2.1 us, 32 tokens of 128
+// heads into E2M1 2.5, or 3.6 where a row needs the exact form); for many the row
+// arithmetic, some 700 instructions a token (8192 tokens of 16 heads into E2M1: 13.1
+// us, of which the rows alone 9.8; 57 MB at 4.4 TB/s, 0.65 of the measured copy
 // bandwidth).  With half the blocks on an SM the time is the same, with smaller
 // register budgets 17 and 22 us.  One warp makes a token's row:
 // lane l owns latents 16 l .. 16 l + 15, which are one block of the E2M1 form,

@@ -239,3 +239,42 @@ def test_page_refusals():
         api.mla_kv_copy_pages(p.cache, p.cache[:1], p.ids([0]), p.ids([1]))
     p.fork([], [])
     p.same()
+
+
+def test_calls_in_a_row_see_each_others_writes():
+    """Append, copy, append, fork and free back to back, each launched while the one
+    before runs: the same bytes as with a wait after every call."""
+    T, bs, layers = 40, 16, 1
+    g = torch.Generator(device=DEV).manual_seed(5)
+    kv = torch.randn(30, T, 576, generator=g, device=DEV).to(torch.bfloat16)
+    cs = torch.randn(64, 64, generator=g, device=DEV)
+    pos = torch.randint(0, 64, (T,), generator=g, device=DEV).int()
+    ids = lambda *x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+    src, dst, p0, p1 = ids(0, 1, 2), ids(8, 9, 10), ids(0), ids(1)
+
+    def run(wait):
+        sync = torch.cuda.synchronize if wait else lambda: None
+        pool = torch.zeros(layers, 14, bs, 324, dtype=torch.uint8, device=DEV)
+        table = torch.full((2, 4), -1, dtype=torch.int32, device=DEV)
+        table[0, :3] = ids(8, 9, 10)
+        lens, refs, err = ids(T, 0), torch.zeros(14, dtype=torch.int32, device=DEV), ids(0)
+        refs[8:11] = 1
+        refs[:3] = 1
+        slots, seen = torch.arange(T, device=DEV).int(), []
+        torch.cuda.synchronize()
+        for k in range(30):
+            api.mla_kv_append(kv[k][:, :512], kv[k][:, 512:], pool[0], slots, pos, cs, kv_scale=0.25, err_flag=err)
+            sync()
+            api.mla_kv_copy_pages(pool, pool, src, dst, err_flag=err)
+            sync()
+            api.mla_kv_fork(pool, table, lens, refs, p0, p1, err_flag=err)
+            sync()
+            seen.append((pool.clone(), table.clone(), refs.clone()))
+            api.mla_kv_free(table, lens, refs, p1, block_size=bs, err_flag=err)
+            sync()
+        torch.cuda.synchronize()
+        assert err.item() == 0
+        return seen
+
+    for a, b in zip(run(False), run(True)):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
