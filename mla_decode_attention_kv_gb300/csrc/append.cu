@@ -11,12 +11,13 @@
 // axes (time, height, width) a pair reads the row of its section's position.
 //
 // What is stored in 8 or 4 bits is the nearest code of the value itself.  A
-// value computed in plain fp32 is off by up to 2^-19 (the sum of squares) and
-// lands, once in a few million values, on the wrong side of a border between
+// value computed in plain fp32 is off by up to 2^-20 (in halves of a last bit: the
+// sum of squares 15, halved by the root, rsqrtf 4, its products with the value and
+// the scale 4) and lands, once in a few million values, on the wrong side of a border between
 // two 4-bit codes that lie a third of their size apart; the cache would then
 // depend on the order of a sum.  So a row is made twice over: in fp32, where
-// each code is taken at a little less and a little more (2^-18) than the value,
-// and, where some code of the row differs (a row in some 200 for E2M1, in 15
+// each code is taken at a little less and a little more (2^-19) than the value,
+// and, where some code of the row differs (a row in some 400 for E2M1, in 30
 // for E4M3), again exactly: values as unevaluated sums hi + lo of two fp32
 // numbers (sums and products with their exact errors, Dekker and Knuth), about
 // 2^-46 off, rounded with lo folded into the last bit of hi (round to odd),
@@ -24,11 +25,11 @@
 // are always made the exact way.
 //
 // What bounds it: the launch for few tokens (one token 2.1 us, 32 tokens of 128
-// heads into E2M1 2.5, or 3.6 where a row needs the exact form); for many the row
-// arithmetic, some 700 instructions a token (8192 tokens of 16 heads into E2M1: 13.1
-// us, of which the rows alone 9.8; 57 MB at 4.4 TB/s, 0.65 of the measured copy
-// bandwidth).  With half the blocks on an SM the time is the same, with smaller
-// register budgets 17 and 22 us.  One warp makes a token's row:
+// heads into E2M1 3.6, 1.3 of them where a row needs the exact form); for many the
+// row arithmetic (8192 tokens of 16 heads into E2M1: 13.1 us, of which the rows
+// alone 9.8; 57 MB at 4.4 TB/s, 0.65 of the measured copy bandwidth).  With half the
+// blocks on an SM the time is the same, with smaller register budgets 17 and 22 us.
+// One warp makes a token's row:
 // lane l owns latents 16 l .. 16 l + 15, which are one block of the E2M1 form,
 // so a block's maximum and its 8 bytes of codes stay in a lane; the key's pair
 // l belongs to lane l.  The queries go to blocks of their own, eight lanes a
@@ -146,7 +147,7 @@ __device__ __forceinline__ uint32_t to_e2m1x2(float x, float y) {   // x in the 
 }
 
 // A little less and a little more than a value: the bounds of its fp32 error.
-constexpr float kLess = 1.f - 0x1p-18f, kMore = 1.f + 0x1p-18f;
+constexpr float kLess = 1.f - 0x1p-19f, kMore = 1.f + 0x1p-19f;
 
 // The mean square plus eps counts as at least this, so that a row of zeros with
 // eps 0 stays zeros, and the estimate's square stays in range (a NaN passes).
