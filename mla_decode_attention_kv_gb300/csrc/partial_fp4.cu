@@ -241,7 +241,7 @@ template <int N>
 constexpr int kCut4 = N == 64 ? 8 : 6;
 
 struct PartScratch {
-  unsigned long long scan[32];
+  int2 scan[32];
   int4 pre[1024];                  // of each thread's units: tiles and cost before, tiles of the first
   int bound[kFp4MaxCtas + 1];      // first tile of each CTA's share
   int whole[kFp4MaxCtas + 1];      // cost before the first unit that starts at or behind it
@@ -272,25 +272,23 @@ __device__ __forceinline__ Range4 partition4(const Fp4Params& fp, PartScratch* p
       cost += cost_of(nt);
     }
   }
-  const unsigned long long own = (static_cast<unsigned long long>(cost) << 32) | static_cast<unsigned>(cnt);
-  unsigned long long incl = own, before = 0, all = 0;
+  int incl_t = cnt, incl_c = cost;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const unsigned long long y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
+    const int y = __shfl_up_sync(0xffffffffu, incl_t, o), z = __shfl_up_sync(0xffffffffu, incl_c, o);
+    if (lane >= o) {
+      incl_t += y;
+      incl_c += z;
+    }
   }
-  if (lane == 31) ps->scan[warp] = incl;
+  if (lane == 31) ps->scan[warp] = make_int2(incl_t, incl_c);
   if (tid == 0) ps->rng = {0, 0, -1, 0};
   __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    const unsigned long long x = ps->scan[w];
-    before += w < warp ? x : 0;
-    all += x;
-  }
-  before += incl - own;
-  ps->pre[tid] = make_int4(static_cast<int>(before & 0xffffffffu), static_cast<int>(before >> 32), ntiles, 0);
-  const int total = static_cast<int>(all & 0xffffffffu), all_cost = static_cast<int>(all >> 32);
+  // (the warps' sums by reductions: as a loop in every warp 1 us of a call)
+  const int2 sums = lane < kWarps ? ps->scan[lane] : make_int2(0, 0);
+  const int total = __reduce_add_sync(0xffffffffu, sums.x), all_cost = __reduce_add_sync(0xffffffffu, sums.y);
+  ps->pre[tid] = make_int4(__reduce_add_sync(0xffffffffu, lane < warp ? sums.x : 0) + incl_t - cnt,
+                           __reduce_add_sync(0xffffffffu, lane < warp ? sums.y : 0) + incl_c - cost, ntiles, 0);
   if (total == 0) {
     if (fp.split && tid == 0) {
       fp.ws_units[cid] = make_int4(-1, 0, 0, 0);
@@ -976,16 +974,17 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
         pk[k / 2] = pack2<BF16>(x[k], x[k + 1]);
       }
     };
-    while (it.valid) {
-      const Unit4 ui = it.ui;
+    // One tile: the first and the last of its piece, with `left` tokens of the unit from
+    // its first on.  False: given up (the barriers of a group agree on it).
+    auto tile = [&](const Unit4& ui, bool first, bool last, int left) {
       const int sb = g & 1;
-      const bool cur = ui.p == fp.S, first = it.first();
+      const bool cur = ui.p == fp.S;
       const float sl = cur ? fp.scale_log2 : fp.scale_log2 * fp.kv_scale;
       // rows below nmin are masked for this thread's token: all of a token past
       // the end; in the CURRENT part the rows of earlier query tokens
       int nmin = N;
-      if (it.tok0() + tok < ui.hi) nmin = cur ? min(N, max(0, tok * fp.H - ui.g * N)) : 0;
-      const bool all = !cur && it.tok0() + kTile4 <= ui.hi;
+      if (tok < left) nmin = cur ? min(N, max(0, tok * fp.H - ui.g * N)) : 0;
+      const bool all = !cur && left >= kTile4;
       // P's place is as a rule free before the scores are there: waited for first, it is
       // off the path from the scores to the weights (16 rows 307 -> 304 us, 64 rows 862
       // -> 838 us; with 32 rows it is the other way round, 324 -> 343 us)
@@ -1003,7 +1002,7 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
           const float mx = col_reduce<NC, true>(x, lane);
           red_of(q)[wq * NG + cr] = mx;
         }
-        if (!named_bar_and(barid, 128, ok)) break;
+        if (!named_bar_and(barid, 128, ok)) return false;
         if (wq == 0 && lane < NG * PASSES) {
           const float* r = red_of(0) + (lane / NG) * (4 * NG) + lane % NG;
           const float t = fmaxf(fmaxf(r[0], r[NG]), fmaxf(r[2 * NG], r[3 * NG]));
@@ -1065,7 +1064,7 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
         const int mine = flags[(g % 3) * 2 + grp], other = flags[(g % 3) * 2 + (grp ^ 1)];
         if (mine | other) {
           if (mine) {
-            if (!named_bar_and(barid, 128, ok)) break;
+            if (!named_bar_and(barid, 128, ok)) return false;
 #pragma unroll
             for (int q = 0; q < PASSES; ++q) {
               float x[NC];
@@ -1088,7 +1087,7 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar[L::B_S_EMPTY + sb]);
-      if (it.last()) {
+      if (last) {
         // ---- epilogue of the piece: row sums over the tokens, O / l, LSE.  The sums,
         // factors and places are worked out while the last PV product runs.
         const bool whole = it.whole();
@@ -1099,7 +1098,7 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
           const float part = col_reduce<NC, false>(l[q], lane);
           red_of(q)[N * 4 + wq * NG + cr] = part;
         }
-        if (!named_bar_and(barid, 128, ok)) break;
+        if (!named_bar_and(barid, 128, ok)) return false;
         // row `lane` of the group's, in every warp: its sum, its factor and where it goes (-1: nowhere)
         constexpr int NR = NG * PASSES;
         float inv = 0.f;
@@ -1223,8 +1222,25 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
           tc_fence_before();
         }
       }
-      it.advance(fp);
-      ++g;
+      return true;
+    };
+    // 64 rows: a piece at a time, so that little lives along its tiles (128 heads 778 ->
+    // 766 us); fewer rows, where all of it fits the registers: tile by tile (16 heads 313
+    // -> 300 us)
+    if constexpr (N == 64) {
+      bool go = true;
+      while (go && it.valid) {
+        const Unit4 ui = it.ui;
+        int n = it.jend - it.j, left = ui.hi - it.tok0();
+#pragma unroll 1
+        for (bool first = true; go && n > 0; --n, ++g, left -= kTile4, first = false) go = tile(ui, first, n == 1, left);
+        it.next_piece(fp);
+      }
+    } else {
+      while (it.valid && tile(it.ui, it.first(), it.last(), it.ui.hi - it.tok0())) {
+        it.advance(fp);
+        ++g;
+      }
     }
   } else {
     // ------------------------------------------------ unpacking
