@@ -26,7 +26,7 @@
 //
 // What bounds it: the launch for few tokens (one token 2.1 us, 32 tokens of 128
 // heads into E2M1 3.6, 1.3 of them where a row needs the exact form); for many the
-// row arithmetic (8192 tokens of 16 heads into E2M1: 13.1 us, of which the rows
+// row arithmetic (8192 tokens of 16 heads into E2M1: 13.0 us, of which the rows
 // alone 9.8; 57 MB at 4.4 TB/s, 0.65 of the measured copy bandwidth).  With half the
 // blocks on an SM the time is the same, with smaller register budgets 17 and 22 us.
 // One warp makes a token's row:

@@ -18,15 +18,15 @@
 //   O^T += V^T P^T  A = the same tile read MN-major [latent x 64 tokens],
 //                   B = P^T [64 tokens x rows] (MN-major)
 // The tokens and the latents fill the MMAs' M, the rows (query tokens x heads
-// of one sequence, 16, 32 or 64 a unit) are N: 16 heads cost a quarter of 64,
+// of one sequence, 16, 32 or 64 a unit) are N, so that few heads cost less,
 // where M = heads would cost the same for any number.  O^T [512 x rows] is 4
 // x rows columns of tensor memory, at most half of it, so one CTA holds all of
 // a unit, and several query tokens' rows share one pass over the history.
-// Measured (16 sequences of 131072 tokens): 16 heads 301 us, 2.26 TB/s of pages
-// and 0.33 of the measured copy bandwidth (2750 cycles a tile of 64 tokens), 32
-// heads 313, 64 heads 407, 128 heads 778 us (two units of 64 rows; the products
+// Measured (16 sequences of 131072 tokens): 16 heads 297 us, 2.29 TB/s of pages
+// and 0.34 of the measured copy bandwidth (2700 cycles a tile of 64 tokens), 32
+// heads 312, 64 heads 401, 128 heads 765 us (two units of 64 rows; the products
 // alone would take 305 us at the measured bf16 rate).  The 16-bit kernel takes 780
-// us for 128 heads and as much for 16.
+// us for 128 heads.
 //
 // One persistent CTA per SM, 896 threads:
 //   w0      producer: raw pages (codes, scales) by bulk copies, queries by TMA
@@ -43,7 +43,7 @@
 // tile and three quarters, and one raw tile instead of two; there the way from the
 // weights of a tile over the slots that they free to the scores of the next sets the
 // pace, and a quarter is the shortest step on it (128 heads: halves in a ring of one
-// and a half tiles 836 us, quarters 801, with the ring above 778).  With 16 rows,
+// and a half tiles 836 us, quarters 801, with the ring above 785 at that step).  With 16 rows,
 // where shared memory sets it, quarters are 9 % slower.
 //
 // Only a tile with a weight past 2^8 (and the first of a piece) reduces the rows'
@@ -229,7 +229,7 @@ struct Iter4 {
 // leave the busiest CTA more than kCut4 tiles above the even share), without one a
 // CTA takes the whole units whose first tile lies in its share.
 // Measured over a ragged batch (64 sequences of 512 to 65536 tokens in 16
-// shards) with a unit at 1, 2, 3 and 4 tiles: 16 heads 162, 146, 152 and 158 us;
+// shards) with a unit at 1, 2, 3 and 4 tiles: 16 heads 162, 146, 152 and 158 us,
 // 128 heads (units of 64 rows) at 2, 3 and 4: 413, 394 and 410 us.
 constexpr int kCostTile = 1;
 template <int N>
