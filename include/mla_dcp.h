@@ -249,6 +249,9 @@ int mla_dcp_decode_partial_fp8(const void* q_abs, const void* q_pe, const void* 
  *              latent that is not finite makes them NaN)
  *   kv_scale   > 0 and finite (scale * kv_scale too); MLA_ERR_BAD_SHAPE otherwise
  *   workspace  of mla_dcp_decode_partial_fp4_workspace_size bytes, or NULL
+ *   sizes      (max_blocks + num_shards) * block_size, and the tiles of 64 tokens
+ *              of all sequences and groups of 64 rows (query tokens x heads), each
+ *              below about 2^30; MLA_ERR_BAD_SHAPE otherwise
  * Precision: every code * s is a value of either 16-bit type, so the tensor
  * cores multiply the cache as it is stored by the query as it is given; the
  * softmax weights are rounded to in_dtype before the PV product, as in the
@@ -454,6 +457,7 @@ int mla_gather_kv(const void* kv_cache, const int32_t* block_table, const int32_
  *             MLA_KV_E2M1; E4M3 bytes for MLA_KV_E4M3.  Every token has a row,
  *             stored or not.
  * Positions and slots out of range set MLA_DEV_BAD_POSITION / MLA_DEV_BAD_SLOT.
+ * T (1 + H / 16) is at most about 2^31 (MLA_ERR_BAD_SHAPE).
  */
 int mla_kv_append(const void* c_kv, int64_t c_stride, const void* k_pe, int64_t k_stride,
                   const void* norm_weight, float eps, const void* q_pe, int64_t q_stride,

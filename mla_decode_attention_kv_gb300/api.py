@@ -98,7 +98,7 @@ def mla_dcp_decode_partial(q_abs, q_pe, kv_cache, block_table, seq_lens, num_sha
     [N, B*q, P, H/N] (mla_dcp_decode_partial_sliced: block n is what rank n
     receives in a head-scattered all-to-all).
     workspace: "default" (one kept per device and stream, see
-    partial_workspace), a uint8 CUDA tensor of at least
+    partial_workspace; over E2M1 pages a captured call gets its own), a uint8 CUDA tensor of at least
     mla_dcp_decode_partial_workspace_size bytes, or None (pairs of CTAs then
     take whole shards)."""
     if is_fp4_cache(kv_cache):
