@@ -348,13 +348,13 @@ def _fork(s):
     c = s["case"]
     bs = c["block_size"]
     table, lens, refs, pool = s["table"], s["lens"], s["refs"], s["pool"]
+    kids, parents = s["children"].long(), s["parents"].long()
     if own:
         from mla_decode_attention_kv_gb300 import api
         api.mla_kv_free(table, lens, refs, s["children"], block_size=bs, err_flag=s["err"])
         api.mla_kv_fork(pool, table, lens, refs, s["parents"], s["children"], err_flag=s["err"])
         return {"table": table, "lens": lens, "refs": refs, "pool": pool}
     # give back what the forked rows hold
-    kids, parents = s["children"].long(), s["parents"].long()
     col = torch.arange(table.shape[1], device=table.device)
     held = col < (-(-lens[kids] // bs))[:, None]
     refs.scatter_add_(0, table[kids].clamp(min=0).long().flatten(), -held.int().flatten())
