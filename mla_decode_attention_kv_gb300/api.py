@@ -80,6 +80,18 @@ def is_fp4_cache(kv_cache) -> bool:
     return kv_cache.dtype == torch.uint8 and kv_cache.shape[-1] == E2M1_ROW
 
 
+def _need_rows(kv_cache, dtype: Optional[torch.dtype], size: int = 2):
+    """kv_cache has rows of 576 values of `size` bytes (16-bit ones in `dtype`, or raw
+    words): a call over such rows would read a pool of another format, E2M1 pages for
+    one, past its end."""
+    if kv_cache.element_size() != size or (
+            dtype is not None and kv_cache.is_floating_point() and kv_cache.dtype != dtype):
+        raise TypeError(f"kv_cache of {kv_cache.dtype} in a call over rows of "
+                        f"{dtype or f'{8 * size}-bit values'}")
+    if kv_cache.dim() != 3 or kv_cache.shape[-1] != D_QK:
+        raise ValueError(f"kv_cache must be [num_blocks, block_size, {D_QK}], not {list(kv_cache.shape)}")
+
+
 def mla_dcp_decode_partial(q_abs, q_pe, kv_cache, block_table, seq_lens, num_shards: int, *,
                            kv_cur=None, scale: float = DEFAULT_SCALE, part_dtype=None,
                            o_part=None, lse_part=None, err_flag=None, stream=None,
@@ -105,6 +117,8 @@ def mla_dcp_decode_partial(q_abs, q_pe, kv_cache, block_table, seq_lens, num_sha
         return _partial_fp4(q_abs, q_pe, kv_cache, block_table, seq_lens, num_shards, kv_cur, scale,
                             part_dtype, o_part, lse_part, err_flag, stream, workspace, head_slices,
                             1.0 if kv_scale is None else kv_scale)
+    fp8 = is_fp8_cache(kv_cache)
+    _need_rows(kv_cache, None if fp8 else q_abs.dtype, 1 if fp8 else 2)
     B, q_len, H, _ = q_abs.shape
     num_blocks, bs, _ = kv_cache.shape
     P = num_shards + (1 if kv_cur is not None else 0)
@@ -128,7 +142,7 @@ def mla_dcp_decode_partial(q_abs, q_pe, kv_cache, block_table, seq_lens, num_sha
         workspace = partial_workspace(q_abs.device, B, q_len, num_shards, kv_cur is not None,
                                       stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    if is_fp8_cache(kv_cache):
+    if fp8:
         if kv_cur is not None and not is_fp8_cache(kv_cur):
             raise TypeError("kv_cur must be E4M3 bytes like kv_cache")
         st = _ffi.lib().mla_dcp_decode_partial_fp8(
@@ -178,7 +192,9 @@ def mla_dcp_decode_partial_noalloc(q_abs, q_pe, kv_cache, block_table, seq_lens,
     """mla_dcp_decode_partial with the library's fixed scratch array instead of
     a workspace: allocates nothing (o_part / lse_part are required), for
     callers that cannot lend the library device memory.  Calls that may
-    overlap in time share that array and must be serialised."""
+    overlap in time share that array and must be serialised.  kv_cache is in the
+    dtype of q_abs (no E4M3 or E2M1 cache)."""
+    _need_rows(kv_cache, q_abs.dtype)
     B, q_len, H, _ = q_abs.shape
     num_blocks, bs, _ = kv_cache.shape
     for t, n in ((q_abs, "q_abs"), (q_pe, "q_pe"), (kv_cache, "kv_cache"),
@@ -253,11 +269,18 @@ def mla_lse_combine_vup(o_part, lse_part, W_UV, *, o_local=None, lse_local=None,
 
 def mla_gather_kv(kv_cache, block_table, seq_lens, max_len: int, *, dst=None, err_flag=None,
                   stream=None):
-    """dst [B, max_len, 576]: each sequence's paged history, bit-exact."""
+    """dst [B, max_len, 576]: each sequence's paged history, bit-exact, of a 16-bit
+    cache (dst in its dtype)."""
+    _need_rows(kv_cache, None)
     B = block_table.shape[0]
     num_blocks, bs, _ = kv_cache.shape
     if dst is None:
         dst = torch.empty((B, max_len, D_QK), dtype=kv_cache.dtype, device=kv_cache.device)
+    elif dst.element_size() != 2 or dst.numel() < B * max_len * D_QK:
+        raise ValueError(f"dst must hold [{B}, {max_len}, {D_QK}] values of 16 bits")
+    for t, n in ((kv_cache, "kv_cache"), (block_table, "block_table"), (seq_lens, "seq_lens"),
+                 (dst, "dst")):
+        _need(t, n)
     st = _ffi.lib().mla_gather_kv(_p(kv_cache), _p(block_table), _p(seq_lens), B, num_blocks, bs,
                                   block_table.shape[1], max_len, _p(dst), _p(err_flag),
                                   _s(stream))
