@@ -1,8 +1,9 @@
 """Python binding of the C ABI (include/mla_dcp.h) for torch CUDA tensors.
 
 Argument marshalling only: every call checks shapes, allocates outputs the
-caller did not pass (torch owns device memory), and hands raw pointers to the
-CUDA library on the current (or given) stream.  No arithmetic of the method
+caller did not pass (torch owns device memory; they belong to the stream that
+the call runs on), and hands raw pointers to the CUDA library on the current (or
+given) stream.  No arithmetic of the method
 happens here and there is no fallback path.
 """
 from __future__ import annotations
@@ -44,6 +45,29 @@ def _need(t: torch.Tensor, name: str):
         raise ValueError(f"{name} must be a contiguous CUDA tensor")
 
 
+def torch_stream(stream, device) -> torch.cuda.Stream:
+    """`stream` (anything with a cuda_stream handle) as a stream of torch."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(stream.cuda_stream, device)
+
+
+def _empty(shape, dtype, device, stream):
+    """A new tensor that a call on `stream` (None: the current one) writes.  Its memory is
+    ordered by that stream's work: a block of the current stream could be one that it has
+    given up but still works on.  Marked as used by the current stream as well, where a
+    caller goes on with it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    if stream.cuda_stream == current.cuda_stream:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(torch_stream(stream, device)):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(current)
+    return t
+
+
 _WORKSPACES = {}
 
 
@@ -65,7 +89,7 @@ def partial_workspace(device, B: int, q_len: int, num_shards: int, has_current: 
     key = (device.index, s.cuda_stream)
     ws = _WORKSPACES.get(key)
     if ws is None or ws.numel() < need:
-        ws = torch.empty(need, dtype=torch.uint8, device=device)
+        ws = _empty(need, torch.uint8, device, s)
         _WORKSPACES[key] = ws
     return ws
 
@@ -133,9 +157,9 @@ def mla_dcp_decode_partial(q_abs, q_pe, kv_cache, block_table, seq_lens, num_sha
         o_shape = (head_slices, B * q_len, P, hs, D_LATENT)
         l_shape = (head_slices, B * q_len, P, hs)
     if o_part is None:
-        o_part = torch.empty(o_shape, dtype=part_dtype, device=q_abs.device)
+        o_part = _empty(o_shape, part_dtype, q_abs.device, stream)
     if lse_part is None:
-        lse_part = torch.empty(l_shape, dtype=torch.float32, device=q_abs.device)
+        lse_part = _empty(l_shape, torch.float32, q_abs.device, stream)
     if isinstance(workspace, str):
         if workspace != "default":
             raise ValueError("workspace must be 'default', a tensor or None")
@@ -176,9 +200,9 @@ def mla_dcp_combine_exchanged(o_recv, lse_recv, *, hist_parts: int, local_src: i
     _need(lse_recv, "lse_recv")
     out_dtype = out_dtype or o_recv.dtype
     if o_latent is None:
-        o_latent = torch.empty((T, Hs, D_LATENT), dtype=out_dtype, device=o_recv.device)
+        o_latent = _empty((T, Hs, D_LATENT), out_dtype, o_recv.device, stream)
     if lse_out is None:
-        lse_out = torch.empty((T, Hs), dtype=torch.float32, device=o_recv.device)
+        lse_out = _empty((T, Hs), torch.float32, o_recv.device, stream)
     st = _ffi.lib().mla_dcp_combine_exchanged(
         _p(o_recv), _p(lse_recv), N, P, int(hist_parts), int(local_src), T, Hs,
         _code(o_recv.dtype), _code(o_latent.dtype), _p(o_latent), _p(lse_out), _s(stream))
@@ -226,9 +250,9 @@ def mla_lse_combine(o_part, lse_part, *, o_local=None, lse_local=None, out_dtype
     _need(lse_part, "lse_part")
     out_dtype = out_dtype or o_part.dtype
     if o_latent is None:
-        o_latent = torch.empty((T, H, D_LATENT), dtype=out_dtype, device=o_part.device)
+        o_latent = _empty((T, H, D_LATENT), out_dtype, o_part.device, stream)
     if lse_out is None:
-        lse_out = torch.empty((T, H), dtype=torch.float32, device=o_part.device)
+        lse_out = _empty((T, H), torch.float32, o_part.device, stream)
     st = _ffi.lib().mla_lse_combine(
         _p(o_part), _p(lse_part), P, _p(o_local), _p(lse_local), T, H, _code(o_part.dtype),
         _code(o_latent.dtype), _p(o_latent), _p(lse_out), _s(stream))
@@ -243,7 +267,7 @@ def mla_vup(o_latent, W_UV, *, out=None, err_flag=None, stream=None):
     _need(o_latent, "o_latent")
     _need(W_UV, "W_UV")
     if out is None:
-        out = torch.empty((T, H * D_V), dtype=W_UV.dtype, device=W_UV.device)
+        out = _empty((T, H * D_V), W_UV.dtype, W_UV.device, stream)
     st = _ffi.lib().mla_vup(_p(o_latent), _p(W_UV), T, H, _code(W_UV.dtype), _p(out),
                             _p(err_flag), _s(stream))
     _ffi.check("mla_vup", st)
@@ -258,7 +282,7 @@ def mla_lse_combine_vup(o_part, lse_part, W_UV, *, o_local=None, lse_local=None,
     _need(o_part, "o_part")
     _need(W_UV, "W_UV")
     if out is None:
-        out = torch.empty((T, H * D_V), dtype=W_UV.dtype, device=W_UV.device)
+        out = _empty((T, H * D_V), W_UV.dtype, W_UV.device, stream)
     st = _ffi.lib().mla_lse_combine_vup(
         _p(o_part), _p(lse_part), P, _p(o_local), _p(lse_local), _p(W_UV), T, H,
         _code(o_part.dtype), _code(W_UV.dtype), _p(out), _p(o_latent), _p(lse_out),
@@ -275,7 +299,7 @@ def mla_gather_kv(kv_cache, block_table, seq_lens, max_len: int, *, dst=None, er
     B = block_table.shape[0]
     num_blocks, bs, _ = kv_cache.shape
     if dst is None:
-        dst = torch.empty((B, max_len, D_QK), dtype=kv_cache.dtype, device=kv_cache.device)
+        dst = _empty((B, max_len, D_QK), kv_cache.dtype, kv_cache.device, stream)
     elif dst.element_size() != 2 or dst.numel() < B * max_len * D_QK:
         raise ValueError(f"dst must hold [{B}, {max_len}, {D_QK}] values of 16 bits")
     for t, n in ((kv_cache, "kv_cache"), (block_table, "block_table"), (seq_lens, "seq_lens"),

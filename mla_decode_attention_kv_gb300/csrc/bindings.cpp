@@ -8,6 +8,7 @@
 // Wrong types raise TypeError, wrong shapes, strides and devices ValueError.
 #include <ATen/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -136,6 +137,23 @@ at::Tensor make(c10::IntArrayRef shape, at::ScalarType dt, const at::Tensor& lik
   return at::Tensor(at::detail::empty_cuda(shape, dt, like.device(), std::nullopt));
 }
 
+// A new tensor of the call's stream, whose work orders its memory: a block of the
+// current stream could be one that it has given up but still works on.
+at::Tensor make_on(const Stream& stream, c10::IntArrayRef shape, at::ScalarType dt, const at::Tensor& like) {
+  const c10::cuda::CUDAStreamGuard guard(stream.s);
+  return make(shape, dt, like);
+}
+
+// An output for the caller: made on the call's stream, and, where another one is
+// current, marked as used there too, as that is where a caller goes on with it.
+at::Tensor output(const Stream& stream, c10::IntArrayRef shape, at::ScalarType dt, const at::Tensor& like) {
+  const c10::cuda::CUDAStream current = c10::cuda::getCurrentCUDAStream(like.get_device());
+  if (current.stream() == stream.s.stream()) return make(shape, dt, like);
+  at::Tensor t = make_on(stream, shape, dt, like);
+  if (t.numel() > 0) c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), current);
+  return t;
+}
+
 PyObject* result(int status, std::initializer_list<std::optional<at::Tensor>> out) {
   PyObject* r = PyTuple_New(static_cast<Py_ssize_t>(out.size()) + 1);
   if (!r) return nullptr;
@@ -218,7 +236,7 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
         bad_value("q_pe must be [T, H, 64] with unit stride along its heads");
       H = q_pe->size(1);
       if (a[9] == Py_None) {
-        q_out = make({T, H, kRope}, dt, c_kv);
+        q_out = output(stream, {T, H, kRope}, dt, c_kv);
       } else {
         q_out = tensor(a[9], "q_out");
         on(*q_out, dev, "q_out", dt);
@@ -232,7 +250,7 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::ScalarType kt = fmt == MLA_KV_E4M3 ? ct : dt;
     if (PyUnicode_Check(a[10])) {
       if (PyUnicode_CompareWithASCIIString(a[10], "new") != 0) bad_value("kv_out must be None, 'new' or a tensor");
-      kv_out = make({T, kQk}, kt, c_kv);
+      kv_out = output(stream, {T, kQk}, kt, c_kv);
     } else if (a[10] != Py_None) {
       kv_out = tensor(a[10], "kv_out");
       on(*kv_out, dev, "kv_out", kt);
@@ -271,8 +289,7 @@ at::Tensor default_workspace(const at::Tensor& like, int dev, const Stream& stre
   if (keep && it != kept->end()) return it->second;
   const uint64_t need = mla_dcp_decode_partial_fp4_workspace_size(B, q_len, shards, cur);
   if (need == 0) return at::Tensor();   // invalid sizes: the call itself reports them
-  const c10::cuda::CUDAStreamGuard g(stream.s);
-  at::Tensor t = make({static_cast<int64_t>(need)}, at::kByte, like);
+  at::Tensor t = make_on(stream, {static_cast<int64_t>(need)}, at::kByte, like);
   if (keep) kept->emplace(key, t);
   return t;
 }
@@ -316,8 +333,8 @@ PyObject* partial_fp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (P < 0) bad_value("num_shards is negative");
     const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(dev));
     const Stream stream = stream_of(a[15], dev);
-    const at::Tensor o = a[9] == Py_None ? make(wide, pt, q_abs) : tensor(a[9], "o_part");
-    const at::Tensor lse = a[10] == Py_None ? make(rows, at::kFloat, q_abs) : tensor(a[10], "lse_part");
+    const at::Tensor o = a[9] == Py_None ? output(stream, wide, pt, q_abs) : tensor(a[9], "o_part");
+    const at::Tensor lse = a[10] == Py_None ? output(stream, rows, at::kFloat, q_abs) : tensor(a[10], "lse_part");
     on(o, dev, "o_part", pt);
     on(lse, dev, "lse_part", at::kFloat);
     if (o.sizes() != c10::IntArrayRef(wide) || !o.is_contiguous() || lse.sizes() != c10::IntArrayRef(rows) || !lse.is_contiguous())
@@ -440,9 +457,8 @@ PyObject* kv_fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Stream stream = stream_of(a[8], p.dev);
     at::Tensor ws;
     if (a[6] == Py_None) {
-      // made on the call's stream: freed in its order
-      const c10::cuda::CUDAStreamGuard g(stream.s);
-      ws = make({std::max<int64_t>(16, static_cast<int64_t>(mla_kv_fork_workspace_size(fits(count, "n"))))}, at::kByte, cache);
+      ws = make_on(stream, {std::max<int64_t>(16, static_cast<int64_t>(mla_kv_fork_workspace_size(fits(count, "n"))))},
+                   at::kByte, cache);
     } else {
       ws = tensor(a[6], "workspace");
       on(ws, p.dev, "workspace");

@@ -89,6 +89,16 @@ def dcp_decode_step(q_abs, q_pe, kv_cache, block_table, seq_lens, W_UV, num_shar
     ``api.mla_dcp_decode_partial``.  Returns this rank's heads [r*H/N,
     (r+1)*H/N): the output [B*q, (H/N)*128], the combined latent
     [B*q, H/N, 512] and its LSE [B*q, H/N]."""
+    if stream is not None:
+        # the exchange and W_UV's slice go to the current stream: the whole step to this one
+        current = torch.cuda.current_stream(q_abs.device)
+        with torch.cuda.stream(api.torch_stream(stream, q_abs.device)):
+            outs = dcp_decode_step(q_abs, q_pe, kv_cache, block_table, seq_lens, W_UV, num_shards,
+                                   kv_cur=kv_cur, group=group, scale=scale, part_dtype=part_dtype,
+                                   err_flag=err_flag, workspace=workspace, kv_scale=kv_scale)
+        for t in outs:
+            t.record_stream(current)
+        return outs
     world = dist.get_world_size(group)
     rank = dist.get_rank(group)
     H = q_abs.shape[2]
