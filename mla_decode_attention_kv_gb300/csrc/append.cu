@@ -548,8 +548,8 @@ __device__ void rotate_queries(const AppendParams& ap, int64_t item, int lane) {
 
 template <bool BF16, int KIND>
 __global__ void __launch_bounds__(kAppendThreads, 16) mla_kv_append_kernel(const __grid_constant__ AppendParams ap) {
-  griddep_launch_dependents();
   griddep_wait();
+  griddep_launch_dependents();
   const int blk = static_cast<int>(blockIdx.x);
   if (blk < ap.row_blocks) {
     const int t = blk * (kAppendThreads / 32) + (threadIdx.x >> 5);

@@ -41,8 +41,8 @@ __device__ __forceinline__ void copy_chunk(const char* src, char* dst, uint64_t 
 
 // ---------------------------------------------------------------- copy
 __global__ void __launch_bounds__(kCopyThreads) mla_copy_pages_kernel(const CopyParams cp) {
-  griddep_launch_dependents();
   griddep_wait();
+  griddep_launch_dependents();
   const int i = blockIdx.x / cp.chunks, chunk = blockIdx.x - i * cp.chunks;
   const int a = __ldg(cp.src_ids + i), b = __ldg(cp.dst_ids + i);
   if (a < 0 || a >= cp.src_blocks || b < 0 || b >= cp.dst_blocks) {
@@ -64,8 +64,8 @@ int launch_copy_pages(CopyParams cp, cudaStream_t stream) {
 // first thread, so a row named twice is given back once.
 __global__ void __launch_bounds__(256) mla_kv_free_kernel(const FreeParams fp) {
   __shared__ int s_pages;
-  griddep_launch_dependents();
   griddep_wait();
+  griddep_launch_dependents();
   const int r = __ldg(fp.rows + blockIdx.x);
   if (r < 0 || r >= fp.num_rows) {
     if (threadIdx.x == 0) set_error(fp.err, kDevBadRow);
@@ -136,10 +136,10 @@ __global__ void __launch_bounds__(kPlanThreads) mla_kv_fork_plan_kernel(const Fo
   __shared__ int s_bad;
   int32_t* fresh = fp.ws + 4;
   int32_t* list = fresh + fp.n;
-  griddep_launch_dependents();
   for (int i = threadIdx.x; i < (fp.rows + 31) / 32; i += kPlanThreads) s_child[i] = s_parent[i] = 0;
   if (threadIdx.x == 0) s_bad = 0;
   griddep_wait();   // the grid before, a mla_kv_free for one, is done
+  griddep_launch_dependents();
   __syncthreads();
   const int per = (fp.n + kPlanThreads - 1) / kPlanThreads;
   const int a = min(fp.n, static_cast<int>(threadIdx.x) * per), e = min(fp.n, a + per);
@@ -219,8 +219,8 @@ __global__ void __launch_bounds__(kPlanThreads) mla_kv_fork_plan_kernel(const Fo
 }
 
 __global__ void __launch_bounds__(kCopyThreads) mla_kv_fork_apply_kernel(const ForkParams fp) {
-  griddep_launch_dependents();
   griddep_wait();   // the plan is complete
+  griddep_launch_dependents();
   if (fp.ws[0] == 0) return;
   const int per = fp.layers * fp.chunks + 1;
   const int k = blockIdx.x / per, j = blockIdx.x - k * per;

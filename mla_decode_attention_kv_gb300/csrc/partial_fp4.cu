@@ -644,9 +644,10 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
     prefetch_tmap(&tm_qpe);
   }
   // (programmatic launches: this grid's start overlaps the one before, the
-  // merge grid's start this one; each waits for the other to be done)
-  griddep_launch_dependents();
+  // next grid's start this one; each waits for the other to be done, and lets the
+  // next go only then: the V-up reads W_UV before its own wait)
   griddep_wait();
+  griddep_launch_dependents();
   Range4 rng;
   if constexpr (SHARES) rng = partition4<N, L::kThreads>(fp, reinterpret_cast<PartScratch*>(smem), tab, cid, ncta);
   else rng = single4<N>(fp, tab, cid);

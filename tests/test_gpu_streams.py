@@ -169,3 +169,30 @@ def test_dcp_step_on_another_stream(tmp_path):
         assert all(torch.equal(a, b) for a, b in zip(copies, want))
     finally:
         dist.destroy_process_group()
+
+
+def test_vup_behind_the_partials_sees_weights_written_before_them():
+    """W_UV written by a grid that lets the next one start early, then the partials over
+    E2M1 pages and the V-up, which reads W_UV ahead of its wait for the partials: the same
+    as with a wait after every call."""
+    c = Fp4([300, 50], 16, cur=True, seed=6)
+    g = torch.Generator(device=DEV).manual_seed(3)
+    Ws = [torch.randn(16, 512, 128, generator=g, device=DEV).to(torch.bfloat16) for _ in range(6)]
+    ids = torch.arange(16, dtype=torch.int32, device=DEV)
+
+    def run(wait):
+        sync = torch.cuda.synchronize if wait else lambda: None
+        W, outs = torch.zeros_like(Ws[0]), []
+        torch.cuda.synchronize()
+        for k in range(60):
+            api.mla_kv_copy_pages(Ws[k % 6], W, ids, ids, err_flag=c.err)
+            sync()
+            o, lse = c.run()
+            sync()
+            outs.append(api.mla_lse_combine_vup(o, lse, W, err_flag=c.err))
+            sync()
+        torch.cuda.synchronize()
+        assert c.err.item() == 0
+        return outs
+
+    assert all(torch.equal(a, b) for a, b in zip(run(False), run(True)))
