@@ -201,7 +201,7 @@ __device__ __forceinline__ void e2m1_values(uint32_t c, float d, uint32_t* w) {
 // Out-of-range positions are recorded and read as 0.
 __device__ __forceinline__ int pair_position(const AppendParams& ap, int t, int i) {
   const int axis = (i >= ap.sec1) + (i >= ap.sec2);
-  int pos = __ldg(ap.positions + static_cast<int64_t>(axis) * ap.T + t);
+  int pos = ap.positions[static_cast<int64_t>(axis) * ap.T + t];
   if (pos < 0 || pos >= ap.max_pos) {
     set_error(ap.err, kDevBadPosition);
     pos = 0;
@@ -234,8 +234,8 @@ __device__ __forceinline__ bool append_row(const AppendParams& ap, int t, int la
     kb = load1<BF16>(ap.k_pe, t * ap.k_stride + 32 + lane);
   }
   const float* cs = ap.cos_sin + static_cast<int64_t>(pair_position(ap, t, lane)) * 64;
-  const float co = __ldg(cs + lane), si = __ldg(cs + 32 + lane);
-  const int slot = __ldg(ap.slots + t);
+  const float co = cs[lane], si = cs[32 + lane];
+  const int slot = ap.slots[t];
 
   float y[16];       // the row's values: EXACT, rounded to odd; otherwise y * by
   float by = 1.f;
@@ -243,7 +243,7 @@ __device__ __forceinline__ bool append_row(const AppendParams& ap, int t, int la
   if (ap.weight) {
     uint32_t ww[8];
     const uint4* wsrc = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(ap.weight) + 16 * lane);
-    const uint4 a = __ldg(wsrc), b = __ldg(wsrc + 1);
+    const uint4 a = wsrc[0], b = wsrc[1];
     ww[0] = a.x; ww[1] = a.y; ww[2] = a.z; ww[3] = a.w;
     ww[4] = b.x; ww[5] = b.y; ww[6] = b.z; ww[7] = b.w;
     if constexpr (EXACT) {
@@ -506,15 +506,15 @@ __device__ void rotate_queries(const AppendParams& ap, int64_t item, int lane) {
   const bool cut = (ap.sec1 > i0 && ap.sec1 < i0 + 4) || (ap.sec2 > i0 && ap.sec2 < i0 + 4);
   if (!cut) {
     const float* cs = ap.cos_sin + static_cast<int64_t>(pair_position(ap, t, i0)) * 64 + i0;
-    co = __ldg(reinterpret_cast<const float4*>(cs));
-    si = __ldg(reinterpret_cast<const float4*>(cs + 32));
+    co = *reinterpret_cast<const float4*>(cs);
+    si = *reinterpret_cast<const float4*>(cs + 32);
   } else {
     float c[4], s[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const float* cs = ap.cos_sin + static_cast<int64_t>(pair_position(ap, t, i0 + k)) * 64 + i0 + k;
-      c[k] = __ldg(cs);
-      s[k] = __ldg(cs + 32);
+      c[k] = cs[0];
+      s[k] = cs[32];
     }
     co = make_float4(c[0], c[1], c[2], c[3]);
     si = make_float4(s[0], s[1], s[2], s[3]);

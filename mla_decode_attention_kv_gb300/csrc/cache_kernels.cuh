@@ -20,7 +20,9 @@ enum CacheError : int {
 // the stream, for which every block waits (griddep_wait) before it reads or writes.
 // Only behind that wait does a block let the next grid go (griddep_launch_dependents):
 // a grid that does some reading before its own wait, the V-up's of W_UV, then still
-// finds everything but its direct predecessor done.
+// finds everything but its direct predecessor done.  What the grid before may have
+// written (tables, ids, lengths) is read by plain loads: __ldg asks for data that
+// nothing writes as long as the kernel lives, its time before the wait included.
 // Calls back to back, without it and so: 8 pages copied 4.1 and 2.8 us, 8192 tokens
 // appended 14.3 and 11.8, 64 rows forked 16.4 and 14.1.
 template <class... A, class... B>

@@ -44,7 +44,7 @@ __global__ void __launch_bounds__(kCopyThreads) mla_copy_pages_kernel(const Copy
   griddep_wait();
   griddep_launch_dependents();
   const int i = blockIdx.x / cp.chunks, chunk = blockIdx.x - i * cp.chunks;
-  const int a = __ldg(cp.src_ids + i), b = __ldg(cp.dst_ids + i);
+  const int a = cp.src_ids[i], b = cp.dst_ids[i];
   if (a < 0 || a >= cp.src_blocks || b < 0 || b >= cp.dst_blocks) {
     if (threadIdx.x == 0) set_error(cp.err, kDevBadBlockId);
     return;
@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(256) mla_kv_free_kernel(const FreeParams fp) {
   __shared__ int s_pages;
   griddep_wait();
   griddep_launch_dependents();
-  const int r = __ldg(fp.rows + blockIdx.x);
+  const int r = fp.rows[blockIdx.x];
   if (r < 0 || r >= fp.num_rows) {
     if (threadIdx.x == 0) set_error(fp.err, kDevBadRow);
     return;

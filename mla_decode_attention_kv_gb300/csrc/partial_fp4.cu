@@ -667,7 +667,7 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
     auto fetch = [&](const Iter4<N>& t) {
       if (!t.valid || t.ui.p == fp.S || lane >= nbox) return 0;
       const int tk = min(t.tok0() + lane * fp.box, t.ui.hi - 1);
-      return __ldg(fp.block_table + static_cast<int64_t>(t.ui.b) * fp.max_blocks + (tk >> fp.bs_shift));
+      return fp.block_table[static_cast<int64_t>(t.ui.b) * fp.max_blocks + (tk >> fp.bs_shift)];
     };
     int id_cur = fetch(it);
     while (it.valid) {
