@@ -49,7 +49,7 @@ __device__ __forceinline__ RowWeights row_weights(const float* lse_part, int P, 
   for (int k = 0; k < 3; ++k) {
     const int p = lane + 32 * k;
     v[k] = -INFINITY;
-    if (p < np) v[k] = p < P ? __ldg(lse_part + (t * P + p) * H + h) : __ldg(lse_local + t * H + h);
+    if (p < np) v[k] = p < P ? lse_part[(t * P + p) * H + h] : lse_local[t * H + h];
     mx = fmaxf(mx, v[k]);
   }
 #pragma unroll
@@ -74,7 +74,9 @@ __device__ __forceinline__ float weight_of(const RowWeights& rw, int p) {
   return __shfl_sync(0xffffffffu, x, p & 31);
 }
 
-// 16 consecutive elements of one partial row: 64 bytes (fp32) or 32 bytes.
+// 16 consecutive elements of one partial row: 64 bytes (fp32) or 32 bytes.  (Plain
+// loads here and of the LSEs: the fused kernels start while the partials are written,
+// which __ldg does not allow for.)
 template <bool F32>
 struct Chunk16 {
   uint4 v[F32 ? 4 : 2];
@@ -86,7 +88,7 @@ __device__ __forceinline__ Chunk16<F32> load16(const void* src, int64_t e) {
   const uint4* p = F32 ? reinterpret_cast<const uint4*>(static_cast<const float*>(src) + e)
                        : reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(src) + e);
 #pragma unroll
-  for (int i = 0; i < (F32 ? 4 : 2); ++i) x.v[i] = __ldg(p + i);
+  for (int i = 0; i < (F32 ? 4 : 2); ++i) x.v[i] = p[i];
   return x;
 }
 
@@ -363,8 +365,8 @@ __global__ void __launch_bounds__(256, 1)
           const uint4* src = reinterpret_cast<const uint4*>(
               static_cast<const uint16_t*>(o_latent_in) +
               ((t0 + rr) * static_cast<int64_t>(H) + h) * 512 + lane * 16);
-          a = __ldg(src);
-          b = __ldg(src + 1);
+          a = src[0];
+          b = src[1];
         }
         *reinterpret_cast<uint4*>(sB + c * (kVupRows * 128) + sw128_offset(rr, u)) = a;
         *reinterpret_cast<uint4*>(sB + c * (kVupRows * 128) + sw128_offset(rr, u + 1)) = b;
@@ -607,8 +609,7 @@ __global__ void __launch_bounds__(256, 1)
         const int64_t t = t0 + i % TB;
         float v = -INFINITY;
         if (t < va.T)
-          v = p < va.P ? __ldg(va.lse_part + (t * va.P + p) * va.H + h)
-                       : __ldg(va.lse_local + t * va.H + h);
+          v = p < va.P ? va.lse_part[(t * va.P + p) * va.H + h] : va.lse_local[t * va.H + h];
         s_lse[i] = v;
       }
       named_bar_sync(2, 64);

@@ -99,3 +99,42 @@ def test_copies_and_frees_by_ids_that_the_call_before_moved():
         return outs
 
     assert all(torch.equal(x, y) for u, v in zip(run(False), run(True)) for x, y in zip(u, v))
+
+
+@pytest.mark.parametrize("part", [BF, torch.float32])
+@pytest.mark.parametrize("cache", ["16-bit", "e2m1"])
+def test_combine_directly_behind_the_partials(part, cache):
+    """Partials and the combine with the V-up (its two forms) into the same buffers, other
+    queries every step: the combine starts while the partials are written."""
+    B, H, L, bs = 6, 64, 700, 64
+    g = torch.Generator(device=DEV).manual_seed(1)
+    n = -(-L // bs)
+    if cache == "e2m1":
+        pool = torch.randint(0, 256, (B * n, bs * 324), generator=g, device=DEV, dtype=torch.uint8)
+        pool[:, bs * 288:] = pool[:, bs * 288:] % 24 + 40
+        pool = pool.view(B * n, bs, 324)
+    else:
+        pool = torch.randn(B * n, bs, 576, generator=g, device=DEV).to(BF)
+    table = torch.randperm(B * n, generator=g, device=DEV).int().view(B, n)
+    lens, err = torch.full((B,), L, dtype=torch.int32, device=DEV), _ids(0)
+    W = torch.randn(H, 512, 128, generator=g, device=DEV).to(BF)
+    qs = [(torch.randn(B, 1, H, 512, generator=g, device=DEV).to(BF), torch.randn(B, 1, H, 64, generator=g, device=DEV).to(BF))
+          for _ in range(5)]
+
+    def run(wait):
+        sync = torch.cuda.synchronize if wait else lambda: None
+        o = torch.zeros(B, 1, 4, H, 512, dtype=part, device=DEV)
+        lse, outs = torch.zeros(B, 1, 4, H, device=DEV), []
+        torch.cuda.synchronize()
+        for k in range(40):
+            api.mla_dcp_decode_partial(*qs[k % 5], pool, table, lens, 4, o_part=o, lse_part=lse, err_flag=err)
+            sync()
+            outs.append(api.mla_lse_combine_vup(o, lse, W, err_flag=err))
+            sync()
+            outs.append(api.mla_vup(o[:, :, 0].contiguous().to(BF), W, err_flag=err))
+            sync()
+        torch.cuda.synchronize()
+        assert err.item() == 0
+        return outs
+
+    assert all(torch.equal(x, y) for x, y in zip(run(False), run(True)))
