@@ -493,7 +493,7 @@ int mla_kv_copy_pages(const void* src, uint64_t src_layer_stride, int src_blocks
  *   block_table [num_rows, max_blocks] int32, seq_lens [num_rows] int32,
  *   ref_counts [num_blocks] int32: rows that hold each page, 0 = free
  *   rows [n] int32 (device); a row named twice is given back once
- * MLA_DEV_BAD_ROW, MLA_DEV_BAD_SEQ_LEN (that row's pages stay counted),
+ * MLA_DEV_BAD_ROW, MLA_DEV_BAD_SEQ_LEN (that row stays as it is, length and all),
  * MLA_DEV_BAD_BLOCK_ID and MLA_DEV_BAD_REF_COUNT (a count that is 0 already;
  * it stays 0) as they are met.
  */

@@ -60,8 +60,8 @@ int launch_copy_pages(CopyParams cp, cudaStream_t stream) {
 }
 
 // ---------------------------------------------------------------- free
-// One block per row.  The row's length is taken (exchanged with 0) by its
-// first thread, so a row named twice is given back once.
+// One block per row.  The row's length is taken (swapped for 0) by its first
+// thread, so a row named twice is given back once.
 __global__ void __launch_bounds__(256) mla_kv_free_kernel(const FreeParams fp) {
   __shared__ int s_pages;
   griddep_wait();
@@ -72,10 +72,12 @@ __global__ void __launch_bounds__(256) mla_kv_free_kernel(const FreeParams fp) {
     return;
   }
   if (threadIdx.x == 0) {
-    int L = atomicExch(fp.lens + r, 0);
+    int L = *static_cast<volatile const int32_t*>(fp.lens + r);
     const int64_t cap = static_cast<int64_t>(fp.max_blocks) * fp.bs;
-    if (L < 0 || L > cap) {
+    if (L < 0 || L > cap) {   // left as it is: an emptied row would lose its pages
       set_error(fp.err, kDevBadSeqLen);
+      L = 0;
+    } else if (atomicCAS(fp.lens + r, L, 0) != L) {
       L = 0;
     }
     s_pages = static_cast<int>((static_cast<int64_t>(L) + fp.bs - 1) / fp.bs);
