@@ -400,7 +400,8 @@ int mla_dcp_decode_partial_fp4(const void* q_abs, const void* q_pe, const void* 
     fp.ws_units = reinterpret_cast<int4*>(w);
     fp.ws_bounds = reinterpret_cast<int*>(w + static_cast<size_t>(ctas) * 16);
     fp.ws_lse = reinterpret_cast<float*>(w + mla::fp4_workspace_recs(ctas));
-    fp.ws_o = w + mla::fp4_workspace_recs(ctas) + 2 * static_cast<size_t>(ctas) * mla::kFp4MaxRows * 4;
+    fp.ws_o = reinterpret_cast<float*>(w + mla::fp4_workspace_recs(ctas) +
+                                       2 * static_cast<size_t>(ctas) * mla::kFp4MaxRows * 4);
   }
   return launched(mla::launch_partial_fp4(tm_qlat, tm_qpe, fp, rows, bf16, reinterpret_cast<cudaStream_t>(stream)));
 }

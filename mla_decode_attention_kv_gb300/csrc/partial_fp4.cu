@@ -50,6 +50,15 @@
 // maxima over the tokens (the lanes) and rescales O.  Row sums stay in registers,
 // one partial sum per token lane and row, and are reduced once per piece.
 //
+// Roundings: the weights go to the query's 16-bit type for the PV product, whose two
+// operands share a type and whose V is exact in it (a second term would double that
+// product): o is off by half a step of sqrt(sum p^2 c^2), 0.3 to 0.9 of what rounding
+// the output itself takes.  Scores, maxima, row sums (of the unrounded weights), O and
+// the pieces of a cut unit are fp32; an output is rounded once.  (Pieces in fp32 and
+// not in the output's type: 16 x 131072 x 16 heads 297 -> 299 us, ragged 142 -> 145, 8 x
+// 32768 of two tokens 211 -> 217, with errors against 64 bits of 1.14, 1.22 and 1.08
+// times those of an output rounded alone, 1.31, 1.24 and 1.14 before.)
+//
 // Every wait is bounded, as in the 16-bit kernel.
 #include <mutex>
 #include <type_traits>
@@ -1092,7 +1101,8 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
         // ---- epilogue of the piece: row sums over the tokens, O / l, LSE.  The sums,
         // factors and places are worked out while the last PV product runs.
         const bool whole = it.whole();
-        const int esz = fp.part_dtype == kFP32 ? 4 : 2;
+        // (a piece goes to the workspace in fp32, so that a row is rounded once, cut or not)
+        const bool narrow = whole && fp.part_dtype != kFP32;
         char* out = static_cast<char*>(whole ? fp.o_part : fp.ws_o);
 #pragma unroll
         for (int q = 0; q < PASSES; ++q) {
@@ -1123,7 +1133,7 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
         ok = __all_sync(0xffffffffu, waits.lazy(&bar[L::B_P_EMPTY], g & 1)) != 0;
         tc_fence_after();
         if (!ok) {
-        } else if (esz == 2) {
+        } else if (narrow) {
           // 32 latents of 8 rows at a time: read as matrix fragments, scaled,
           // stored transposed into the warp's staging (16-byte unit j of row k at
           // unit j ^ (k / 2 & 3): no bank conflicts) and from there to the rows,
@@ -1370,7 +1380,6 @@ __global__ void __launch_bounds__(256) mla_partial_fp4_merge_kernel(const Fp4Par
   if (u < 0) return;
   const int p = u % fp.P, gb = u / fp.P, b = gb % fp.B, r = (gb / fp.B) * rows + n;
   if (r >= fp.R) return;
-  const bool f32 = fp.part_dtype == kFP32;
   float acc[16];
 #pragma unroll
   for (int t = 0; t < 16; ++t) acc[t] = 0.f;
@@ -1405,35 +1414,20 @@ __global__ void __launch_bounds__(256) mla_partial_fp4_merge_kernel(const Fp4Par
       const int64_t e0 = __shfl_sync(0xffffffffu, row, k) * 512 + lane * 16;
       if (wk == 0.f) continue;
       wsum += wk;
-      if (f32) {
-        const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(fp.ws_o) + e0);
+      const float4* src = reinterpret_cast<const float4*>(fp.ws_o + e0);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float4 f = src[j];
-          acc[4 * j] = fmaf(wk, f.x, acc[4 * j]);
-          acc[4 * j + 1] = fmaf(wk, f.y, acc[4 * j + 1]);
-          acc[4 * j + 2] = fmaf(wk, f.z, acc[4 * j + 2]);
-          acc[4 * j + 3] = fmaf(wk, f.w, acc[4 * j + 3]);
-        }
-      } else {
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(fp.ws_o) + e0);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const uint4 h = src[j];
-          const uint32_t hw[4] = {h.x, h.y, h.z, h.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 f2 = unpack2(hw[i], fp.part_dtype);
-            acc[8 * j + 2 * i] = fmaf(wk, f2.x, acc[8 * j + 2 * i]);
-            acc[8 * j + 2 * i + 1] = fmaf(wk, f2.y, acc[8 * j + 2 * i + 1]);
-          }
-        }
+      for (int j = 0; j < 4; ++j) {
+        const float4 f = src[j];
+        acc[4 * j] = fmaf(wk, f.x, acc[4 * j]);
+        acc[4 * j + 1] = fmaf(wk, f.y, acc[4 * j + 1]);
+        acc[4 * j + 2] = fmaf(wk, f.z, acc[4 * j + 2]);
+        acc[4 * j + 3] = fmaf(wk, f.w, acc[4 * j + 3]);
       }
     }
   }
   const float inv = 1.f / wsum;
   const int64_t row = out_row4(fp, b, r, p);
-  if (f32) {
+  if (fp.part_dtype == kFP32) {
     float4* d = reinterpret_cast<float4*>(static_cast<float*>(fp.o_part) + row * 512 + lane * 16);
 #pragma unroll
     for (int j = 0; j < 4; ++j)

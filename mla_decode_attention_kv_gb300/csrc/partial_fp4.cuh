@@ -42,7 +42,7 @@ struct Fp4Params {
   uint32_t spin_limit;
   // workspace (split: CTAs that share the tiles exactly, 0: whole units)
   int split;
-  void* ws_o;            // pieces of O / l in the partial dtype, [2 * ctas][rows][512]
+  float* ws_o;           // pieces of O / l, [2 * ctas][rows][512]
   float* ws_lse;         // [2 * ctas][rows], log2
   int4* ws_units;        // [ctas]: {unit, its first tile, first CTA, last CTA} of the unit that ends here
   int* ws_bounds;        // [ctas + 1]: first tile of each CTA's share, then the tile total
