@@ -255,7 +255,8 @@ int mla_dcp_decode_partial_fp8(const void* q_abs, const void* q_pe, const void* 
  * Precision: every code * s is a value of either 16-bit type, so the tensor
  * cores multiply the cache as it is stored by the query as it is given; the
  * softmax weights are rounded to in_dtype before the PV product, as in the
- * 16-bit call (their sums, and with them the LSE, are not); the pieces of a cut
+ * 16-bit call (their sums, and with them the LSE, are not; fp16 weights below 2^-21
+ * of the largest are off by up to 2^-32 of it); the pieces of a cut
  * shard are kept in fp32, so a row is rounded to part_dtype once, cut or not.
  */
 int mla_dcp_decode_partial_fp4(const void* q_abs, const void* q_pe, const void* kv_cache,

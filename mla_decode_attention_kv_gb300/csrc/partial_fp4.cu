@@ -46,7 +46,7 @@
 // and a half tiles 836 us, quarters 801, with the ring above 785 at that step).  With 16 rows,
 // where shared memory sets it, quarters are 9 % slower.
 //
-// Only a tile with a weight past 2^8 (and the first of a piece) reduces the rows'
+// Only a tile with a weight past 2^8 of the reference (and the first of a piece) reduces the rows'
 // maxima over the tokens (the lanes) and rescales O.  Row sums stay in registers,
 // one partial sum per token lane and row, and are reduced once per piece.
 //
@@ -606,7 +606,11 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
     mla_partial_fp4_kernel(const __grid_constant__ CUtensorMap tm_qlat, const __grid_constant__ CUtensorMap tm_qpe,
                            const Fp4Params fp) {
   using L = Smem4<N>;
-  constexpr float kThresh = 8.f;               // lazy rescale: weights stay below 2^8
+  // Weights are taken relative to a row's reference maximum and, for fp16, whose least
+  // normal value is 2^-14, times 2^7: a weight down to 2^-21 of the maximum's keeps its
+  // eleven bits and one down to 2^-32 some, where a long history has many of those.
+  constexpr float kLift = BF16 ? 0.f : 7.f;
+  constexpr float kThresh = 8.f + kLift;       // lazy rescale: weights stay below 2^8 (2^15 as lifted)
 
   // (the kernel has no static shared memory, so the block starts where the
   // alignment puts it; the 128-byte swizzle needs 1024)
@@ -871,7 +875,7 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
     auto red_of = [&](int q) { return reinterpret_cast<float*>(smem + L::kRedOff) + (grp * PASSES + q) * (4 * NG); };   // [4][NG]
     volatile int* flags = reinterpret_cast<volatile int*>(smem + L::kFlagOff);
     float l[PASSES][NC];
-    // Reference maxima of pass q, in shared memory; the 64-row kernel, which would
+    // Reference maxima of pass q (less the lift), in shared memory; the 64-row kernel, which would
     // spill them, reads them there, the others keep a copy in registers (64 rows, 32 x
     // 4096 tokens x 128 heads: 93 us with registers, 86 without; 16 rows, 16 x 131072
     // tokens: 306 and 312).
@@ -945,7 +949,7 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
         const float t = fmaxf(fmaxf(r[0], r[NG]), fmaxf(r[2 * NG], r[3 * NG]));
         a[k] = 1.f;
         if (t > kThresh) {   // (t is relative to m, which `scores` left here)
-          const float mn = m[k] + t;
+          const float mn = m[k] + (t - kLift);
           a[k] = fast_exp2(m[k] - mn);
           m[k] = mn;
           lq[k] *= a[k];
@@ -1016,7 +1020,7 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
         if (wq == 0 && lane < NG * PASSES) {
           const float* r = red_of(0) + (lane / NG) * (4 * NG) + lane % NG;
           const float t = fmaxf(fmaxf(r[0], r[NG]), fmaxf(r[2 * NG], r[3 * NG]));
-          reinterpret_cast<float*>(smem + L::kMOff)[col0(0) + lane] = t == -INFINITY ? 0.f : t;
+          reinterpret_cast<float*>(smem + L::kMOff)[col0(0) + lane] = t == -INFINITY ? 0.f : t - kLift;
         }
         named_bar_sync(barid, 128);
         if constexpr (kKeepM) {
@@ -1025,7 +1029,7 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
         }
       }
       // The weights are made and handed over against the reference maxima as
-      // they stand; a warp that finds one past 2^8 raises its group's flag of
+      // they stand; a warp that finds one past the limit raises its group's flag of
       // this tile, and the group makes them again before the PV product, which
       // looks at the flags, reads them.  (A barrier to agree first cost 500
       // cycles of every tile.)
