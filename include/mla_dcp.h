@@ -444,8 +444,9 @@ int mla_gather_kv(const void* kv_cache, const int32_t* block_table, const int32_
  *   k_pe      [T, 64] dtype, rows k_stride elements apart
  *   q_pe      [T, H, 64] dtype, strides q_stride, q_head_stride; or NULL
  *   q_out     [T, H, 64] dtype, strides qo_stride, qo_head_stride; may be q_pe
- *             itself (same strides); NULL with q_pe
- *             (strides >= 0, multiples of 8 elements)
+ *             itself (same strides, MLA_ERR_BAD_SHAPE otherwise); NULL with q_pe
+ *             (strides >= 0, multiples of 8 elements; the rows of q_out do not
+ *             overlap: MLA_ERR_BAD_SHAPE)
  *   positions [num_axes, T] int32 in [0, max_pos), num_axes 1 to 3
  *   sections  HOST array [num_axes]: pairs of each axis in turn, sum 32
  *   cos_sin   [max_pos, 64] float32: a row holds 32 cosines, then 32 sines

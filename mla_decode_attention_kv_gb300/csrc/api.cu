@@ -95,6 +95,16 @@ bool page_layout_ok(uint64_t page_bytes, int num_layers, int n) {
   return per_page * num_layers + 1 <= (uint64_t{INT32_MAX}) / static_cast<uint64_t>(n);
 }
 
+// The 64-wide rows of T tokens and H heads at these strides do not overlap, one of the
+// two dimensions lying inside the other's step.
+bool rows_apart(int64_t T, int64_t stride, int64_t H, int64_t head_stride) {
+  if (T > 1 && stride < MLA_D_ROPE) return false;
+  if (H > 1 && head_stride < MLA_D_ROPE) return false;
+  if (T == 1 || H == 1) return true;
+  // (compared by quotients: the products may pass 64 bits)
+  return (stride - MLA_D_ROPE) / head_stride >= H - 1 || (head_stride - MLA_D_ROPE) / stride >= T - 1;
+}
+
 int launched(int rc) {
   if (rc != 0) return MLA_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
@@ -640,7 +650,11 @@ int mla_kv_append(const void* c_kv, int64_t c_stride, const void* k_pe, int64_t 
   // rows are read in 16-byte pieces
   if (c_stride < 0 || c_stride % 8 != 0 || k_stride < 0 || k_stride % 8 != 0) return MLA_ERR_BAD_SHAPE;
   if (q_pe && (q_stride < 0 || q_stride % 8 != 0 || q_head_stride < 0 || q_head_stride % 8 != 0 ||
-               qo_stride < 0 || qo_stride % 8 != 0 || qo_head_stride < 0 || qo_head_stride % 8 != 0))
+               qo_stride < 0 || qo_stride % 8 != 0 || qo_head_stride < 0 || qo_head_stride % 8 != 0 ||
+               !rows_apart(T, qo_stride, H, qo_head_stride)))
+    return MLA_ERR_BAD_SHAPE;
+  // in place a warp writes what it has read: the places have to be the same
+  if (q_pe && q_pe == q_out && ((T > 1 && q_stride != qo_stride) || (H > 1 && q_head_stride != qo_head_stride)))
     return MLA_ERR_BAD_SHAPE;
   if (!aligned16(c_kv) || !aligned16(k_pe) || !aligned16(norm_weight) || !aligned16(q_pe) ||
       !aligned16(q_out) || !aligned16(cos_sin) || !aligned16(kv_cache) || !aligned16(kv_out))
