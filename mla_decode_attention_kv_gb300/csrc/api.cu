@@ -643,7 +643,7 @@ int mla_kv_append(const void* c_kv, int64_t c_stride, const void* k_pe, int64_t 
     return MLA_ERR_BAD_SHAPE;
   int sum = 0;
   for (int a = 0; a < num_axes; ++a) {
-    if (sections[a] < 0) return MLA_ERR_BAD_SHAPE;
+    if (sections[a] < 0 || sections[a] > MLA_D_ROPE / 2) return MLA_ERR_BAD_SHAPE;
     sum += sections[a];
   }
   if (sum != MLA_D_ROPE / 2) return MLA_ERR_BAD_SHAPE;

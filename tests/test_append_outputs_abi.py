@@ -1,5 +1,5 @@
-"""Host checks of mla_kv_append's outputs (no GPU): what would make its writes race is
-refused before anything is launched."""
+"""Host checks of mla_kv_append's outputs and sections (no GPU): what would make its
+writes race or its axes wrap is refused before anything is launched."""
 import ctypes
 
 import pytest
@@ -46,3 +46,14 @@ def test_in_place_with_other_strides_is_refused(lib):
     assert _append(lib, qo=FAKE, T=1, qos=0) == PAST_THE_CHECK
     assert _append(lib, qo=FAKE, T=1, qos=0, qoh=128) == BAD_SHAPE
     assert _append(lib, qo=FAKE, H=1, qoh=0) == PAST_THE_CHECK
+
+
+@pytest.mark.parametrize("sections", [
+    (2 ** 31 - 1, 2 ** 31 - 1, 34), (33, -1), (2 ** 31 - 1, -(2 ** 31 - 1) + 32), (40, 40, -48), (0, 0, 0), (16, 15)])
+def test_sections_that_do_not_sum_to_32(lib, sections):
+    assert _append(lib, sections=sections) == BAD_SHAPE
+
+
+@pytest.mark.parametrize("sections", [(32,), (0, 32), (32, 0, 0), (0, 0, 32), (1, 30, 1)])
+def test_sections_that_sum_to_32(lib, sections):
+    assert _append(lib, sections=sections) == PAST_THE_CHECK
