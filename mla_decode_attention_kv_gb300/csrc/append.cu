@@ -87,7 +87,8 @@ __device__ __forceinline__ F2 mul_diff(float a, float c, float b, float s) {   /
   const float p2 = b * s, e2 = fmaf(b, s, -p2);
   const F2 d = two_sum(p1, -p2);
   const float lo = d.lo + (e1 - e2);
-  return lo == 0.f ? F2{d.hi, 0.f} : renorm(d.hi, lo);   // (a zero keeps the sum's sign)
+  // (a zero keeps the sum's sign; an infinity, whose errors are NaN, stays one)
+  return lo == 0.f || lo != lo ? F2{d.hi, 0.f} : renorm(d.hi, lo);
 }
 
 template <bool BF16>
