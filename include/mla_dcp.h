@@ -437,8 +437,8 @@ int mla_gather_kv(const void* kv_cache, const int32_t* block_table, const int32_
  *         code = rn_E2M1(value / (s kv_scale)), 0 where s is 0; a zero keeps
  *         its sign; a block that holds a NaN gets s = NaN
  * (exactly so where kv_scale is a power of two; q_out is computed in fp32).
- * mean(c^2) + eps counts as at least 2^-120 (a row of zeros stays zeros); beyond
- * 1e16 inputs leave the range of its fp32 sum.
+ * mean(c^2) + eps counts as at least 2^-120 (a row of zeros stays zeros).  With the
+ * norm, an infinity makes its row zeros and itself NaN, and a NaN all of the row NaN.
  *
  *   c_kv      [T, 512] dtype, rows c_stride elements apart
  *   k_pe      [T, 64] dtype, rows k_stride elements apart

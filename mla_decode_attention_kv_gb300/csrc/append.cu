@@ -249,41 +249,50 @@ __device__ __forceinline__ bool append_row(const AppendParams& ap, int t, int la
     ww[4] = b.x; ww[5] = b.y; ww[6] = b.z; ww[7] = b.w;
     if constexpr (EXACT) {
       // sum of squares: the squares of 16-bit values are exact in fp32, each
-      // addition's error is kept
-      float s = 0.f, e = 0.f;
+      // addition's error is kept.  Where it passes fp32 (bf16 rows from some 1e18 on)
+      // it is taken again of the values times 2^-70, the same for the lanes' products.
+      float s, e, sc = 1.f;
+      while (true) {
+        s = e = 0.f;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float2 f = unpack<BF16>(cw[k]);
-        F2 u = two_sum(s, f.x * f.x);
-        e += u.lo;
-        u = two_sum(u.hi, f.y * f.y);
-        s = u.hi;
-        e += u.lo;
-      }
+        for (int k = 0; k < 8; ++k) {
+          const float2 f = unpack<BF16>(cw[k]);
+          const float fx = f.x * sc, fy = f.y * sc;
+          F2 u = two_sum(s, fx * fx);
+          e += u.lo;
+          u = two_sum(u.hi, fy * fy);
+          s = u.hi;
+          e += u.lo;
+        }
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        const float s2 = __shfl_xor_sync(0xffffffffu, s, o), e2 = __shfl_xor_sync(0xffffffffu, e, o);
-        const F2 u = two_sum(s, s2);
-        s = u.hi;
-        e = (e + e2) + u.lo;
+        for (int o = 16; o > 0; o >>= 1) {
+          const float s2 = __shfl_xor_sync(0xffffffffu, s, o), e2 = __shfl_xor_sync(0xffffffffu, e, o);
+          const F2 u = two_sum(s, s2);
+          s = u.hi;
+          e = (e + e2) + u.lo;
+        }
+        if (!BF16 || s < INFINITY || sc != 1.f) break;   // (all lanes have the same s)
+        sc = 0x1p-70f;
       }
-      F2 m = two_sum(s * (1.f / 512), ap.eps);
+      F2 m = two_sum(s * (1.f / 512), ap.eps * (sc * sc));
       m = renorm(m.hi, m.lo + e * (1.f / 512));
       if (m.hi < kLeastMean) m = {kLeastMean, 0.f};
       // 1 / sqrt(m): the fp32 estimate and one Newton step on its exact residual
-      const float r0 = rsqrtf(m.hi);
+      float r0 = rsqrtf(m.hi);
       const float r2 = r0 * r0, r2e = fmaf(r0, r0, -r2);
       const float res = fmaf(-m.hi, r2, 1.f) - (m.hi * r2e + m.lo * r2);
-      const float rl = 0.5f * r0 * res;
+      float rl = 0.5f * r0 * res;
+      if (s == INFINITY) r0 = rl = 0.f;   // a row with an infinity
+      const bool plain = s < INFINITY;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const float2 f = unpack<BF16>(cw[k]), w = unpack<BF16>(ww[k]);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float xw = h ? f.y * w.y : f.x * w.x;   // exact
+          const float xw = h ? f.y * sc * w.y : f.x * sc * w.x;   // exact
           const float p = xw * r0;
           const F2 v = renorm(p, fmaf(xw, r0, -p) + xw * rl);
-          y[2 * k + h] = xw == 0.f ? xw : to_odd(v.hi, v.lo);
+          y[2 * k + h] = xw == 0.f || !plain ? p : to_odd(v.hi, v.lo);
         }
       }
     } else {
@@ -297,6 +306,7 @@ __device__ __forceinline__ bool append_row(const AppendParams& ap, int t, int la
       s += e;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      same = s < INFINITY;
       const float mean = fmaf(s, 1.f / 512, ap.eps);
       by = rsqrtf(mean < kLeastMean ? kLeastMean : mean);
 #pragma unroll

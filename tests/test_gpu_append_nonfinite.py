@@ -73,3 +73,44 @@ def test_keys_with_infinities_and_nan(kind, interleaved, dt):
     k[7, :] = INF
     k[8, pair[1]] = INF
     check(c, c.run()[1])
+
+
+@KINDS
+@pytest.mark.parametrize("weight", [True, False])
+@pytest.mark.parametrize("dt", [BF, HF])
+def test_latents_with_infinities_and_nan(kind, weight, dt):
+    """With the norm an infinite latent makes its row zeros (signed) and itself NaN, a NaN
+    all of the row NaN; without it they go to the cache as they are."""
+    c = Case(7, 1, kind, dt, pad=False, weight=weight, seed=3)
+    lat = c.kv_a
+    lat[1, 17] = INF
+    lat[2, 511] = -INF
+    lat[3, 0] = NAN
+    lat[4, 5], lat[4, 100] = INF, NAN
+    lat[5, 3:40] = 0
+    lat[5, 7] = INF
+    lat[6, 9], lat[6, 10] = INF, -INF
+    check(c, c.run()[1])
+
+
+@KINDS
+@pytest.mark.parametrize("size", [1e15, 1e18, 3e19, 1e25, 1e36, 1e38])
+def test_rows_whose_squares_pass_fp32(kind, size):
+    """bf16 latents up to the type's end: normalised like any others."""
+    c = Case(20, 1, kind, BF, pad=False, seed=4)
+    g = torch.Generator(device=DEV).manual_seed(5)
+    x = torch.rand(20, 512, generator=g, device=DEV) * 2 - 1
+    c.kv_a[:, :512] = (x * size).to(BF)
+    c.kv_a[3, 1:] = 1.0                                     # one huge value among small ones
+    c.kv_a[4] = 0
+    check(c, c.run()[1])
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "e2m1"])
+@pytest.mark.parametrize("kv_scale", [2.0 ** -99, 2.0 ** -20, 2.0 ** 20, 2.0 ** 60, 2.0 ** 99])
+def test_scales_at_the_ends_of_their_range(kind, kv_scale):
+    """Rows and weights that such scales are for: values of some kv_scale."""
+    c = Case(40, 1, kind, BF, pad=False, seed=6, kv_scale=kv_scale)
+    c.weight = (c.weight.float() * min(kv_scale, 2.0 ** 60)).to(BF)
+    c.kv_a[20:, :512] = (c.kv_a[20:, :512].float() * 2.0 ** 62).to(BF)
+    check(c, c.run()[1])
