@@ -438,7 +438,8 @@ int mla_gather_kv(const void* kv_cache, const int32_t* block_table, const int32_
  *         its sign; a block that holds a NaN gets s = NaN
  * (exactly so where kv_scale is a power of two; q_out is computed in fp32).
  * mean(c^2) + eps counts as at least 2^-120 (a row of zeros stays zeros).  With the
- * norm, an infinity makes its row zeros and itself NaN, and a NaN all of the row NaN.
+ * norm, an infinity makes its row zeros and itself NaN, and a NaN all of the row NaN;
+ * c * w is within fp32.
  *
  *   c_kv      [T, 512] dtype, rows c_stride elements apart
  *   k_pe      [T, 64] dtype, rows k_stride elements apart

@@ -456,7 +456,8 @@ __device__ __forceinline__ bool append_row(const AppendParams& ap, int t, int la
       for (int k = 0; k < 4; ++k) w[k] = to_e4m3x4(q + 4 * k, 1.f);
     } else {
       const float rd = ap.inv_kv * by;
-      same &= rd < INFINITY || by != by;
+      // (a product below fp32's normal range keeps too few bits; a NaN goes that way too)
+      same &= rd < INFINITY && rd >= 0x1p-100f;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         w[k] = to_e4m3x4(y + 4 * k, rd * kLess);

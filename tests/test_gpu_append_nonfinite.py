@@ -114,3 +114,13 @@ def test_scales_at_the_ends_of_their_range(kind, kv_scale):
     c.weight = (c.weight.float() * min(kv_scale, 2.0 ** 60)).to(BF)
     c.kv_a[20:, :512] = (c.kv_a[20:, :512].float() * 2.0 ** 62).to(BF)
     check(c, c.run()[1])
+
+
+def test_scale_times_norm_below_the_normal_range():
+    """1 / kv_scale times the norm's factor below 2^-126: an E4M3 code taken by that
+    product would miss borders.  (c * w stays within fp32, |c| < 6 * 2^38, w < 4 * 2^85.)"""
+    c = Case(6000, 1, "e4m3", BF, pad=False, seed=7, kv_scale=2.0 ** 94, bs=64)
+    c.weight = (c.weight.float() * 2.0 ** 85).to(BF)
+    c.kv_a[:, :512] = (torch.randn(6000, 512, generator=torch.Generator(device=DEV).manual_seed(8), device=DEV)
+                       * 2.0 ** 38).clamp(-6 * 2.0 ** 38, 6 * 2.0 ** 38).to(BF)
+    check(c, c.run()[1])
