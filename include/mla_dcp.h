@@ -538,7 +538,9 @@ int mla_kv_fork(void* kv_cache, uint64_t layer_stride, uint64_t page_bytes, int 
  * mla_debug_set_spin_limit -- test hook for the device error path: the
  * number of polls after which a pipeline wait of mla_dcp_decode_partial (and
  * of mla_dcp_decode_partial_noalloc) gives up and records
- * MLA_DEV_WAIT_TIMEOUT; 0 restores the default of 2^22 polls.  It applies
+ * MLA_DEV_WAIT_TIMEOUT; 0 restores the default of 2^22 polls.  (The E4M3 call's
+ * waits too; the E2M1 call's end within a poll as a rule, so with a limit below 64
+ * it copies nothing in, and all of them run out.)  It applies
  * to every call launched after it, from any host thread.  With a limit short
  * enough to run out, that call's outputs are unspecified and *err_flag reads
  * MLA_DEV_WAIT_TIMEOUT; the kernel still waits for its own copies and MMAs

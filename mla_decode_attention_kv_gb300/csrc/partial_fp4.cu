@@ -78,6 +78,10 @@ constexpr int kRawCodes = kTile4 * kE2m1Codes;   // 18432
 constexpr int kRawStage = kTile4 * kE2m1Row;     // 20736
 constexpr int kChunk = kTile4 * 128;             // 8 KB: 64 columns of a tile
 constexpr int kUnits4 = 8;                       // units whose geometry is kept in shared memory
+// A poll limit (mla_debug_set_spin_limit) below this one is a test of the giving up: no
+// wait here lasts as long as one poll may suspend its thread, so the producer then
+// copies nothing, and every wait runs out.
+constexpr uint32_t kShortPolls = 64;
 
 struct Unit4 {
   int b, g, p, lo, hi;
@@ -674,6 +678,7 @@ __global__ void __launch_bounds__(Smem4<N>::kThreads, 1)
     // ------------------------------------------------ producer
     Iter4<N> it;
     it.start(fp, tab, rng);
+    if (fp.spin_limit < kShortPolls) it.valid = false;
     const int nbox = kTile4 / fp.box;
     int rs = 0, qloads = 0;
     // (the id of a lane's page is loaded one tile ahead)
