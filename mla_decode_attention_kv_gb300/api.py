@@ -133,10 +133,10 @@ def mla_dcp_decode_partial(q_abs, q_pe, kv_cache, block_table, seq_lens, num_sha
     with head_slices = N > 1 they are [N, B*q, P, H/N, 512] and
     [N, B*q, P, H/N] (mla_dcp_decode_partial_sliced: block n is what rank n
     receives in a head-scattered all-to-all).
-    workspace: "default" (one kept per device and stream, see
-    partial_workspace; over E2M1 pages a captured call gets its own), a uint8 CUDA tensor of at least
-    mla_dcp_decode_partial_workspace_size bytes, or None (pairs of CTAs then
-    take whole shards)."""
+    workspace: "default" (one of some 40 MB kept per device and stream, see
+    partial_workspace; over E2M1 pages a captured call gets its own), a uint8 CUDA
+    tensor of at least mla_dcp_decode_partial_workspace_size bytes (over E2M1 pages
+    mla_dcp_decode_partial_fp4_workspace_size), or None (CTAs then take whole shards)."""
     if is_fp4_cache(kv_cache):
         return _partial_fp4(q_abs, q_pe, kv_cache, block_table, seq_lens, num_shards, kv_cur, scale,
                             part_dtype, o_part, lse_part, err_flag, stream, workspace, head_slices,

@@ -24,10 +24,11 @@
 // which rounds on to fewer bits the same way as hi + lo itself.  16-bit rows
 // are always made the exact way.
 //
-// What bounds it: the launch for few tokens (one token 2.1 us, 32 tokens of 128
-// heads into E2M1 3.6, 1.3 of them where a row needs the exact form); for many the
-// row arithmetic (8192 tokens of 16 heads into E2M1: 13.0 us, of which the rows
-// alone 9.8; 57 MB at 4.4 TB/s, 0.65 of the measured copy bandwidth).  With half the
+// What bounds it: the launch for few tokens (one token 2.2 us, 32 tokens of 128
+// heads into E2M1 3.7, 1.3 of them where a row needs the exact form); for many the
+// row arithmetic (8192 tokens of 16 heads into E2M1: 12.9 us, of which the rows
+// alone 9.8; 57 MB at 4.4 TB/s, 0.65 of the measured copy bandwidth; with other inputs
+// each time 14.0, into E4M3 12.7, into 16 bits 15.7).  With half the
 // blocks on an SM the time is the same, with smaller register budgets 17 and 22 us.
 // One warp makes a token's row:
 // lane l owns latents 16 l .. 16 l + 15, which are one block of the E2M1 form,

@@ -24,7 +24,7 @@ enum CacheError : int {
 // written (tables, ids, lengths) is read by plain loads: __ldg asks for data that
 // nothing writes as long as the kernel lives, its time before the wait included.
 // Calls back to back, without it and so: 8 pages copied 4.1 and 2.8 us, 8192 tokens
-// appended 14.3 and 11.8, 64 rows forked 16.4 and 14.1.
+// appended 14.3 and 11.8, 64 rows forked 16.4 and 14.7.
 template <class... A, class... B>
 inline cudaError_t launch_overlapped(void (*kernel)(A...), dim3 grid, unsigned threads, cudaStream_t stream, B&&... args) {
   cudaLaunchConfig_t cfg = {};

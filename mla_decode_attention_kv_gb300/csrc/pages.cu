@@ -5,8 +5,8 @@
 // What bounds them: the copies move each byte once in and once out of HBM (1024
 // E2M1 pages of 64 tokens in 8 layers: 50.9 us, 6.7 TB/s, 0.98 of the measured copy
 // bandwidth); the bookkeeping is a few dependent reads, so for few pages the launch
-// and that chain count (8 pages copied 1.6 us; a fork of 4 rows 8.7 us, of 64 rows
-// with 4 layers' pages of 73 KB 13.7 us, in two launches).
+// and that chain count (8 pages copied 1.6 us; 4 rows given back and forked into again
+// 9.5 us, 64 rows with 4 layers' pages of 73 KB 14.5 us, in three launches).
 #include "cache_kernels.cuh"
 #include "common.cuh"
 

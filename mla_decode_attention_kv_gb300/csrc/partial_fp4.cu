@@ -22,9 +22,9 @@
 // where M = heads would cost the same for any number.  O^T [512 x rows] is 4
 // x rows columns of tensor memory, at most half of it, so one CTA holds all of
 // a unit, and several query tokens' rows share one pass over the history.
-// Measured (16 sequences of 131072 tokens): 16 heads 297 us, 2.29 TB/s of pages
+// Measured (16 sequences of 131072 tokens): 16 heads 299 us, 2.27 TB/s of pages
 // and 0.34 of the measured copy bandwidth (2700 cycles a tile of 64 tokens), 32
-// heads 312, 64 heads 401, 128 heads 765 us (two units of 64 rows; the products
+// heads 316, 64 heads 408, 128 heads 771 us (two units of 64 rows; the products
 // alone would take 305 us at the measured bf16 rate).  The 16-bit kernel takes 780
 // us for 128 heads.
 //

@@ -111,3 +111,27 @@ def test_graphs_of_one_pool_replayed_in_turn_with_eager_calls():
         eager = cs[(k + 1) % 3].run()
         assert all(torch.equal(a, b) for a, b in zip(outs[k], want[k]))
         assert all(torch.equal(a, b) for a, b in zip(eager, want[(k + 1) % 3]))
+
+
+def test_captured_calls_on_a_given_stream():
+    """stream= inside a capture, another one current: outputs from the graph's memory."""
+    c = Fp4([3000, 500], 16, shards=2, bs=64, cur=True, seed=3)
+    want_o, want_l = [t.clone() for t in c.run()]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        for _ in range(3):
+            o, lse = c.run(stream=side)
+        lat = api.mla_lse_combine(o, lse, stream=side)[0]
+        main.wait_stream(side)
+        copy = lat.clone()
+    for _ in range(3):
+        o.zero_()
+        copy.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, want_o) and torch.equal(lse, want_l) and c.err.item() == 0
+        assert torch.equal(copy, api.mla_lse_combine(want_o, want_l)[0])
